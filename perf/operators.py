@@ -181,7 +181,8 @@ def _run_plain(s):
 
 
 def _mx4_codes(x):
-    """fp32 [..., K] -> E2M1 codes [..., K/2] (even k in the low half byte), E8M0 scale codes [..., K/32].
+    """fp32 [..., M, K] -> E2M1 codes [..., M, K/2] (even k in the low half byte) and E8M0
+    scale codes, slice by slice of 256 k: [..., K/256, M, 8], zeros behind the last block.
 
     A block's scale is 2^(floor(log2 max|x|) - 2); x over the scale goes to the
     nearest of 0, .5, 1, 1.5, 2, 3, 4, 6, ties to the even code, at most 6."""
@@ -193,14 +194,21 @@ def _mx4_codes(x):
     a = y.abs()
     a = torch.where(a < 2, torch.round(2 * a), torch.where(a < 4, torch.round(a) + 2, torch.round(a / 2) + 4))
     code = (a.clamp(max=7) + 8 * torch.signbit(y)).to(torch.uint8).flatten(-2)
-    return code[..., 0::2] | code[..., 1::2] << 4, (e + 127).to(torch.uint8)
+    scale = torch.nn.functional.pad((e + 127).to(torch.uint8), (0, -e.shape[-1] % 8))
+    scale = scale.unflatten(-1, (-1, 8)).transpose(-3, -2).contiguous()
+    return code[..., 0::2] | code[..., 1::2] << 4, scale
+
+
+def _by_row(scale, blocks):
+    """Scale codes [..., K/256, M, 8] -> [..., M, K/32]."""
+    return scale.transpose(-3, -2).flatten(-2)[..., :blocks]
 
 
 def _mx4_values(q, scale):
     """The fp32 values that codes and scales stand for."""
     grid = torch.tensor(E2M1 + tuple(-v for v in E2M1), device=q.device)
-    v = torch.stack([grid[(q & 15).int()], grid[(q >> 4).int()]], dim=-1).flatten(-2)
-    return (v.unflatten(-1, (-1, 32)) * torch.exp2(scale.float() - 127)[..., None]).flatten(-2)
+    v = torch.stack([grid[(q & 15).int()], grid[(q >> 4).int()]], dim=-1).flatten(-2).unflatten(-1, (-1, 32))
+    return (v * torch.exp2(_by_row(scale, v.shape[-2]).float() - 127)[..., None]).flatten(-2)
 
 
 def work(case):
@@ -268,7 +276,8 @@ def _exact_values(q, scale):
     sign, low = 1 - 2 * torch.floor(c / 8), torch.remainder(c, 8)
     ex, man = torch.floor(low / 2), torch.remainder(low, 2)
     v = torch.where(ex == 0, man / 2, (1 + man / 2) * torch.exp2(ex - 1))
-    return sign * v * torch.exp2(scale.double() - 127).repeat_interleave(32, dim=-1)
+    blocks = torch.stack([scale[b // 8, :, b % 8] for b in range(c.shape[-1] // 32)], dim=-1)
+    return sign * v * torch.exp2(blocks.double() - 127).repeat_interleave(32, dim=-1)
 
 
 def _exact_rounding(x):
