@@ -54,6 +54,9 @@ HBM_PEAK_GBS = 8000.0
 MFMA_BF16_PEAK_TFLOPS = 2500.0
 MFMA_FP8_PEAK_TFLOPS = 5000.0
 KERNEL_NAME = "grouped_gemm_kernel"
+# what that kernel is built from; csrc/ holds the other operators' kernels too
+KERNEL_SOURCES = ("gg_common.h", "gg_mainloop.h", "gg_mainloop_q8.h", "gg_schedule.h",
+                  "grouped_gemm.hip")
 
 DESCRIPTIONS = {
     "tiny": "tiny ragged grouped GEMM: E=4, K=256, N=256, m=[3,0,17,9]",
@@ -66,14 +69,14 @@ DESCRIPTIONS = {
 
 
 def kernel_source_hash():
-    """Hash of the kernel sources with comments and blank space taken out, so
+    """Hash of the sources of grouped_gemm_kernel with comments and blank space taken out, so
     that a change to a comment does not mark the measured counters stale. The
     blocks only the tracing build compiles (#ifdef GG_TILE_TRACE) are taken
     out too: the product library is built without them."""
     import re
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "moe_ragged_grouped_amd", "csrc")
-    for fn in sorted(os.listdir(csrc)):
+    for fn in KERNEL_SOURCES:
         with open(os.path.join(csrc, fn), encoding="utf-8") as f:
             text = f.read()
         text = re.sub(r"#ifdef GG_TILE_TRACE\b.*?#endif", " ", text, flags=re.S)

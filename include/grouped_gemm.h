@@ -55,6 +55,8 @@ typedef enum {
 /* Largest K and N gg_grouped_gemm_bf16 accepts. */
 #define GG_MAX_K (1 << 22)
 #define GG_MAX_N (1 << 24)
+/* Largest N of the data gradients, which sum over it. */
+#define GG_MAX_DGRAD_N (1 << 21)
 
 /*
  * gg_grouped_gemm_bf16 -- the grouped product (worklog section 2; glossary
@@ -278,6 +280,187 @@ gg_status_t gg_grouped_gemm_fp8_swiglu(const void *Aq, const float *a_scale, con
                                        const float *b_scale, const int32_t *group_offsets,
                                        void *H, int32_t E, int32_t K, int32_t N, int32_t M_cap,
                                        int32_t bm, void *stream);
+
+/*
+ * gg_grouped_gemm_bf16_dgrad -- the data gradient of the grouped product: with
+ * dC the gradient of C = gg_grouped_gemm_bf16(A, B),
+ *
+ *   dA[r][k] = sum_n dC[r][n] * B[e][k][n]          for the rows r of expert e
+ *
+ *   dC  bf16 [M_cap][N], row-major, 16-byte aligned, rows grouped by expert as
+ *       A's in the product. Rows at or beyond off[E] are never read.
+ *   B   bf16 [E][K][N], the weights exactly as the product takes them (nothing
+ *       is transposed beforehand). The slice of an expert with no rows is
+ *       never read.
+ *   dA  fp32 [M_cap][K], 16-byte aligned. Rows [0, off[E]) are overwritten;
+ *       rows past them are not touched.
+ * group_offsets, E, M_cap, bm, the stream, the status codes and the conditions
+ * for them are those of gg_grouped_gemm_bf16 (arrays of no rows, M_cap = 0, may
+ * be NULL here and below); K and N are multiples of 8, N <= GG_MAX_DGRAD_N
+ * and K <= GG_MAX_N (the sum runs over N here).
+ * Accumulation is fp32 in the matrix cores, as accurate as the product's with
+ * N in the place of K.
+ */
+gg_status_t gg_grouped_gemm_bf16_dgrad(const void *dC, const void *B,
+                                       const int32_t *group_offsets, float *dA, int32_t E,
+                                       int32_t K, int32_t N, int32_t M_cap, int32_t bm,
+                                       void *stream);
+
+/*
+ * gg_grouped_gemm_bf16_dgrad_bf16out -- the same with dA bf16 [M_cap][K], each
+ * element the fp32 result rounded once to the nearest bf16 (ties to even).
+ */
+gg_status_t gg_grouped_gemm_bf16_dgrad_bf16out(const void *dC, const void *B,
+                                               const int32_t *group_offsets, void *dA, int32_t E,
+                                               int32_t K, int32_t N, int32_t M_cap, int32_t bm,
+                                               void *stream);
+
+/*
+ * gg_grouped_gemm_bf16_dgrad_swiglu -- the data gradient of the down projection
+ * taken through the SwiGLU before it, in one launch. An expert's layer is
+ *   C = X B1 (gate in column 2j, up in column 2j+1),  H = silu(gate) * up,
+ *   Y = H B2;
+ * given dY, this entry point computes dH = dY B2^T (in fp32, never stored) and
+ *   dC[r][2j]   = dH[r][j] * up * s * (1 + gate * (1 - s)),  s = 1 / (1 + e^-gate)
+ *   dC[r][2j+1] = dH[r][j] * gate * s
+ *   H[r][j]     = gate * s * up                    (where H is not NULL)
+ *
+ *   dY  bf16 [M_cap][N];  B  bf16 [E][K][N], the down projection (K = the width
+ *       of H);  C  bf16 [M_cap][2K], the gate and up columns interleaved, as
+ *       gg_grouped_gemm_bf16_bf16out gives them;
+ *   dC  bf16 [M_cap][2K], and H bf16 [M_cap][K] or NULL: the operand of the down
+ *       projection's weight gradient, which a forward pass that kept only C has
+ *       not stored. dC may be C itself. Rows at or beyond off[E] of C are not
+ *       read, of dC and H not written. All are 16-byte aligned.
+ * Everything is evaluated in fp32 (hardware exp2 and reciprocal, each within one
+ * ulp) and rounded once to bf16 on its way out. s is 0 where e^-gate overflows
+ * (gate below about -88.7), where dC and H then are 0 within 3e-37 relative to
+ * |dH * up| and |up|; an infinite gate gives NaN. Sizes, offsets, bm, the
+ * stream and the status codes are those of gg_grouped_gemm_bf16_dgrad.
+ */
+gg_status_t gg_grouped_gemm_bf16_dgrad_swiglu(const void *dY, const void *B,
+                                              const int32_t *group_offsets, const void *C, void *dC,
+                                              void *H, int32_t E, int32_t K, int32_t N,
+                                              int32_t M_cap, int32_t bm, void *stream);
+
+/*
+ * gg_grouped_gemm_bf16_wgrad -- the weight gradient of the grouped product:
+ *
+ *   dB[e][k][n] = sum over the rows r of expert e of A[r][k] * dC[r][n]
+ *
+ *   A   bf16 [M_cap][K] and dC bf16 [M_cap][N], row-major, 16-byte aligned, rows
+ *       grouped by expert. Rows at or beyond off[E] are never read. Both may be
+ *       NULL where M_cap is 0.
+ *   dB  fp32 [E][K][N], 16-byte aligned. Every element is written: an expert
+ *       with no rows gets zeros. With accumulate != 0 the sums are added to what
+ *       dB holds (each element by one fp32 addition), and experts with no rows
+ *       are left as they are.
+ *   group_offsets  int32 [E+1] on the device. Malformed offsets never make the
+ *       kernel read or write outside its arrays (they are clamped as in
+ *       gg_grouped_gemm_bf16).
+ *   K and N are multiples of 8, at most GG_MAX_K; E in [1, GG_MAX_EXPERTS];
+ *   M_cap in [0, 2^31 - 257].
+ * The sum over an expert's rows is taken in fp32 in the matrix cores, in the
+ * order of the rows: no atomics, so equal inputs give equal bits.
+ */
+gg_status_t gg_grouped_gemm_bf16_wgrad(const void *A, const void *dC,
+                                       const int32_t *group_offsets, float *dB,
+                                       int32_t accumulate, int32_t E, int32_t K, int32_t N,
+                                       int32_t M_cap, void *stream);
+
+/*
+ * gg_grouped_gemm_bf16_wgrad_bf16out -- the same with dB bf16 [E][K][N], each
+ * element the fp32 sum rounded once to the nearest bf16 (ties to even). There
+ * is no accumulating form: sums held in bf16 would lose what is added to them.
+ */
+gg_status_t gg_grouped_gemm_bf16_wgrad_bf16out(const void *A, const void *dC,
+                                               const int32_t *group_offsets, void *dB, int32_t E,
+                                               int32_t K, int32_t N, int32_t M_cap, void *stream);
+
+/*
+ * 4-bit microscaled operands ("mx4", the OCP Microscaling format MXFP4). Blocks
+ * of 32 values along K share a scale 2^(s - 127), s a byte (E8M0; 255 is NaN).
+ * A value is a 4-bit E2M1 code: bit 3 the sign, codes 0..7 the magnitudes
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   codes   uint8 [rows][K/2]: byte j of a row holds k = 2j in its low half and
+ *           k = 2j + 1 in its high half.
+ *   scales  uint8 [ceil(K/256)][rows][8]: the block of k = 32 b .. 32 b + 31 of
+ *           row r has its scale at [b / 8][r][b % 8]. (A tile's scales of one
+ *           slice of 256 k are then one run of memory.) Bytes past the last
+ *           block are ignored by every entry point and written as 0.
+ * Weights are kept per expert with the output columns as rows: codes
+ * [E][N][K/2], scales [E][ceil(K/256)][N][8]. K is a multiple of 32.
+ *
+ * gg_mx4_quantize -- X bf16 [rows][K] to codes and scales. A block's scale is
+ * 2^(floor(log2 max|x|) - 2), at least 2^-127; x over the scale goes to the
+ * nearest value, ties to the even code, and magnitudes over 6 become 6 (the
+ * format's own rule: the largest values of a block may be up to 8 scales). A
+ * block of zeros gets scale byte 0. A block that holds an infinity or a NaN
+ * gets scale byte 255 and codes 0, and so stands for NaN throughout.
+ * X, q and scales are 16-byte aligned; rows in [0, 2^31 - 1], K <= GG_MAX_K.
+ */
+gg_status_t gg_mx4_quantize(const void *X, void *q, void *scales, int64_t rows, int32_t K,
+                            void *stream);
+
+/*
+ * gg_mx4_quantize_weights -- B bf16 [E][K][N] (the layout of the bf16 product)
+ * to codes [E][N][K/2] and scales [E][ceil(K/256)][N][8], blocks along K, by the
+ * rule of gg_mx4_quantize. N is a multiple of 8, at most GG_MAX_MX4_WEIGHT_N.
+ */
+#define GG_MAX_MX4_WEIGHT_N (65535 * 256)
+gg_status_t gg_mx4_quantize_weights(const void *B, void *q, void *scales, int32_t E, int32_t K,
+                                    int32_t N, void *stream);
+
+/*
+ * gg_mx4_dequantize -- the values that codes and scales stand for:
+ * Y bf16 [batch][rows][K] from codes [batch][rows][K/2] and scales
+ * [batch][ceil(K/256)][rows][8] (batch = E and rows = N for weights, batch = 1
+ * for activations). Every such value is a bf16 value except 4 and 6 times
+ * 2^127 (scale byte 254), which become infinite; scale byte 255 gives NaN.
+ * batch in [0, 65535]; rows in [0, 2^31 - 1].
+ */
+gg_status_t gg_mx4_dequantize(const void *q, const void *scales, void *Y, int32_t batch,
+                              int64_t rows, int32_t K, void *stream);
+
+/*
+ * gg_grouped_gemm_mx4 -- the grouped product of 4-bit microscaled activations
+ * and weights on the matrix cores' own 4-bit format:
+ *
+ *   C[r][n] = sum_k val(Aq, a_scale)[r][k] * val(Bq, b_scale)[e][n][k]
+ *
+ *   Aq, a_scale  codes uint8 [M_cap][K/2] and scales uint8 [ceil(K/256)][M_cap][8].
+ *                Codes of rows at or beyond off[E] are never used.
+ *   Bq, b_scale  codes uint8 [E][N][K/2] and scales uint8 [E][ceil(K/256)][N][8].
+ *   C            fp32 [M_cap][N]. Rows at or beyond off[E] are not touched.
+ * K is a multiple of 32 and at most GG_MAX_K, N a multiple of 8 and at most
+ * GG_MAX_N; all pointers but group_offsets (4) are 16-byte aligned. Offsets, E,
+ * M_cap, bm, the stream and the status codes are those of gg_grouped_gemm_bf16.
+ * Products of two values are exact and accumulate in fp32; a NaN scale makes the
+ * row's or the column's results NaN.
+ */
+gg_status_t gg_grouped_gemm_mx4(const void *Aq, const void *a_scale, const void *Bq,
+                                const void *b_scale, const int32_t *group_offsets, float *C,
+                                int32_t E, int32_t K, int32_t N, int32_t M_cap, int32_t bm,
+                                void *stream);
+
+/*
+ * gg_grouped_gemm_mx4_bf16out -- the same with C bf16 [M_cap][N], each element
+ * the fp32 result rounded once to the nearest bf16 (ties to even).
+ */
+gg_status_t gg_grouped_gemm_mx4_bf16out(const void *Aq, const void *a_scale, const void *Bq,
+                                        const void *b_scale, const int32_t *group_offsets, void *C,
+                                        int32_t E, int32_t K, int32_t N, int32_t M_cap, int32_t bm,
+                                        void *stream);
+
+/*
+ * gg_grouped_gemm_mx4_swiglu -- gg_grouped_gemm_mx4 for the gate and up
+ * projections, N = 2 I interleaved columns, with the SwiGLU of
+ * gg_grouped_gemm_bf16_swiglu in the epilogue: H bf16 [M_cap][N/2].
+ */
+gg_status_t gg_grouped_gemm_mx4_swiglu(const void *Aq, const void *a_scale, const void *Bq,
+                                       const void *b_scale, const int32_t *group_offsets, void *H,
+                                       int32_t E, int32_t K, int32_t N, int32_t M_cap, int32_t bm,
+                                       void *stream);
 
 /*
  * gg_tile_schedule -- the flat tile list the product kernel consumes,

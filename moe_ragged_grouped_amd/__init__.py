@@ -16,7 +16,9 @@ import os
 
 __all__ = ["grouped_gemm", "grouped_gemm_swiglu", "grouped_gemm_gather",
            "grouped_gemm_gather_combine", "grouped_gemm_fp8w", "grouped_gemm_fp8",
-           "grouped_gemm_fp8_swiglu", "tile_schedule", "library_path", "load_library",
+           "grouped_gemm_fp8_swiglu", "grouped_gemm_dgrad", "grouped_gemm_dgrad_swiglu",
+           "grouped_gemm_wgrad", "mx4_quantize", "mx4_quantize_weights", "mx4_dequantize",
+           "grouped_gemm_mx4", "grouped_gemm_mx4_swiglu", "tile_schedule", "library_path", "load_library",
            "traced_grouped_gemm", "trace_library_path", "load_trace_library",
            "GroupedGemmError", "BM_CHOICES", "TILE_N", "MAX_EXPERTS", "SYMBOLS",
            "TRACE_SYMBOLS", "TRACE_WORKGROUPS", "TRACE_RECORD"]
@@ -31,7 +33,12 @@ MAX_EXPERTS = 1024
 SYMBOLS = ("gg_grouped_gemm_bf16", "gg_grouped_gemm_bf16_bf16out", "gg_grouped_gemm_bf16_swiglu",
            "gg_grouped_gemm_bf16_gather", "gg_grouped_gemm_bf16_gather_combine",
            "gg_grouped_gemm_fp8w", "gg_grouped_gemm_fp8", "gg_grouped_gemm_fp8_bf16out",
-           "gg_grouped_gemm_fp8_swiglu", "gg_tile_schedule", "gg_status_string")
+           "gg_grouped_gemm_fp8_swiglu", "gg_grouped_gemm_bf16_dgrad",
+           "gg_grouped_gemm_bf16_dgrad_bf16out", "gg_grouped_gemm_bf16_dgrad_swiglu",
+           "gg_grouped_gemm_bf16_wgrad", "gg_grouped_gemm_bf16_wgrad_bf16out", "gg_mx4_quantize",
+           "gg_mx4_quantize_weights", "gg_mx4_dequantize", "gg_grouped_gemm_mx4",
+           "gg_grouped_gemm_mx4_bf16out", "gg_grouped_gemm_mx4_swiglu", "gg_tile_schedule",
+           "gg_status_string")
 
 # the tracing build (include/grouped_gemm_trace.h): a diagnostic library
 _TRACE_LIB_PATH = os.path.join(_HERE, "libmoe_ragged_grouped_amd_trace.so")
@@ -82,6 +89,22 @@ def load_library():
         lib.gg_grouped_gemm_fp8_swiglu.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                                    i32, vp]
         lib.gg_grouped_gemm_fp8_swiglu.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        for name, args in (
+                ("gg_grouped_gemm_bf16_dgrad", [vp] * 4 + [i32] * 5),
+                ("gg_grouped_gemm_bf16_dgrad_bf16out", [vp] * 4 + [i32] * 5),
+                ("gg_grouped_gemm_bf16_dgrad_swiglu", [vp] * 6 + [i32] * 5),
+                ("gg_grouped_gemm_bf16_wgrad", [vp] * 4 + [i32] * 5),
+                ("gg_grouped_gemm_bf16_wgrad_bf16out", [vp] * 4 + [i32] * 4),
+                ("gg_mx4_quantize", [vp] * 3 + [i64, i32]),
+                ("gg_mx4_quantize_weights", [vp] * 3 + [i32] * 3),
+                ("gg_mx4_dequantize", [vp] * 3 + [i32, i64, i32]),
+                ("gg_grouped_gemm_mx4", [vp] * 6 + [i32] * 5),
+                ("gg_grouped_gemm_mx4_bf16out", [vp] * 6 + [i32] * 5),
+                ("gg_grouped_gemm_mx4_swiglu", [vp] * 6 + [i32] * 5)):
+            fn = getattr(lib, name)
+            fn.argtypes = args + [vp]
+            fn.restype = ctypes.c_int
         lib.gg_tile_schedule.argtypes = [vp, i32, i32, i32, i32, vp, vp, i32, vp]
         lib.gg_tile_schedule.restype = ctypes.c_int
         lib.gg_status_string.argtypes = [ctypes.c_int]
@@ -370,6 +393,264 @@ def grouped_gemm_fp8_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
                                         b_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(),
                                         E, K, N, M_cap, int(bm), _stream_handle(Aq.device, stream))
     _check(st, "gg_grouped_gemm_fp8_swiglu")
+    return out
+
+
+# ---- gradients and 4-bit operators
+
+def _device_args(what, **tensors):
+    """Checks that every tensor (name=(tensor, dtypes, dims)) is contiguous, of
+    one of its dtypes and of its rank, and that all are on one device; returns
+    that device."""
+    dev = None
+    for name, (t, dtypes, dims) in tensors.items():
+        if t.dtype not in dtypes:
+            raise TypeError("%s: %s must be %s" % (what, name, " or ".join(str(d) for d in dtypes)))
+        if t.dim() != dims:
+            raise ValueError("%s: %s must have %d dimensions, not %d" % (what, name, dims, t.dim()))
+    for name, (t, _, _) in tensors.items():
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("%s: %s must be a contiguous device tensor" % (what, name))
+        if dev is not None and t.device != dev:
+            raise ValueError("%s: tensors are on %s and %s" % (what, dev, t.device))
+        dev = t.device
+    return dev
+
+
+def _match(what, ok, *tensors):
+    if not ok:
+        raise ValueError("%s: shape mismatch: %s" % (what, ", ".join(str(tuple(t.shape)) for t in tensors)))
+
+
+def _out(what, out, shape, dtypes, dtype, dev, stream):
+    """The given output, checked, or a new one of ``dtype`` (default: the first
+    of ``dtypes``) whose memory belongs to the stream that writes it."""
+    import torch
+    if dtype is not None and dtype not in dtypes:
+        raise TypeError("%s: out_dtype must be %s" % (what, " or ".join(str(d) for d in dtypes)))
+    if out is None:
+        dtype = dtypes[0] if dtype is None else dtype
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=dev)
+    if (out.dtype not in dtypes or (dtype is not None and out.dtype != dtype)
+            or tuple(out.shape) != tuple(shape) or not out.is_contiguous() or out.device != dev):
+        raise ValueError("%s: out must be a contiguous %s %s tensor on %s" % (
+            what, " or ".join(str(d) for d in ([dtype] if dtype else dtypes)), list(shape), dev))
+    return out
+
+
+def _call(name, dev, stream, *args):
+    """Calls one entry point on the tensors' device, whichever is current."""
+    import torch
+    fn = getattr(load_library(), name)
+    if stream is not None and stream.device != dev:
+        raise ValueError("%s: the stream is on %s, the tensors on %s" % (name, stream.device, dev))
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, _stream_handle(dev, stream)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream_handle(dev, stream)), name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_dtype=None):
+    """dA[off[e]:off[e+1]] = dC[off[e]:off[e+1]] @ B[e].T for every expert e, in one launch.
+
+    The gradient of grouped_gemm(A, B, offsets) with respect to A. dC: bf16
+    [M_cap, N]; B: bf16 [E, K, N], as the product takes it; out: optional fp32
+    or bf16 [M_cap, K] (out_dtype, default fp32, when out is not given; bf16 is
+    the fp32 sum rounded to nearest even). offsets, bm and stream as in
+    grouped_gemm. Rows at or past offsets[E] are left as they were.
+    """
+    import torch
+    what = "grouped_gemm_dgrad"
+    dev = _device_args(what, dC=(dC, (torch.bfloat16,), 2), B=(B, (torch.bfloat16,), 3),
+                       offsets=(offsets, (torch.int32,), 1))
+    E, K, N = B.shape
+    M_cap = dC.shape[0]
+    _match(what, dC.shape[1] == N and offsets.shape[0] == E + 1, dC, B, offsets)
+    out = _out(what, out, (M_cap, K), (torch.float32, torch.bfloat16), out_dtype, dev, stream)
+    name = "gg_grouped_gemm_bf16_dgrad" + ("" if out.dtype == torch.float32 else "_bf16out")
+    _call(name, dev, stream, dC.data_ptr(), B.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K,
+          N, M_cap, int(bm))
+    return out
+
+
+def grouped_gemm_dgrad_swiglu(dY, B, offsets, C, out=None, out_h=None, with_h: bool = False,
+                              bm: int = 0, stream=None):
+    """The gradient of H = silu(gate) * up, Y = grouped_gemm(H, B, offsets), in one launch.
+
+    dY: bf16 [M_cap, N]; B: bf16 [E, K, N], the down projection; C: bf16
+    [M_cap, 2K], gate in column 2j and up in column 2j+1 (grouped_gemm with bf16
+    output on interleaved weights). Returns dC, bf16 [M_cap, 2K], the gradient
+    of C (``out``, which may be C itself); with with_h or out_h also H, bf16
+    [M_cap, K], which the down projection's weight gradient needs. The gradient
+    of H stays in fp32 registers; everything is rounded once. Rows at or past
+    offsets[E] are left as they were. offsets, bm, stream as in grouped_gemm.
+    """
+    import torch
+    what = "grouped_gemm_dgrad_swiglu"
+    bf = (torch.bfloat16,)
+    dev = _device_args(what, dY=(dY, bf, 2), B=(B, bf, 3), offsets=(offsets, (torch.int32,), 1),
+                       C=(C, bf, 2))
+    E, K, N = B.shape
+    M_cap = dY.shape[0]
+    _match(what, dY.shape[1] == N and offsets.shape[0] == E + 1
+           and tuple(C.shape) == (M_cap, 2 * K), dY, B, offsets, C)
+    out = _out(what, out, (M_cap, 2 * K), bf, None, dev, stream)
+    h = None
+    if with_h or out_h is not None:
+        h = _out(what, out_h, (M_cap, K), bf, None, dev, stream)
+    _call("gg_grouped_gemm_bf16_dgrad_swiglu", dev, stream, dY.data_ptr(), B.data_ptr(),
+          offsets.data_ptr(), C.data_ptr(), out.data_ptr(), _ptr(h), E, K, N, M_cap, int(bm))
+    return out if h is None else (out, h)
+
+
+def grouped_gemm_wgrad(A, dC, offsets, out=None, accumulate: bool = False, stream=None,
+                       out_dtype=None):
+    """dB[e] = A[off[e]:off[e+1]].T @ dC[off[e]:off[e+1]] for every expert e, in one launch.
+
+    The gradient of grouped_gemm(A, B, offsets) with respect to B. A: bf16
+    [M_cap, K]; dC: bf16 [M_cap, N]; offsets: int32 [E+1]; out: optional fp32 or
+    bf16 [E, K, N] (out_dtype, default fp32, when out is not given; bf16 is the
+    fp32 sum rounded to nearest even). An expert with no rows gets zeros. With
+    accumulate the sums are added to ``out``, which must then be given and fp32.
+    The sums take no atomics: equal inputs give equal bits.
+    """
+    import torch
+    what = "grouped_gemm_wgrad"
+    dev = _device_args(what, A=(A, (torch.bfloat16,), 2), dC=(dC, (torch.bfloat16,), 2),
+                       offsets=(offsets, (torch.int32,), 1))
+    M_cap, K = A.shape
+    N = dC.shape[1]
+    E = offsets.shape[0] - 1
+    _match(what, dC.shape[0] == M_cap and E >= 1, A, dC, offsets)
+    if accumulate and (out is None or out.dtype != torch.float32):
+        raise ValueError("%s: accumulate needs an fp32 out to add to" % what)
+    out = _out(what, out, (E, K, N), (torch.float32, torch.bfloat16), out_dtype, dev, stream)
+    args = (A.data_ptr(), dC.data_ptr(), offsets.data_ptr(), out.data_ptr())
+    if out.dtype == torch.float32:
+        _call("gg_grouped_gemm_bf16_wgrad", dev, stream, *args, int(accumulate), E, K, N, M_cap)
+    else:
+        _call("gg_grouped_gemm_bf16_wgrad_bf16out", dev, stream, *args, E, K, N, M_cap)
+    return out
+
+
+def _mx4_slices(K: int) -> int:
+    """Slices of 256 k: the first dimension of a scale tensor."""
+    return -(-K // 256)
+
+
+def mx4_quantize(X, out=None, out_scale=None, stream=None):
+    """bf16 rows [M, K] -> 4-bit microscaled (codes uint8 [M, K/2], scales uint8 [ceil(K/256), M, 8]).
+
+    Blocks of 32 values along K share the scale 2^(floor(log2 max|x|) - 2); a
+    value goes to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 times it, ties to the
+    even code, at most 6. A block with an infinity or a NaN stands for NaN. K is
+    a multiple of 32. Byte j of a row of codes holds k = 2j (low half) and
+    2j + 1; block b of row r has its scale byte at scales[b // 8, r, b % 8].
+    """
+    import torch
+    what = "mx4_quantize"
+    dev = _device_args(what, X=(X, (torch.bfloat16,), 2))
+    M, K = X.shape
+    u8 = (torch.uint8,)
+    q = _out(what, out, (M, K // 2), u8, None, dev, stream)
+    s = _out(what, out_scale, (_mx4_slices(K), M, 8), u8, None, dev, stream)
+    _call("gg_mx4_quantize", dev, stream, X.data_ptr(), q.data_ptr(), s.data_ptr(), M, K)
+    return q, s
+
+
+def mx4_quantize_weights(B, out=None, out_scale=None, stream=None):
+    """bf16 weights [E, K, N] -> (codes uint8 [E, N, K/2], scales uint8 [E, ceil(K/256), N, 8]).
+
+    The rule of mx4_quantize, blocks along K: what grouped_gemm_mx4 takes as
+    weights, made once when the weights are loaded.
+    """
+    import torch
+    what = "mx4_quantize_weights"
+    dev = _device_args(what, B=(B, (torch.bfloat16,), 3))
+    E, K, N = B.shape
+    u8 = (torch.uint8,)
+    q = _out(what, out, (E, N, K // 2), u8, None, dev, stream)
+    s = _out(what, out_scale, (E, _mx4_slices(K), N, 8), u8, None, dev, stream)
+    _call("gg_mx4_quantize_weights", dev, stream, B.data_ptr(), q.data_ptr(), s.data_ptr(), E, K, N)
+    return q, s
+
+
+def mx4_dequantize(q, scales, out=None, stream=None):
+    """The bf16 values that 4-bit codes and scales stand for.
+
+    q: uint8 [M, K/2] with scales [ceil(K/256), M, 8], or weights [E, N, K/2]
+    with [E, ceil(K/256), N, 8]; returns bf16 [M, K] or [E, N, K].
+    """
+    import torch
+    what = "mx4_dequantize"
+    u8 = (torch.uint8,)
+    if q.dim() not in (2, 3):
+        raise ValueError("%s: codes are [M, K/2] or [E, N, K/2]" % what)
+    dev = _device_args(what, q=(q, u8, q.dim()), scales=(scales, u8, q.dim() + 1))
+    batch = q.shape[0] if q.dim() == 3 else 1
+    rows, K = q.shape[-2], 2 * q.shape[-1]
+    lead = (batch,) if q.dim() == 3 else ()
+    _match(what, tuple(scales.shape) == lead + (_mx4_slices(K), rows, 8), q, scales)
+    y = _out(what, out, lead + (rows, K), (torch.bfloat16,), None, dev, stream)
+    _call("gg_mx4_dequantize", dev, stream, q.data_ptr(), scales.data_ptr(), y.data_ptr(), batch,
+          rows, K)
+    return y
+
+
+def _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets):
+    import torch
+    u8 = (torch.uint8,)
+    dev = _device_args(what, Aq=(Aq, u8, 2), a_scale=(a_scale, u8, 3), Bq=(Bq, u8, 3),
+                       b_scale=(b_scale, u8, 4), offsets=(offsets, (torch.int32,), 1))
+    E, N, half = Bq.shape
+    M_cap, K = Aq.shape[0], 2 * half
+    _match(what, Aq.shape[1] == half and offsets.shape[0] == E + 1
+           and tuple(a_scale.shape) == (_mx4_slices(K), M_cap, 8)
+           and tuple(b_scale.shape) == (E, _mx4_slices(K), N, 8), Aq, a_scale, Bq, b_scale, offsets)
+    return dev, E, K, N, M_cap
+
+
+def grouped_gemm_mx4(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, stream=None,
+                     out_dtype=None):
+    """C = val(Aq, a_scale) @ val(Bq[e], b_scale[e]).T per expert, 4-bit matrix cores, one launch.
+
+    Aq, a_scale: codes and scales of the rows (mx4_quantize); Bq, b_scale: of the
+    weights (mx4_quantize_weights); offsets int32 [E+1]; out: optional fp32 or
+    bf16 [M_cap, N] (out_dtype when out is not given, default fp32; bf16 is the
+    fp32 result rounded to nearest even). N must be a multiple of 8. Rows at or
+    past offsets[E] are left as they were. bm and stream as in grouped_gemm.
+    """
+    import torch
+    what = "grouped_gemm_mx4"
+    dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets)
+    out = _out(what, out, (M_cap, N), (torch.float32, torch.bfloat16), out_dtype, dev, stream)
+    name = "gg_grouped_gemm_mx4" + ("" if out.dtype == torch.float32 else "_bf16out")
+    _call(name, dev, stream, Aq.data_ptr(), a_scale.data_ptr(), Bq.data_ptr(), b_scale.data_ptr(),
+          offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap, int(bm))
+    return out
+
+
+def grouped_gemm_mx4_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, stream=None):
+    """H[r, j] = silu(C[r, 2j]) * C[r, 2j+1] for C = grouped_gemm_mx4 (interleaved columns).
+
+    Arguments of grouped_gemm_mx4; out: optional bf16 [M_cap, N // 2]. The
+    activation runs in fp32 in the epilogue and is rounded once to bf16.
+    """
+    import torch
+    what = "grouped_gemm_mx4_swiglu"
+    dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets)
+    out = _out(what, out, (M_cap, N // 2), (torch.bfloat16,), None, dev, stream)
+    _call("gg_grouped_gemm_mx4_swiglu", dev, stream, Aq.data_ptr(), a_scale.data_ptr(),
+          Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap,
+          int(bm))
     return out
 
 

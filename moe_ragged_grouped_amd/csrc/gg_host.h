@@ -1,0 +1,68 @@
+// Host-side pieces the gradient and 4-bit entry points share: argument
+// checks, and the launch limits of a persistent kernel per device.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "gg_schedule.h"
+#include "grouped_gemm.h"
+
+namespace gg {
+
+constexpr int kRingXcds = 8;
+constexpr int kHostMaxDevices = 64;
+
+inline bool is_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+inline bool valid_bm(int bm) {
+  return bm == 0 || bm == 16 || bm == 32 || bm == 64 || bm == 128 || bm == 256;
+}
+
+// Groups, rows and tile height; the upper bound of the tile count of a
+// product with `cols` output columns (narrowest tiles: `narrow` columns).
+inline gg_status_t check_groups(const int32_t *off, int E, int cols, int M_cap, int bm, int narrow,
+                                long long *bound) {
+  if (off == nullptr || E < 1 || cols < 1 || M_cap < 0 || !valid_bm(bm)) return GG_ERR_INVALID_VALUE;
+  if (E > kMaxExperts) return GG_ERR_UNSUPPORTED;
+  if (!is_aligned(off, 4)) return GG_ERR_MISALIGNED;
+  const long long hmin = bm ? bm : 16;
+  const long long b = ((long long)M_cap / hmin + E) * ((cols + (long long)narrow - 1) / narrow);
+  // tile ids and rows + tile height must stay inside int32
+  if (b > (1LL << 28) || (long long)M_cap + 256 > INT32_MAX) return GG_ERR_UNSUPPORTED;
+  *bound = b;
+  return GG_OK;
+}
+
+// One workgroup per CU of the current device. The kernel's dynamic LDS limit
+// is raised once per device and kernel.
+struct RingLaunch {
+  int grid = 0;
+  hipError_t err = hipSuccess;
+};
+
+template <auto Kernel>
+inline RingLaunch ring_launch(int dev, int lds) {
+  static RingLaunch cache[kHostMaxDevices];
+  static std::once_flag once[kHostMaxDevices];
+  std::call_once(once[dev], [dev, lds]() {
+    RingLaunch li;
+    int cus = 0;
+    li.err = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (li.err == hipSuccess)
+      li.err = hipFuncSetAttribute((const void *)Kernel,
+                                   hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    li.grid = cus - cus % kRingXcds;
+    if (li.grid < kRingXcds) li.grid = kRingXcds;
+    cache[dev] = li;
+  });
+  return cache[dev];
+}
+
+inline bool current_device(int *dev) {
+  return hipGetDevice(dev) == hipSuccess && *dev >= 0 && *dev < kHostMaxDevices;
+}
+
+}  // namespace gg

@@ -1,0 +1,490 @@
+// 4-bit microscaled operands for gfx950: quantisation, what the codes stand
+// for, and the ragged grouped product of them.
+//
+// The format is the OCP MX one for 4 bits: blocks of 32 values along K share a
+// scale 2^(code - 127) (E8M0, 0xFF = NaN); a value is E2M1, one of 0, .5, 1,
+// 1.5, 2, 3, 4, 6 with a sign. Codes lie two to a byte, the even k in the low
+// half. Scale bytes lie slice by slice, a slice being 256 k or 8 blocks:
+// scales[k / 256][row][(k / 32) % 8], so that the scales of a tile's rows in
+// one slice are one run of memory.
+
+#include "gg_common.h"
+#include "gg_host.h"
+#include "gg_ring.h"
+#include "gg_schedule.h"
+#include "grouped_gemm.h"
+
+namespace gg {
+
+constexpr int kBlockK = 32, kSliceK = 256, kSliceBlocks = kSliceK / kBlockK;
+constexpr int kQThreads = 256;
+
+// Scale code of a block whose largest magnitude has the bf16 bits `top`
+// (sign cleared): 2^(floor(log2 top) - 2), not below 2^-127; NaN where the
+// block holds an infinity or a NaN.
+__device__ __forceinline__ int scale_code(uint32_t top) {
+  const int e = (int)(top >> 7);  // 127 + floor(log2), 0 for zeros and subnormals
+  return e == 255 ? 255 : max(e - 2, 0);
+}
+
+// 2^(code - 127) as a float (code 0 is the subnormal 2^-127)
+__device__ __forceinline__ float scale_value(int code) {
+  return __builtin_bit_cast(float, code == 0 ? 0x00400000u : (uint32_t)code << 23);
+}
+
+// Eight bf16 values -> eight codes: v / scale to the nearest E2M1 value, ties
+// to even, at most 6 (v_cvt_scalef32_pk_fp4_bf16; checked against the
+// definition for every bf16 pattern).
+template <int PAIR>
+__device__ __forceinline__ uint32_t encode2(uint32_t q, uint32_t two, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, two), scale, PAIR);
+}
+__device__ __forceinline__ uint32_t encode8(u32x4 v, float scale) {
+  return encode2<3>(encode2<2>(encode2<1>(encode2<0>(0, v.x, scale), v.y, scale), v.z, scale), v.w,
+                    scale);
+}
+
+typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ uint32_t top8(u32x4 v) {
+  constexpr uint32_t kMag = 0x7fff7fffu;
+  return max_u16x2(max_u16x2(v.x & kMag, v.y & kMag), max_u16x2(v.z & kMag, v.w & kMag));
+}
+__device__ __forceinline__ uint32_t top_of_pair(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+
+// Rows: a lane takes 8 values (one 16-byte load, one 4-byte store), four
+// lanes a block. kChunks loads of a thread are in flight together.
+constexpr int kChunks = 4;
+
+__global__ __launch_bounds__(kQThreads) void mx4_rows_kernel(const u32x4 *__restrict__ X,
+                                                             uint32_t *__restrict__ q,
+                                                             uint8_t *__restrict__ scales,
+                                                             long long rows, int K) {
+  const uint32_t per_row = (uint32_t)K / 8;
+  const long long total = rows * per_row;
+  const long long c0 = (long long)blockIdx.x * (kQThreads * kChunks);
+  const long long row0 = c0 / per_row;
+  const uint32_t rem0 = (uint32_t)(c0 - row0 * per_row);
+  u32x4 v[kChunks];
+#pragma unroll
+  for (int j = 0; j < kChunks; ++j) {
+    const long long c = c0 + j * kQThreads + threadIdx.x;
+    v[j] = c < total ? X[c] : u32x4{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int j = 0; j < kChunks; ++j) {
+    const long long c = c0 + j * kQThreads + threadIdx.x;
+    uint32_t m = top8(v[j]);
+    m = max_u16x2(m, __shfl_xor(m, 1, kWave));
+    m = max_u16x2(m, __shfl_xor(m, 2, kWave));
+    const int code = scale_code(top_of_pair(m));
+    if (c >= total) continue;  // whole blocks: total is a multiple of 4
+    q[c] = code == 255 ? 0u : encode8(v[j], scale_value(code));
+    if (threadIdx.x % 4 == 0) {
+      const uint32_t at = rem0 + j * kQThreads + threadIdx.x;
+      const long long r = row0 + at / per_row;
+      int b = (int)(at % per_row) / 4;
+      uint8_t *const s = scales + ((long long)(b / kSliceBlocks) * rows + r) * kSliceBlocks;
+      s[b % kSliceBlocks] = (uint8_t)code;
+      if (b == K / kBlockK - 1)
+        while (++b % kSliceBlocks != 0) s[b % kSliceBlocks] = 0;  // no block there
+    }
+  }
+}
+
+// Weights [K][N] of an expert -> [N][K / 2]: blocks run down the columns. A
+// workgroup takes 256 k x 256 n; wave w block w of the slice, a lane four
+// columns (32 loads of 8 bytes, 512 bytes of a row to a wave). Codes go
+// through LDS, so that a column's 128 bytes leave as one run.
+constexpr int kWqThreads = 512, kWqCols = 256;
+
+__global__ __launch_bounds__(kWqThreads) void mx4_weights_kernel(const uint16_t *__restrict__ B,
+                                                                 uint8_t *__restrict__ q,
+                                                                 uint8_t *__restrict__ scales,
+                                                                 int K, int N, int slices) {
+  __shared__ __attribute__((aligned(16))) uint8_t codes[kWqCols * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t sc[kWqCols * kSliceBlocks];
+  const int slice = blockIdx.x % slices, e = blockIdx.x / slices;
+  const int n0 = blockIdx.y * kWqCols;
+  const int tid = threadIdx.x, w = tid / kWave, lane = tid % kWave;
+  const int k0 = slice * kSliceK + w * kBlockK;
+  const int n = n0 + 4 * lane;
+  const bool in = k0 < K && n < N;  // K is a multiple of 32, N of 8
+  const uint16_t *const src = B + ((size_t)e * K + k0) * N + n;
+  u32x2 v[kBlockK];
+#pragma unroll
+  for (int k = 0; k < kBlockK; ++k)
+    v[k] = in ? *(const gbl_u32x2 *)(src + (size_t)k * N) : u32x2{0, 0};
+  uint32_t m[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < kBlockK; ++k) {
+    m[0] = max_u16x2(m[0], v[k].x & 0x7fff7fffu);
+    m[1] = max_u16x2(m[1], v[k].y & 0x7fff7fffu);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t top = j % 2 ? m[j / 2] >> 16 : m[j / 2] & 0xffffu;
+    const int code = scale_code(top);
+    const float scale = scale_value(code);
+    u32x4 out;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      u32x4 in8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = v[8 * d + 2 * i][j / 2], b = v[8 * d + 2 * i + 1][j / 2];
+        in8[i] = j % 2 ? (a >> 16) | (b & 0xffff0000u) : (a & 0xffffu) | (b << 16);
+      }
+      out[d] = code == 255 ? 0u : encode8(in8, scale);
+    }
+    const int col = 4 * lane + j;
+    // chunk w of column col at chunk w ^ (lane % 8): the lanes of a store
+    // would otherwise all meet in the same banks
+    *(u32x4 *)(codes + col * 128 + 16 * (w ^ (lane % 8))) = out;
+    sc[col * kSliceBlocks + w] = k0 < K ? (uint8_t)code : 0;
+  }
+  __syncthreads();
+  const int c = tid % 8;
+#pragma unroll
+  for (int i = 0; i < kWqCols / (kWqThreads / 8); ++i) {
+    const int col = i * (kWqThreads / 8) + tid / 8;
+    const int k = slice * kSliceK + c * kBlockK;
+    if (k < K && n0 + col < N)
+      *(gbl_u32x4 *)(q + ((size_t)e * N + n0 + col) * (K / 2) + k / 2) =
+          *(const u32x4 *)(codes + col * 128 + 16 * (c ^ (col / 4 % 8)));
+  }
+  if (tid < kWqCols && n0 + tid < N)
+    *(gbl_u32x2 *)(scales + (((size_t)e * slices + slice) * N + n0 + tid) * kSliceBlocks) =
+        *(const u32x2 *)(sc + tid * kSliceBlocks);
+}
+
+// The bf16 values that codes and scales stand for, 8 to a lane. Every value
+// below 2^128 is a bf16 value; larger ones become infinite.
+__global__ __launch_bounds__(kQThreads) void mx4_values_kernel(const uint32_t *__restrict__ q,
+                                                               const uint8_t *__restrict__ scales,
+                                                               u32x4 *__restrict__ Y,
+                                                               long long rows, int K, int slices) {
+  const uint32_t per_row = (uint32_t)K / 8;
+  const long long total = rows * per_row;
+  const long long c0 = (long long)blockIdx.x * (kQThreads * kChunks);
+  const long long row0 = c0 / per_row;
+  const uint32_t rem0 = (uint32_t)(c0 - row0 * per_row);
+  const size_t base = (size_t)blockIdx.y * total;  // this batch
+  uint32_t w[kChunks];
+  int code[kChunks];
+#pragma unroll
+  for (int j = 0; j < kChunks; ++j) {
+    const long long c = c0 + j * kQThreads + threadIdx.x;
+    w[j] = 0;
+    code[j] = 0;
+    if (c < total) {
+      const uint32_t at = rem0 + j * kQThreads + threadIdx.x;
+      const long long r = row0 + at / per_row;
+      const int b = (int)(at % per_row) / 4;
+      w[j] = q[base + c];
+      code[j] = scales[(((size_t)blockIdx.y * slices + b / kSliceBlocks) * rows + r) * kSliceBlocks +
+                       b % kSliceBlocks];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kChunks; ++j) {
+    const long long c = c0 + j * kQThreads + threadIdx.x;
+    if (c >= total) continue;
+    u32x4 y = {0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+    if (code[j] != 255) {
+      const float s = scale_value(code[j]);
+      y.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 0));
+      y.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 1));
+      y.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 2));
+      y.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 3));
+    }
+    Y[base + c] = y;
+  }
+}
+
+// ----------------------------------------------------------------- product
+
+enum class MOut { F32, BF16, SwiGlu };
+
+struct Mx4Params {
+  const char *A, *As;   // [M_cap][K / 2], [slices][M_cap][8]
+  const char *B, *Bs;   // [E][N][K / 2], [E][slices][N][8]
+  const int32_t *off;
+  void *C;
+  int E, K, N, M_cap;
+  int bm_fixed, tile_cap;
+};
+
+// Tile heights as in gg_mainloop.h, eight waves, and the deepest ring that
+// 160 KB of LDS hold.
+using M16 = RingCfg<16, 128, 1, 8, 6, true>;
+using M16M = RingCfg<16, 256, 1, 8, 4, true>;
+using M16W = RingCfg<16, 512, 1, 8, 2, true>;
+using M32 = RingCfg<32, 256, 1, 8, 4, true>;
+using M64 = RingCfg<64, 256, 1, 8, 3, true>;
+using M128 = RingCfg<128, 256, 2, 4, 3, true>;
+using M256 = RingCfg<256, 256, 2, 4, 2, true>;
+
+__device__ __forceinline__ uint32_t swiglu_pair(f32x4 v) {
+  const f32x2 h = {silu(v.x) * v.y, silu(v.z) * v.w};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(h, bf16x2));
+}
+
+template <class C, MOut O>
+__device__ __forceinline__ void mx4_tile(const Mx4Params &p, const Tile &tl, lds_u8 *lds) {
+  const int row0 = __builtin_amdgcn_readfirstlane(tl.row0);
+  const int col0 = __builtin_amdgcn_readfirstlane(tl.col0);
+  const int expert = __builtin_amdgcn_readfirstlane(tl.expert);
+  // sizes the compiler cannot see through: what it derives from them is then
+  // computed per tile instead of being kept (and spilled) across tiles
+  int K_ = p.K, N_ = p.N, M_ = p.M_cap;
+  asm volatile("" : "+s"(K_), "+s"(N_), "+s"(M_));
+  const int slices = cdiv(K_, kSliceK);
+  RingTile t;
+  t.pitch = (uint32_t)K_ / 2;
+  t.A = p.A + (size_t)row0 * t.pitch;
+  t.B = p.B + ((size_t)expert * N_ + col0) * t.pitch;
+  t.as_step = (size_t)M_ * kSliceBlocks;
+  t.bs_step = (size_t)N_ * kSliceBlocks;
+  t.As = p.As + (size_t)row0 * kSliceBlocks;
+  t.Bs = p.Bs + (size_t)expert * slices * t.bs_step + (size_t)col0 * kSliceBlocks;
+  t.rows = __builtin_amdgcn_readfirstlane(tl.rows);
+  t.ncols = min(C::BN, N_ - col0);
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // keep per-tile index arithmetic inside the tile
+  t.tid = tid;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+  const int wm0 = (wave / C::WN) * C::WTM, wn0 = (wave % C::WN) * C::WTN;
+  const int g = lane / 16, s = lane % 16;
+  const size_t N = N_;
+  f32x4 acc[C::NI][C::MI];
+  auto epi = [&](int mi) {
+    const int m = wm0 + mi * 16 + s;
+    const size_t row = (size_t)(row0 + m);
+    const bool in = m < t.rows;
+    if constexpr (O == MOut::F32) {
+#pragma unroll
+      for (int ni = 0; ni < C::NI; ++ni) {
+        const int n = wn0 + ni * 16 + 4 * g;
+        if (in && n < t.ncols) st_g16((float *)p.C + row * N + col0 + n, acc[ni][mi]);
+      }
+    } else if constexpr (O == MOut::BF16) {
+      uint16_t *const out = (uint16_t *)p.C + row * N + col0;
+      if constexpr (C::NI % 2 == 0) {
+#pragma unroll
+        for (int ni = 0; ni < C::NI; ni += 2) {
+          const u32x4 v = swap_pair(pack_bf16(acc[ni][mi]), pack_bf16(acc[ni + 1][mi]));
+          const int n = wn0 + (ni + g % 2) * 16 + 8 * (g / 2);
+          if (in && n < t.ncols) st_g16u(out + n, v);
+        }
+      } else {
+#pragma unroll
+        for (int ni = 0; ni < C::NI; ++ni) {
+          const int n = wn0 + ni * 16 + 4 * g;
+          if (in && n < t.ncols) st_g8u(out + n, pack_bf16(acc[ni][mi]));
+        }
+      }
+    } else {
+      // two activations a block and lane: columns n, n + 1 and n + 2, n + 3
+      uint16_t *const out = (uint16_t *)p.C + row * (N / 2) + col0 / 2;
+      if constexpr (C::NI % 2 == 0) {
+#pragma unroll
+        for (int ni = 0; ni < C::NI; ni += 2) {
+          const auto h = __builtin_amdgcn_permlane16_swap(swiglu_pair(acc[ni][mi]),
+                                                          swiglu_pair(acc[ni + 1][mi]), false, false);
+          const int n = wn0 + (ni + g % 2) * 16 + 8 * (g / 2);
+          if (in && n < t.ncols) st_g8u(out + n / 2, u32x2{h[0], h[1]});
+        }
+      } else {
+#pragma unroll
+        for (int ni = 0; ni < C::NI; ++ni) {
+          const int n = wn0 + ni * 16 + 4 * g;
+          if (in && n < t.ncols)
+            *(__attribute__((address_space(1))) uint32_t *)(out + n / 2) = swiglu_pair(acc[ni][mi]);
+        }
+      }
+    }
+  };
+  run_ring_tile<C, kCacheStream>(t, lds, acc, K_ / kBlockK, epi);
+}
+
+template <int MASK>
+constexpr int mx4_lds() {
+  int m = 0;
+  const int b[] = {M16::LDS_BYTES, M16M::LDS_BYTES, M16W::LDS_BYTES};
+  if (MASK & 1)
+    for (int v : b) m = m > v ? m : v;
+  if (MASK & 2) m = m > M32::LDS_BYTES ? m : M32::LDS_BYTES;
+  if (MASK & 4) m = m > M64::LDS_BYTES ? m : M64::LDS_BYTES;
+  if (MASK & 8) m = m > M128::LDS_BYTES ? m : M128::LDS_BYTES;
+  if (MASK & 16) m = m > M256::LDS_BYTES ? m : M256::LDS_BYTES;
+  return m;
+}
+
+// MASK bit c compiles in tile height 16 << c.
+template <int MASK, MOut O>
+__global__ __launch_bounds__(kThreads, 1) void mx4_product_kernel(Mx4Params p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds_dyn[];
+  lds_u8 *const lds = (lds_u8 *)lds_dyn;
+  RingSched &sched = *(RingSched *)(lds_dyn + mx4_lds<MASK>());
+  const int G = gridDim.x, b = blockIdx.x;
+  const int total = build_ring_schedule(sched, p.off, p.E, p.M_cap, p.N, p.bm_fixed, p.tile_cap, G);
+  // contiguous tiles on one XCD (workgroup ids go round-robin to the XCDs)
+  const int slot = (b % kRingXcds) * (G / kRingXcds) + b / kRingXcds;
+  for (int base = 0; base < total; base += G) {
+    const int t = base + slot;
+    if (t >= total) break;
+    const Tile tl = decode_ring_tile(sched, p.off, t, p.E, p.M_cap, p.N, p.bm_fixed);
+    switch (tl.bm) {
+      case 16:
+        if constexpr (MASK & 1) {
+          if (tl.bn == kWideN) mx4_tile<M16W, O>(p, tl, lds);
+          else if (tl.bn == kTileN) mx4_tile<M16M, O>(p, tl, lds);
+          else mx4_tile<M16, O>(p, tl, lds);
+        }
+        break;
+      case 32: if constexpr (MASK & 2) mx4_tile<M32, O>(p, tl, lds); break;
+      case 64: if constexpr (MASK & 4) mx4_tile<M64, O>(p, tl, lds); break;
+      case 128: if constexpr (MASK & 8) mx4_tile<M128, O>(p, tl, lds); break;
+      default: if constexpr (MASK & 16) mx4_tile<M256, O>(p, tl, lds); break;
+    }
+  }
+}
+
+static_assert(mx4_lds<31>() + sizeof(RingSched) <= 160 * 1024, "LDS budget");
+
+template <int MASK, MOut O>
+static gg_status_t launch_mx4(const Mx4Params &p, long long bound, hipStream_t stream) {
+  constexpr int lds = mx4_lds<MASK>() + (int)sizeof(RingSched);
+  int dev = 0;
+  if (!current_device(&dev)) return GG_ERR_LAUNCH;
+  const RingLaunch li = ring_launch<mx4_product_kernel<MASK, O>>(dev, lds);
+  if (li.err != hipSuccess) return GG_ERR_LAUNCH;
+  long long g = bound < li.grid ? bound : li.grid;
+  g = (g + kRingXcds - 1) / kRingXcds * kRingXcds;
+  hipLaunchKernelGGL((mx4_product_kernel<MASK, O>), dim3((unsigned)g), dim3(kThreads), lds, stream,
+                     p);
+  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+}
+
+template <MOut O>
+static gg_status_t mx4_product(const void *Aq, const void *a_scale, const void *Bq,
+                               const void *b_scale, const int32_t *off, void *C, int E, int K,
+                               int N, int M_cap, int bm, void *stream) {
+  long long bound = 0;
+  gg_status_t st = check_groups(off, E, N, M_cap, bm, kNarrowN, &bound);
+  if (st != GG_OK) return st;
+  if (Bq == nullptr || b_scale == nullptr || K < 1) return GG_ERR_INVALID_VALUE;
+  // arrays of no rows may be null
+  if (M_cap > 0 && (Aq == nullptr || a_scale == nullptr || C == nullptr)) return GG_ERR_INVALID_VALUE;
+  if (K % kBlockK != 0 || N % 8 != 0) return GG_ERR_MISALIGNED;
+  // a tile's weight rows, 512 * K / 2 bytes, stay within 32-bit offsets
+  if (K > GG_MAX_K || N > GG_MAX_N) return GG_ERR_UNSUPPORTED;
+  if (!is_aligned(Aq, 16) || !is_aligned(a_scale, 16) || !is_aligned(Bq, 16) ||
+      !is_aligned(b_scale, 16) || !is_aligned(C, 16))
+    return GG_ERR_MISALIGNED;
+  if (M_cap == 0) return GG_OK;
+  const Mx4Params p{static_cast<const char *>(Aq), static_cast<const char *>(a_scale),
+                    static_cast<const char *>(Bq), static_cast<const char *>(b_scale), off, C, E, K,
+                    N, M_cap, bm, (int)bound};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (bm) {
+    case 16: return launch_mx4<1, O>(p, bound, s);
+    case 32: return launch_mx4<2, O>(p, bound, s);
+    case 64: return launch_mx4<4, O>(p, bound, s);
+    case 128: return launch_mx4<8, O>(p, bound, s);
+    case 256: return launch_mx4<16, O>(p, bound, s);
+    default: return launch_mx4<31, O>(p, bound, s);
+  }
+}
+
+// Sizes of the row kernels: blocks of a launch, within the grid's limit.
+static gg_status_t check_rows(int64_t rows, int K, long long *blocks) {
+  if (rows < 0 || K < 1) return GG_ERR_INVALID_VALUE;
+  if (K % kBlockK != 0) return GG_ERR_MISALIGNED;
+  if (K > GG_MAX_K || rows > INT32_MAX) return GG_ERR_UNSUPPORTED;
+  const long long per = kQThreads * kChunks;
+  *blocks = (rows * (K / 8) + per - 1) / per;
+  return *blocks > (1LL << 28) ? GG_ERR_UNSUPPORTED : GG_OK;
+}
+
+}  // namespace gg
+
+using namespace gg;
+
+extern "C" gg_status_t gg_mx4_quantize(const void *X, void *q, void *scales, int64_t rows,
+                                       int32_t K, void *stream) {
+  long long blocks = 0;
+  const gg_status_t st = check_rows(rows, K, &blocks);
+  if (st != GG_OK) return st;
+  if (rows == 0) return GG_OK;
+  if (X == nullptr || q == nullptr || scales == nullptr) return GG_ERR_INVALID_VALUE;
+  if (!is_aligned(X, 16) || !is_aligned(q, 16) || !is_aligned(scales, 16)) return GG_ERR_MISALIGNED;
+  hipLaunchKernelGGL(mx4_rows_kernel, dim3((unsigned)blocks), dim3(kQThreads), 0,
+                     static_cast<hipStream_t>(stream), static_cast<const u32x4 *>(X),
+                     static_cast<uint32_t *>(q), static_cast<uint8_t *>(scales), (long long)rows, K);
+  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+}
+
+extern "C" gg_status_t gg_mx4_quantize_weights(const void *B, void *q, void *scales, int32_t E,
+                                               int32_t K, int32_t N, void *stream) {
+  if (B == nullptr || q == nullptr || scales == nullptr || E < 1 || K < 1 || N < 1)
+    return GG_ERR_INVALID_VALUE;
+  if (!is_aligned(B, 16) || !is_aligned(q, 16) || !is_aligned(scales, 16) || K % kBlockK != 0 ||
+      N % 8 != 0)
+    return GG_ERR_MISALIGNED;
+  const long long slices = (K + (long long)kSliceK - 1) / kSliceK, cols = (N + (long long)kWqCols - 1) / kWqCols;
+  // cols is the grid's y
+  if (E > kMaxExperts || K > GG_MAX_K || cols > 65535) return GG_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL(mx4_weights_kernel, dim3((unsigned)(slices * E), (unsigned)cols),
+                     dim3(kWqThreads), 0, static_cast<hipStream_t>(stream),
+                     static_cast<const uint16_t *>(B), static_cast<uint8_t *>(q),
+                     static_cast<uint8_t *>(scales), K, N, (int)slices);
+  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+}
+
+extern "C" gg_status_t gg_mx4_dequantize(const void *q, const void *scales, void *Y, int32_t batch,
+                                         int64_t rows, int32_t K, void *stream) {
+  long long blocks = 0;
+  const gg_status_t st = check_rows(rows, K, &blocks);
+  if (st != GG_OK) return st;
+  if (batch < 0) return GG_ERR_INVALID_VALUE;
+  if (batch > 65535) return GG_ERR_UNSUPPORTED;
+  if (rows == 0 || batch == 0) return GG_OK;
+  if (q == nullptr || scales == nullptr || Y == nullptr) return GG_ERR_INVALID_VALUE;
+  if (!is_aligned(q, 16) || !is_aligned(scales, 16) || !is_aligned(Y, 16)) return GG_ERR_MISALIGNED;
+  hipLaunchKernelGGL(mx4_values_kernel, dim3((unsigned)blocks, (unsigned)batch), dim3(kQThreads), 0,
+                     static_cast<hipStream_t>(stream), static_cast<const uint32_t *>(q),
+                     static_cast<const uint8_t *>(scales), static_cast<u32x4 *>(Y),
+                     (long long)rows, K, (K + kSliceK - 1) / kSliceK);
+  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+}
+
+extern "C" gg_status_t gg_grouped_gemm_mx4(const void *Aq, const void *a_scale, const void *Bq,
+                                           const void *b_scale, const int32_t *group_offsets,
+                                           float *C, int32_t E, int32_t K, int32_t N,
+                                           int32_t M_cap, int32_t bm, void *stream) {
+  return mx4_product<MOut::F32>(Aq, a_scale, Bq, b_scale, group_offsets, C, E, K, N, M_cap, bm,
+                                stream);
+}
+
+extern "C" gg_status_t gg_grouped_gemm_mx4_bf16out(const void *Aq, const void *a_scale,
+                                                   const void *Bq, const void *b_scale,
+                                                   const int32_t *group_offsets, void *C,
+                                                   int32_t E, int32_t K, int32_t N, int32_t M_cap,
+                                                   int32_t bm, void *stream) {
+  return mx4_product<MOut::BF16>(Aq, a_scale, Bq, b_scale, group_offsets, C, E, K, N, M_cap, bm,
+                                 stream);
+}
+
+extern "C" gg_status_t gg_grouped_gemm_mx4_swiglu(const void *Aq, const void *a_scale,
+                                                  const void *Bq, const void *b_scale,
+                                                  const int32_t *group_offsets, void *H, int32_t E,
+                                                  int32_t K, int32_t N, int32_t M_cap, int32_t bm,
+                                                  void *stream) {
+  return mx4_product<MOut::SwiGlu>(Aq, a_scale, Bq, b_scale, group_offsets, H, E, K, N, M_cap, bm,
+                                   stream);
+}

@@ -1,0 +1,342 @@
+// Weight gradient of the ragged grouped product, for gfx950:
+//
+//   dB[e][k][n] = sum over the rows r of expert e of A[r][k] * dC[r][n]
+//
+// The summed index is the row, the slow one of both operands, and its length
+// is the expert's row count: ragged, read on the device, possibly zero (that
+// expert's gradient is zero). An output tile is BM x BN of one expert's
+// weights; its slices are RB rows of A and of dC, brought into a ring of LDS
+// stages by buffer_load ... lds (gg_ring.h) and read by the transposing LDS
+// read (ds_read_b64_tr_b16), which hands a lane the four rows of one column.
+// The buffers end at the group's last row, so the rows of a slice past it
+// read as zeros in both operands.
+//
+// One workgroup per tile, four waves, two workgroups to a CU: while one
+// stores its tile the other multiplies. The tiles of all experts number
+// E * ceil(K / BM) * ceil(N / BN) whatever the routing, so the grid is known on
+// the host and the hardware hands the next tile to whichever CU is free. A
+// launch ends with its longest tile, so experts come in the order of their
+// size class (power of two of the row count), largest first.
+
+#include "gg_common.h"
+#include "gg_host.h"
+#include "gg_ring.h"
+#include "grouped_gemm.h"
+
+namespace gg {
+
+enum class WOut { F32, AddF32, BF16 };
+
+struct WgradParams {
+  const char *A;    // [M_cap][K] bf16
+  const char *dC;   // [M_cap][N] bf16
+  const int32_t *off;
+  void *dB;         // [E][K][N]
+  int E, K, N, M_cap;
+  int tiles;        // tiles of one expert
+  int per_xcd;      // ceil(tiles / 8)
+};
+
+constexpr int kWThreads = 256;
+constexpr int kWWaves = kWThreads / kWave;
+
+template <int BM_, int BN_, int WM_, int WN_, int RB_, int S_>
+struct WgradCfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, RB = RB_, S = S_;
+  static_assert(WM * WN == kWWaves, "one wave per wave tile");
+  static constexpr int WTM = BM / WM, WTN = BN / WN;
+  static constexpr int MI = WTM / 16, NI = WTN / 16;
+  static_assert(MI * 16 * WM == BM && NI * 16 * WN == BN && RB % 32 == 0, "16x16x32 blocks");
+  static constexpr int A_ROW = 2 * BM, B_ROW = 2 * BN;  // bytes of a slice row
+  static constexpr int A_BYTES = RB * A_ROW, B_BYTES = RB * B_ROW, STAGE = A_BYTES + B_BYTES;
+  static constexpr int A_INSTR = A_BYTES / (1024 * kWWaves), B_INSTR = B_BYTES / (1024 * kWWaves);
+  static_assert(A_INSTR * 1024 * kWWaves == A_BYTES && B_INSTR * 1024 * kWWaves == B_BYTES, "loads");
+  static constexpr int LPS = A_INSTR + B_INSTR;
+  static constexpr int LDS_BYTES = S * STAGE;
+};
+
+// Chunk (16 bytes) c of slice row r sits at chunk c ^ swz(r). A transposing
+// read touches rows 8 g + k' (k' < 4) of every lane group g, 32 bytes each;
+// the XOR spreads those over the banks (for 512-byte rows: gg_mainloop.h).
+// 128-byte rows have 8 chunks, and neighbouring rows lie in different halves
+// of the banks already.
+template <int ROW>
+__device__ __forceinline__ int wg_swz(int r) {
+  if constexpr (ROW >= 256) return ((r & 3) << 1) | (((r >> 3) & 1) << 3);
+  else return (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2);
+}
+
+// Byte offset of this lane's load i inside a slice of an operand of `pitch`
+// bytes a row; `col` gets the byte column it starts at.
+template <int ROW>
+__device__ __forceinline__ uint32_t wg_off(int i, int wave, int lane, uint32_t pitch, uint32_t &col) {
+  constexpr int kRows = 1024 / ROW;  // rows of one load instruction
+  const int r = (i * kWWaves + wave) * kRows + lane / (64 / kRows);
+  const int c = (lane % (64 / kRows)) ^ wg_swz<ROW>(r);
+  col = 16u * c;
+  return (uint32_t)r * pitch + col;
+}
+
+template <class C>
+struct WgradTile {
+  const char *A, *B;        // row 0 of the group, first column of the tile
+  uint32_t a_pitch, b_pitch;  // bytes of a row
+  uint32_t a_cols, b_cols;    // bytes of a row from the tile's first column on
+  int rows;
+};
+
+template <class C>
+__device__ __forceinline__ void wg_issue(const WgradTile<C> &t, lds_u8 *stage, int k, int wave,
+                                         int lane) {
+  const int left = min(C::RB, t.rows - k * C::RB);
+  const size_t r0 = (size_t)k * C::RB;
+  // the resource ends with the last row that belongs to the group; a lane
+  // past the row's end is out of range too
+  const buf_rsrc ra = make_buf(t.A + r0 * t.a_pitch, (uint32_t)(left - 1) * t.a_pitch + t.a_cols);
+  const buf_rsrc rb = make_buf(t.B + r0 * t.b_pitch, (uint32_t)(left - 1) * t.b_pitch + t.b_cols);
+#pragma unroll
+  for (int i = 0; i < C::A_INSTR; ++i) {
+    uint32_t col;
+    const uint32_t off = wg_off<C::A_ROW>(i, wave, lane, t.a_pitch, col);
+    dma16(ra, stage + (i * kWWaves + wave) * 1024, col < t.a_cols ? off : kOob);
+  }
+#pragma unroll
+  for (int i = 0; i < C::B_INSTR; ++i) {
+    uint32_t col;
+    const uint32_t off = wg_off<C::B_ROW>(i, wave, lane, t.b_pitch, col);
+    dma16(rb, stage + C::A_BYTES + (i * kWWaves + wave) * 1024, col < t.b_cols ? off : kOob);
+  }
+}
+
+// A 16-column fragment of 32 slice rows: lane 16 g + s gets column s of rows
+// 8 g .. 8 g + 7. p addresses row 8 g + s / 4, four columns of it.
+template <int ROW>
+__device__ __forceinline__ bf16x8 wg_frag(const lds_u8 *p) {
+  const s16x4 lo = lds_read_tr16((const lds_u16 *)p);
+  const s16x4 hi = lds_read_tr16((const lds_u16 *)(p + 4 * ROW));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int ROW>
+__device__ __forceinline__ int wg_frag_off(int lane, int col0) {
+  const int g = lane / 16, s = lane % 16;
+  const int r = 8 * g + s / 4, c = col0 + 4 * (s % 4);
+  return r * ROW + 16 * ((c / 8) ^ wg_swz<ROW>(r)) + 2 * (c % 8);
+}
+
+template <class C>
+__device__ __forceinline__ void wg_step(f32x4 (&acc)[C::NI][C::MI], const WgradTile<C> &t,
+                                        const lds_u8 *__restrict__ cur, lds_u8 *__restrict__ nxt,
+                                        int k_next, int KT, int wave, int lane, int a_off,
+                                        int b_off) {
+  if (k_next < KT) wg_issue<C>(t, nxt, k_next, wave, lane);
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_setprio(1);
+  static_for<C::RB / 32>([&](auto ksc) {
+    constexpr int ks = decltype(ksc)::value;
+    bf16x8 x[C::NI];
+    // a block's 32 bytes are bits 5.. of the chunk index, which the swizzle
+    // XORs: block i is the first one's address XOR 32 i
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ++ni)
+      x[ni] = wg_frag<C::B_ROW>(cur + C::A_BYTES + 32 * ks * C::B_ROW + (b_off ^ (32 * ni)));
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi) {
+      const bf16x8 y = wg_frag<C::A_ROW>(cur + 32 * ks * C::A_ROW + (a_off ^ (32 * mi)));
+#pragma unroll
+      for (int ni = 0; ni < C::NI; ++ni)
+        acc[ni][mi] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[ni], y, acc[ni][mi], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  });
+  __builtin_amdgcn_s_setprio(0);
+}
+
+// The expert at position p of the order by size class, largest class first
+// and by index inside a class. Every thread of the workgroup calls this; all
+// workgroups find the same order.
+struct WgradOrder {
+  int count[kMaxExperts / kWave][32];  // experts of a class in each run of 64
+  int expert;
+};
+
+__device__ __forceinline__ int size_class(int rows) { return rows > 0 ? 32 - __builtin_clz(rows) : 0; }
+
+__device__ __forceinline__ int group_rows(const int32_t *off, int e, int M_cap) {
+  return max(0, clamp_off(off, e + 1, M_cap) - clamp_off(off, e, M_cap));
+}
+
+__device__ __forceinline__ int wgrad_expert(WgradOrder &o, const int32_t *__restrict__ off, int E, int M_cap,
+                                   int p) {
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int runs = cdiv(E, kWave);
+  constexpr int kPer = kMaxExperts / kWThreads;  // runs of 64 a wave may own
+  int cls[kPer], rank[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int run = j * kWWaves + wave, e = run * kWave + lane;
+    cls[j] = -1;
+    rank[j] = 0;
+    if (run < runs) {
+      if (e < E) cls[j] = size_class(group_rows(off, e, M_cap));
+      for (int c = 0; c < 32; ++c) {
+        const unsigned long long b = __ballot(cls[j] == c);
+        if (cls[j] == c) rank[j] = __popcll(b & ((1ull << lane) - 1));
+        if (lane == 0) o.count[run][c] = __popcll(b);
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (cls[j] < 0) continue;
+    const int run = j * kWWaves + wave;
+    int at = rank[j];
+    for (int q = 0; q < runs; ++q) {
+      for (int c = cls[j] + 1; c < 32; ++c) at += o.count[q][c];
+      if (q < run) at += o.count[q][cls[j]];
+    }
+    if (at == p) o.expert = run * kWave + lane;
+  }
+  __syncthreads();
+  return o.expert;
+}
+
+template <class C, WOut O>
+__global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds_dyn[];
+  lds_u8 *const lds = (lds_u8 *)lds_dyn;
+  WgradOrder &order = *(WgradOrder *)(lds_dyn + C::LDS_BYTES);
+  // tiles of one expert in runs of per_xcd to an XCD (workgroup ids go
+  // round-robin to the XCDs), k inner: a run's dC columns stay in one L2
+  const int xcd = blockIdx.x % kRingXcds, i = blockIdx.x / kRingXcds;
+  const int pos = i / p.per_xcd, local = xcd * p.per_xcd + i % p.per_xcd;
+  if (local >= p.tiles) return;
+  const int e = __builtin_amdgcn_readfirstlane(wgrad_expert(order, p.off, p.E, p.M_cap, pos));
+  const int KT_cols = cdiv(p.K, C::BM);
+  const int nt = local / KT_cols, kt = local % KT_cols;
+  const int r0 = __builtin_amdgcn_readfirstlane(clamp_off(p.off, e, p.M_cap));
+  const int rows = __builtin_amdgcn_readfirstlane(group_rows(p.off, e, p.M_cap));
+  if (O == WOut::AddF32 && rows == 0) return;  // nothing to add
+
+  const int col_k = kt * C::BM, col_n = nt * C::BN;
+  WgradTile<C> t;
+  t.a_pitch = 2u * (uint32_t)p.K;
+  t.b_pitch = 2u * (uint32_t)p.N;
+  t.A = p.A + (size_t)r0 * t.a_pitch + 2 * (size_t)col_k;
+  t.B = p.dC + (size_t)r0 * t.b_pitch + 2 * (size_t)col_n;
+  t.a_cols = t.a_pitch - 2u * (uint32_t)col_k;
+  t.b_cols = t.b_pitch - 2u * (uint32_t)col_n;
+  t.rows = rows;
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+  const int wm0 = (wave / C::WN) * C::WTM, wn0 = (wave % C::WN) * C::WTN;
+  const int a_off = wg_frag_off<C::A_ROW>(lane, wm0), b_off = wg_frag_off<C::B_ROW>(lane, wn0);
+
+  f32x4 acc[C::NI][C::MI];
+#pragma unroll
+  for (int ni = 0; ni < C::NI; ++ni)
+#pragma unroll
+    for (int mi = 0; mi < C::MI; ++mi) acc[ni][mi] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int KT = cdiv(rows, C::RB);
+#pragma unroll
+  for (int k = 0; k < C::S - 1; ++k)
+    if (k < KT) wg_issue<C>(t, lds + k * C::STAGE, k, wave, lane);
+  int cur = 0, nxt = C::S - 1;
+  for (int k = 0; k < KT; ++k) {
+    // slices k + 1 .. min(k + S - 2, KT - 1) stay in flight
+    wait_slices<C>(min(C::S - 2, KT - 1 - k));
+    wg_barrier();
+    wg_step<C>(acc, t, lds + cur * C::STAGE, lds + nxt * C::STAGE, k + C::S - 1, KT, wave, lane,
+               a_off, b_off);
+    cur = cur + 1 == C::S ? 0 : cur + 1;
+    nxt = nxt + 1 == C::S ? 0 : nxt + 1;
+  }
+
+  // lane 16 g + s holds columns 4 g .. 4 g + 3 of row s of every block
+  const int g = lane / 16, s = lane % 16;
+  const size_t base = ((size_t)e * p.K + col_k) * p.N + col_n;
+  const int k_in = p.K - col_k, n_in = p.N - col_n;
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi) {
+    const int m = wm0 + mi * 16 + s;
+    const bool in = m < k_in;
+    if constexpr (O == WOut::BF16) {
+#pragma unroll
+      for (int ni = 0; ni < C::NI; ni += 2) {
+        const u32x4 v = swap_pair(pack_bf16(acc[ni][mi]), pack_bf16(acc[ni + 1][mi]));
+        const int n = wn0 + (ni + g % 2) * 16 + 8 * (g / 2);
+        if (in && n < n_in) st_g16u((uint16_t *)p.dB + base + (size_t)m * p.N + n, v);
+      }
+    } else {
+#pragma unroll
+      for (int ni = 0; ni < C::NI; ++ni) {
+        const int n = wn0 + ni * 16 + 4 * g;
+        float *const at = (float *)p.dB + base + (size_t)m * p.N + n;
+        if (in && n < n_in) {
+          if constexpr (O == WOut::AddF32) st_g16(at, acc[ni][mi] + ld_g16f(at));
+          else st_g16(at, acc[ni][mi]);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+using W128 = WgradCfg<128, 256, 2, 2, 32, 3>;  // wave tile 64 x 128
+using W64 = WgradCfg<64, 64, 2, 2, 32, 4>;     // wave tile 32 x 32
+
+static_assert(2 * (W128::LDS_BYTES + (int)sizeof(WgradOrder)) <= 160 * 1024, "two workgroups a CU");
+
+template <class C, WOut O>
+static gg_status_t launch_wgrad(WgradParams p, hipStream_t stream) {
+  constexpr int lds = C::LDS_BYTES + (int)sizeof(WgradOrder);
+  const long long tiles = ((p.K + (long long)C::BM - 1) / C::BM) * ((p.N + (long long)C::BN - 1) / C::BN);
+  const long long per = (tiles + kRingXcds - 1) / kRingXcds;
+  const long long grid = per * kRingXcds * p.E;
+  if (grid > (1LL << 28)) return GG_ERR_UNSUPPORTED;
+  int dev = 0;
+  if (!current_device(&dev)) return GG_ERR_LAUNCH;
+  if (ring_launch<wgrad_kernel<C, O>>(dev, lds).err != hipSuccess) return GG_ERR_LAUNCH;
+  p.tiles = (int)tiles;
+  p.per_xcd = (int)per;
+  hipLaunchKernelGGL((wgrad_kernel<C, O>), dim3((unsigned)grid), dim3(kWThreads), lds, stream, p);
+  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+}
+
+template <WOut O>
+static gg_status_t wgrad(const void *A, const void *dC, const int32_t *off, void *dB, int E, int K,
+                         int N, int M_cap, void *stream) {
+  if (off == nullptr || dB == nullptr || E < 1 || K < 1 || N < 1 || M_cap < 0)
+    return GG_ERR_INVALID_VALUE;
+  if (M_cap > 0 && (A == nullptr || dC == nullptr)) return GG_ERR_INVALID_VALUE;
+  if (!is_aligned(off, 4) || !is_aligned(A, 16) || !is_aligned(dC, 16) || !is_aligned(dB, 16) ||
+      K % 8 != 0 || N % 8 != 0)
+    return GG_ERR_MISALIGNED;
+  if (E > kMaxExperts || K > GG_MAX_K || N > GG_MAX_K || M_cap > INT32_MAX - 256)
+    return GG_ERR_UNSUPPORTED;
+  WgradParams p{static_cast<const char *>(A), static_cast<const char *>(dC), off, dB, E, K, N,
+                M_cap, 0, 0};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const long long big = (long long)E * ((K + 127) / 128) * ((N + 255) / 256);
+  return big >= 256 ? launch_wgrad<W128, O>(p, s) : launch_wgrad<W64, O>(p, s);
+}
+
+}  // namespace gg
+
+using namespace gg;
+
+extern "C" gg_status_t gg_grouped_gemm_bf16_wgrad(const void *A, const void *dC,
+                                                  const int32_t *group_offsets, float *dB,
+                                                  int32_t accumulate, int32_t E, int32_t K,
+                                                  int32_t N, int32_t M_cap, void *stream) {
+  return accumulate ? wgrad<WOut::AddF32>(A, dC, group_offsets, dB, E, K, N, M_cap, stream)
+                    : wgrad<WOut::F32>(A, dC, group_offsets, dB, E, K, N, M_cap, stream);
+}
+
+extern "C" gg_status_t gg_grouped_gemm_bf16_wgrad_bf16out(const void *A, const void *dC,
+                                                          const int32_t *group_offsets, void *dB,
+                                                          int32_t E, int32_t K, int32_t N,
+                                                          int32_t M_cap, void *stream) {
+  return wgrad<WOut::BF16>(A, dC, group_offsets, dB, E, K, N, M_cap, stream);
+}

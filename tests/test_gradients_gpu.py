@@ -1,0 +1,361 @@
+"""The gradients of the grouped product on the GPU against binary64 (needs an MI355X)."""
+
+import numpy as np
+import pytest
+
+import oracle
+import oracle.operators as ref
+import workloads as wl
+from tests import operators as ops
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+BMS = [0, 16, 32, 64, 128, 256]
+DTYPES = ["fp32", "bf16"]
+
+
+@pytest.fixture(scope="module")
+def gg():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import moe_ragged_grouped_amd as m
+    m.load_library()
+    return m
+
+
+def _dt(name):
+    return torch.float32 if name == "fp32" else torch.bfloat16
+
+
+def _check(out, *args):
+    (ops.check_f32 if out == "fp32" else ops.check_bf16)(*args)
+
+
+def _dgrad_case(gg, sizes, K, N, bm, out, seed, spare=3, draw=ops.bits):
+    rng = np.random.default_rng(seed)
+    off = ops.offsets_of(sizes)
+    M = int(off[-1])
+    dC, B = draw(rng, M + spare, N), draw(rng, len(sizes), K, N)
+    got = torch.full((M + spare, K), float("nan"), dtype=_dt(out), device="cuda:0")
+    ret = gg.grouped_gemm_dgrad(ops.to_dev(dC), ops.to_dev(B), ops.to_dev(off), out=got, bm=bm)
+    assert ret is got
+    got = ops.host(got)
+    want, S = ref.dgrad(dC, B, off)
+    assert np.isnan(got[M:]).all(), "rows past the last group were written"
+    return got[:M], want[:M], S[:M]
+
+
+# empty and one-row experts, an expert of several tiles, lengths that end
+# inside a slice (64 columns), inside a 16-byte piece's tile (8) and inside a
+# 128- or 256-wide tile
+SHAPES = [([0, 1, 17, 130, 0, 300], 328, 392), ([5], 8, 8), ([1], 136, 64), ([16, 16, 16], 1032, 72),
+          ([300, 0, 45, 517], 200, 776), ([0, 0, 3], 264, 1000), ([33, 64, 65, 2], 512, 128)]
+
+
+@pytest.mark.parametrize("bm", BMS)
+@pytest.mark.parametrize("sizes,K,N", SHAPES)
+def test_dgrad(gg, sizes, K, N, bm):
+    for i, out in enumerate(DTYPES):
+        got, want, S = _dgrad_case(gg, sizes, K, N, bm, out, 100 + i)
+        _check(out, got, want, ops.sum_bound(N, S), "dgrad %s bm=%d %s" % (sizes, bm, out))
+
+
+@pytest.mark.parametrize("bm", BMS)
+def test_dgrad_integers_are_exact(gg, bm):
+    # every partial sum is an integer below 2^24
+    got, want, _ = _dgrad_case(gg, [5, 0, 40, 129, 16], 264, 512, bm, "fp32", 7, draw=ops.int_bits)
+    assert (got == want).all()
+
+
+def test_dgrad_all_groups_empty(gg):
+    got, want, _ = _dgrad_case(gg, [0, 0], 64, 64, 0, "fp32", 1)
+    assert got.shape == (0, 64)
+
+
+def test_dgrad_no_rows_at_all(gg):
+    dC = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda:0")
+    B = torch.ones((2, 32, 64), dtype=torch.bfloat16, device="cuda:0")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda:0")
+    assert gg.grouped_gemm_dgrad(dC, B, off).shape == (0, 32)
+
+
+def test_dgrad_nonfinite_stays_in_its_rows(gg):
+    # an infinity or NaN in one row or one expert's weights reaches only the
+    # results that sum over it; spare rows of NaN reach none
+    rng = np.random.default_rng(3)
+    off = ops.offsets_of([20, 30, 5])
+    dC, B = ops.bits(rng, 60, 200), ops.bits(rng, 3, 136, 200)
+    dC[55:] = 0x7FC0
+    dC[7, 3] = 0x7F80
+    B[1, 9, 150] = 0x7FC0
+    for bm in BMS:
+        got = ops.host(gg.grouped_gemm_dgrad(ops.to_dev(dC), ops.to_dev(B), ops.to_dev(off), bm=bm))
+        clean = np.ones((55, 136), dtype=bool)
+        clean[7] = False
+        clean[20:50, 9] = False
+        assert np.isfinite(got[:55][clean]).all()
+        assert not np.isfinite(got[7]).any()
+        assert np.isnan(got[20:50, 9]).all()
+
+
+def _swiglu_case(gg, sizes, K, N, bm, seed, with_h, gate_scale=2.0, spare=2, in_place=False):
+    rng = np.random.default_rng(seed)
+    off = ops.offsets_of(sizes)
+    M = int(off[-1])
+    dY, B = ops.bits(rng, M + spare, N, scale=0.5), ops.bits(rng, len(sizes), K, N, scale=0.2)
+    C = ops.bits(rng, M + spare, 2 * K, scale=gate_scale)
+    tC = ops.to_dev(C)
+    nan = float("nan")
+    out = tC if in_place else torch.full((M + spare, 2 * K), nan, dtype=torch.bfloat16, device="cuda:0")
+    h = torch.full((M + spare, K), nan, dtype=torch.bfloat16, device="cuda:0") if with_h else None
+    gg.grouped_gemm_dgrad_swiglu(ops.to_dev(dY), ops.to_dev(B), ops.to_dev(off), tC, out=out, out_h=h,
+                                 bm=bm)
+    c64 = oracle._bf16_to_f64(C)[:M]
+    dh, S = ref.dgrad(dY, B, off)
+    dh, dh_err = dh[:M], ops.sum_bound(N, S[:M])
+    want, want_h = ref.swiglu_grad(dh, c64)
+    err, err_h = ref.swiglu_grad_error(dh, dh_err, c64)
+    got = ops.host(out)
+    what = "dgrad_swiglu %s K=%d N=%d bm=%d" % (sizes, K, N, bm)
+    ops.check_bf16(got[:M], want, err, what)
+    if in_place:
+        assert (ops.bits_of(out)[M:] == C[M:]).all()
+    else:
+        assert np.isnan(got[M:]).all()
+    if with_h:
+        gh = ops.host(h)
+        ops.check_bf16(gh[:M], want_h, err_h, what + " H")
+        assert np.isnan(gh[M:]).all()
+
+
+@pytest.mark.parametrize("bm", BMS)
+@pytest.mark.parametrize("sizes,K,N", SHAPES)
+def test_dgrad_swiglu(gg, sizes, K, N, bm):
+    _swiglu_case(gg, sizes, K, N, bm, 200, True)
+
+
+@pytest.mark.parametrize("bm", [0, 16, 128, 256])
+def test_dgrad_swiglu_without_h_and_in_place(gg, bm):
+    _swiglu_case(gg, [3, 0, 150, 40], 296, 104, bm, 201, False)
+    _swiglu_case(gg, [3, 0, 150, 40], 296, 104, bm, 202, True, in_place=True)
+
+
+def test_dgrad_swiglu_large_gates(gg):
+    # gates out to +-200: e^-gate overflows, sigmoid is 0 or 1
+    _swiglu_case(gg, [70, 9], 128, 64, 0, 203, True, gate_scale=60.0)
+
+
+def test_dgrad_swiglu_differences(gg):
+    # the gradient against central differences of sum(dH * silu(gate) * up) in
+    # binary64; K = N with identity weights, so that dH = dY
+    rng = np.random.default_rng(9)
+    M, I = 12, 64
+    C, dY = ops.bits(rng, M, 2 * I, scale=1.5), ops.bits(rng, M, I)
+    eye = wl.f32_to_bf16_bits(np.eye(I, dtype=np.float32))[None]
+    got = ops.host(gg.grouped_gemm_dgrad_swiglu(ops.to_dev(dY), ops.to_dev(eye),
+                                                ops.to_dev(ops.offsets_of([M])), ops.to_dev(C)))
+    c, d = oracle._bf16_to_f64(C), oracle._bf16_to_f64(dY)
+    loss = lambda x: d * oracle.swiglu_pairs(x)  # noqa: E731
+    h = 2.0 ** -14
+    for which in (0, 1):
+        step = np.zeros_like(c)
+        step[:, which::2] = h
+        diff = (loss(c + step) - loss(c - step)) / (2 * h)
+        # the third derivative times h^2 / 6 (|silu'''| < 1), the cancellation in
+        # binary64, and the rounding to bf16
+        err = np.abs(d) * np.maximum(np.abs(c[:, 1::2]), 1) * h * h + 1e-10 + 2.0 ** -8 * np.abs(diff)
+        assert (np.abs(got[:, which::2] - diff) <= err + 2.0 ** -22).all()
+
+
+def _wgrad_case(gg, sizes, K, N, out, seed, spare=3, draw=ops.bits, accumulate=False, A=None, dC=None):
+    rng = np.random.default_rng(seed)
+    off = ops.offsets_of(sizes)
+    M = int(off[-1])
+    A = draw(rng, M + spare, K) if A is None else A
+    dC = draw(rng, M + spare, N) if dC is None else dC
+    old = rng.standard_normal((len(sizes), K, N)).astype(np.float32)
+    got = ops.to_dev(old) if accumulate else torch.full((len(sizes), K, N), float("nan"), dtype=_dt(out),
+                                                        device="cuda:0")
+    gg.grouped_gemm_wgrad(ops.to_dev(A), ops.to_dev(dC), ops.to_dev(off), out=got, accumulate=accumulate)
+    want, S = ref.wgrad(A, dC, off)
+    n = np.asarray(sizes)[:, None, None]
+    err = ops.sum_bound(n, S)
+    if accumulate:
+        want = want + old
+        err = err + ops.ULP * (np.abs(want) + err)
+        err[np.asarray(sizes) == 0] = 0
+    return ops.host(got), want, err
+
+
+# K and N below, at and past the tiles' 64, 128 and 256; enough experts for the
+# large tiles in the last ones; row counts around the slices' 32
+WSHAPES = [([0, 1, 17, 130, 0, 300], 328, 392), ([5], 8, 8), ([1], 136, 72), ([31, 32, 33, 64, 65], 200, 264),
+           ([97], 1032, 16), ([3, 0, 40, 7] * 16, 264, 520), ([0] * 70 + [50, 1], 256, 776)]
+
+
+@pytest.mark.parametrize("out", DTYPES)
+@pytest.mark.parametrize("sizes,K,N", WSHAPES)
+def test_wgrad(gg, sizes, K, N, out):
+    got, want, err = _wgrad_case(gg, sizes, K, N, out, 300)
+    _check(out, got, want, err, "wgrad %s K=%d N=%d %s" % (sizes[:8], K, N, out))
+    for e, m in enumerate(sizes):
+        if m == 0:
+            assert (got[e] == 0).all()
+
+
+@pytest.mark.parametrize("sizes,K,N", WSHAPES)
+def test_wgrad_accumulate(gg, sizes, K, N):
+    got, want, err = _wgrad_case(gg, sizes, K, N, "fp32", 301, accumulate=True)
+    ops.check_f32(got, want, err, "wgrad accumulate")
+
+
+@pytest.mark.parametrize("sizes,K,N", [([5, 0, 40, 129, 16], 264, 512), ([9, 60, 0, 33] * 20, 256, 520)])
+def test_wgrad_integers_are_exact(gg, sizes, K, N):
+    got, want, _ = _wgrad_case(gg, sizes, K, N, "fp32", 302, draw=ops.int_bits)
+    assert (got == want).all()
+
+
+def test_wgrad_many_experts_and_ties(gg):
+    # 1024 experts of 0 .. 40 rows: the order by size has ties everywhere
+    rng = np.random.default_rng(5)
+    sizes = rng.integers(0, 41, size=1024).tolist()
+    got, want, _ = _wgrad_case(gg, sizes, 24, 40, "fp32", 303, draw=ops.int_bits)
+    assert (got == want).all()
+    got, want, _ = _wgrad_case(gg, sizes[:130], 264, 520, "fp32", 304, draw=ops.int_bits)
+    assert (got == want).all()
+
+
+def test_wgrad_neighbours_rows_stay_out(gg):
+    # NaN in an expert's rows reaches that expert's gradient only
+    rng = np.random.default_rng(6)
+    for sizes, K, N in (([20, 30, 5], 136, 200), ([20, 30, 5] * 30, 256, 264)):
+        off = ops.offsets_of(sizes)
+        A, dC = ops.bits(rng, int(off[-1]) + 4, K), ops.bits(rng, int(off[-1]) + 4, N)
+        A[off[-1]:] = 0x7FC0
+        dC[off[-1]:] = 0x7F80
+        A[off[1]:off[2]] = 0x7FC0
+        got = ops.host(gg.grouped_gemm_wgrad(ops.to_dev(A), ops.to_dev(dC), ops.to_dev(off)))
+        assert np.isnan(got[1]).all()
+        assert np.isfinite(np.delete(got, 1, axis=0)).all()
+
+
+def test_wgrad_no_rows_at_all(gg):
+    off = torch.zeros(4, dtype=torch.int32, device="cuda:0")
+    A = torch.empty((0, 72), dtype=torch.bfloat16, device="cuda:0")
+    dC = torch.empty((0, 40), dtype=torch.bfloat16, device="cuda:0")
+    got = torch.full((3, 72, 40), float("nan"), device="cuda:0")
+    gg.grouped_gemm_wgrad(A, dC, off, out=got)
+    assert (got == 0).all()
+
+
+def test_same_bits_twice(gg):
+    rng = np.random.default_rng(8)
+    off = ops.to_dev(ops.offsets_of([40, 300, 0, 7]))
+    A, dC = ops.to_dev(ops.bits(rng, 347, 264)), ops.to_dev(ops.bits(rng, 347, 392))
+    B = ops.to_dev(ops.bits(rng, 4, 264, 392))
+    for f in (lambda: gg.grouped_gemm_wgrad(A, dC, off), lambda: gg.grouped_gemm_dgrad(dC, B, off)):
+        assert torch.equal(f(), f())
+
+
+@pytest.mark.parametrize("offs", [[0, 9, 4, 30], [-5, 10, 20, 30], [0, 10, 99, 30], [7, 7, 7, 7],
+                                  [30, 20, 10, 0]])
+def test_malformed_offsets_stay_inside(gg, offs):
+    # clamped offsets; what is written lies inside the arrays, guarded on both sides
+    rng = np.random.default_rng(10)
+    M, K, N = 30, 72, 136
+    dC, A, B = ops.bits(rng, M, N), ops.bits(rng, M, K), ops.bits(rng, 3, K, N)
+    off = torch.tensor(offs, dtype=torch.int32, device="cuda:0")
+
+    def guarded(rows, cols):
+        buf = torch.full((rows + 64, cols), -7.0, device="cuda:0")
+        return buf, buf[32:32 + rows]
+
+    for bm in (0, 16, 256):
+        buf, out = guarded(M, K)
+        gg.grouped_gemm_dgrad(ops.to_dev(dC), ops.to_dev(B), off, out=out, bm=bm)
+        assert (buf[:32] == -7).all() and (buf[-32:] == -7).all()
+    buf, out = guarded(3 * K, N)
+    gg.grouped_gemm_wgrad(ops.to_dev(A), ops.to_dev(dC), off, out=out.view(3, K, N))
+    assert (buf[:32] == -7).all() and (buf[-32:] == -7).all() and torch.isfinite(out).all()
+
+
+def test_training_step_of_a_layer(gg):
+    # an expert layer's forward and backward by these operators alone, against
+    # binary64 autograd: loss = sum(Y * W)
+    rng = np.random.default_rng(11)
+    sizes, D, I = [37, 0, 70, 1, 21], 136, 72
+    off = ops.offsets_of(sizes)
+    M, E = int(off[-1]), len(sizes)
+    X, W = ops.bits(rng, M, D), ops.bits(rng, M, D)
+    B1, B2 = ops.bits(rng, E, D, 2 * I, scale=D ** -0.5), ops.bits(rng, E, I, D, scale=I ** -0.5)
+    tX, tdY, tB1, tB2, toff = (ops.to_dev(t) for t in (X, W, B1, B2, off))
+
+    C = gg.grouped_gemm(tX, tB1, toff, out_dtype=torch.bfloat16)
+    dC, H = gg.grouped_gemm_dgrad_swiglu(tdY, tB2, toff, C, with_h=True)
+    dB2 = gg.grouped_gemm_wgrad(H, tdY, toff)
+    dX = gg.grouped_gemm_dgrad(dC, tB1, toff)
+    dB1 = gg.grouped_gemm_wgrad(tX, dC, toff)
+
+    leaf = lambda b: torch.from_numpy(oracle._bf16_to_f64(b)).requires_grad_()  # noqa: E731
+    x, b1, b2 = leaf(X), leaf(B1), leaf(B2)
+    w = torch.from_numpy(oracle._bf16_to_f64(W))
+    loss = 0.0
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        c = x[lo:hi] @ b1[e]
+        h = torch.nn.functional.silu(c[:, 0::2]) * c[:, 1::2]
+        loss = loss + (h @ b2[e] * w[lo:hi]).sum()
+    loss.backward()
+    # Roundings to bf16 on the way, each of at most 2^-8 of the value: gate, up,
+    # the gradient of either, H.
+    for got, want in ((dX, x.grad), (dB1, b1.grad), (dB2, b2.grad)):
+        want = want.numpy()
+        rel = np.linalg.norm(ops.host(got) - want) / np.linalg.norm(want)
+        assert rel < 4 * 2.0 ** -8, rel
+
+
+def test_graph_replays_follow_the_offsets(gg):
+    # captured once, replayed on other rows, weights and group sizes
+    rng = np.random.default_rng(12)
+    K, N, M = 136, 264, 96
+    sets = [([90, 0, 6], 1), ([0, 96, 0], 2), ([30, 31, 35], 3)]
+    A, dC = (torch.zeros((M, c), dtype=torch.bfloat16, device="cuda:0") for c in (K, N))
+    B = torch.zeros((3, K, N), dtype=torch.bfloat16, device="cuda:0")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda:0")
+    C = torch.zeros((M, 2 * K), dtype=torch.bfloat16, device="cuda:0")
+
+    def step():
+        return (gg.grouped_gemm_dgrad(dC, B, off), gg.grouped_gemm_wgrad(A, dC, off),
+                *gg.grouped_gemm_dgrad_swiglu(dC, B, off, C, with_h=True))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for sizes, seed in sets * 2:
+        r = np.random.default_rng(seed)
+        A.copy_(ops.to_dev(ops.bits(r, M, K)))
+        dC.copy_(ops.to_dev(ops.bits(r, M, N)))
+        B.copy_(ops.to_dev(ops.bits(r, 3, K, N)))
+        C.copy_(ops.to_dev(ops.bits(r, M, 2 * K)))
+        off.copy_(ops.to_dev(ops.offsets_of(sizes)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(outs, step()):
+            assert torch.equal(got, want)
+
+
+def test_other_stream(gg):
+    rng = np.random.default_rng(13)
+    off = ops.to_dev(ops.offsets_of([50, 14]))
+    A, dC = ops.to_dev(ops.bits(rng, 64, 136)), ops.to_dev(ops.bits(rng, 64, 264))
+    B = ops.to_dev(ops.bits(rng, 2, 136, 264))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    on_s = [gg.grouped_gemm_dgrad(dC, B, off, stream=s), gg.grouped_gemm_wgrad(A, dC, off, stream=s)]
+    s.synchronize()
+    for got, want in zip(on_s, (gg.grouped_gemm_dgrad(dC, B, off), gg.grouped_gemm_wgrad(A, dC, off))):
+        assert torch.equal(got, want)

@@ -1,0 +1,243 @@
+"""The gradients and the 4-bit operators without a GPU: their references, the
+host checks of the C entry points, the binding's refusals and the build.
+
+No call below reaches the HIP runtime: each is rejected by the host checks, or
+has nothing to do.
+"""
+
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import moe_ragged_grouped_amd as gg
+import moe_ragged_grouped_amd.build as hb
+import oracle
+import oracle.operators as ref
+import workloads as wl
+from tests import operators as ops
+
+INVALID, MISALIGNED, UNSUPPORTED = 1, 2, 3
+
+
+# ---------------------------------------------------------------- references
+
+def _layer(rng, sizes, K, N):
+    off = ops.offsets_of(sizes)
+    M = int(off[-1])
+    return off, ops.bits(rng, M, K), ops.bits(rng, len(sizes), K, N), ops.bits(rng, M, N)
+
+
+def test_gradient_references_against_autograd():
+    rng = np.random.default_rng(0)
+    off, A, B, dC = _layer(rng, [3, 0, 5], 16, 24)
+    a = torch.from_numpy(oracle._bf16_to_f64(A)).requires_grad_()
+    b = torch.from_numpy(oracle._bf16_to_f64(B)).requires_grad_()
+    c = torch.cat([a[off[e]:off[e + 1]] @ b[e] for e in range(3)])
+    c.backward(torch.from_numpy(oracle._bf16_to_f64(dC)))
+    np.testing.assert_allclose(ref.dgrad(dC, B, off)[0], a.grad.numpy(), rtol=1e-12, atol=1e-12)
+    np.testing.assert_allclose(ref.wgrad(A, dC, off)[0], b.grad.numpy(), rtol=1e-12, atol=1e-12)
+    assert (ref.wgrad(A, dC, off)[0][1] == 0).all()
+
+
+def test_swiglu_reference_against_autograd():
+    rng = np.random.default_rng(1)
+    C = rng.standard_normal((7, 24)) * 3
+    dH = rng.standard_normal((7, 12))
+    c = torch.from_numpy(C).requires_grad_()
+    h = torch.nn.functional.silu(c[:, 0::2]) * c[:, 1::2]
+    h.backward(torch.from_numpy(dH))
+    d, H = ref.swiglu_grad(dH, C)
+    np.testing.assert_allclose(d, c.grad.numpy(), rtol=1e-12, atol=1e-12)
+    np.testing.assert_allclose(H, h.detach().numpy(), rtol=1e-12)
+
+
+def test_swiglu_error_bound_covers_a_float32_evaluation():
+    rng = np.random.default_rng(2)
+    C = (rng.standard_normal((400, 64)) * 20).astype(np.float32)
+    dH = rng.standard_normal((400, 32)).astype(np.float32)
+    f = np.float32
+    g, u = C[:, 0::2], C[:, 1::2]
+    with np.errstate(over="ignore"):
+        s = f(1) / (f(1) + np.exp2(-g * f(1.4426950408889634)))
+    got = np.stack([dH * u * (s * (f(1) + g * (f(1) - s))), dH * (g * s)], axis=-1).reshape(C.shape)
+    want, H = ref.swiglu_grad(dH.astype(np.float64), C.astype(np.float64))
+    err, err_h = ref.swiglu_grad_error(dH.astype(np.float64), 0.0, C.astype(np.float64))
+    assert (np.abs(got - want) <= err).all()
+    assert (np.abs(g * s * u - H) <= err_h).all()
+
+
+def test_mx4_reference_by_hand():
+    x = np.zeros((1, 64), dtype=np.float32)
+    x[0, :6] = [4.0, 2.5, -0.75, 7.0, 0.25, -0.0]  # scale 1
+    x[0, 32:35] = [0.75, 0.09375, 0.046875]        # maximum in [1/2, 1): scale 1/8
+    q, s = ref.mx4_encode(wl.f32_to_bf16_bits(x))
+    assert q.shape == (1, 32) and s.shape == (1, 1, 8)
+    assert s[0, 0].tolist() == [127, 124, 0, 0, 0, 0, 0, 0]
+    assert q[0, :3].tolist() == [6 | 4 << 4, 10 | 7 << 4, 0 | 8 << 4]
+    assert q[0, 16:18].tolist() == [7 | 2 << 4, 1]  # 6, .75 -> 1 (tie to even), .375 -> .5
+    v = ref.mx4_values(q, s)
+    assert v[0, :6].tolist() == [4, 2, -1, 6, 0, 0] and v[0, 32:35].tolist() == [0.75, 0.125, 0.0625]
+
+
+def test_mx4_reference_is_the_nearest_value():
+    rng = np.random.default_rng(3)
+    x = ops.bits(rng, 40, 96)
+    q, s = ref.mx4_encode(x)
+    v, t = oracle._bf16_to_f64(x).reshape(40, 3, 32), ref.mx4_values(q, s).reshape(40, 3, 32)
+    scale = np.ldexp(1.0, s[0, :, :3].astype(int) - 127)[..., None]
+    top = np.abs(v).max(-1, keepdims=True)
+    assert ((4 * scale <= top) & (top < 8 * scale)).all()
+    grid = np.concatenate([ref.E2M1, -ref.E2M1]) * scale[..., None]
+    nearest = np.abs(v[..., None] - grid).min(-1)
+    assert (np.abs(v - t) == nearest).all()
+
+
+# ------------------------------------------------------------- host checks
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(gg.library_path()):
+        hb.build()
+    return gg.load_library()
+
+
+ROW = dict(E=4, K=256, N=256, M_cap=29)
+ENTRIES = {
+    "gg_grouped_gemm_bf16_dgrad": dict(dC=16, B=32, off=64, dA=128, **ROW, bm=0),
+    "gg_grouped_gemm_bf16_dgrad_bf16out": dict(dC=16, B=32, off=64, dA=128, **ROW, bm=0),
+    "gg_grouped_gemm_bf16_dgrad_swiglu": dict(dC=16, B=32, off=64, C=80, dA=128, H=144, **ROW, bm=0),
+    "gg_grouped_gemm_bf16_wgrad": dict(A=16, dC=32, off=64, dB=128, acc=0, **ROW),
+    "gg_grouped_gemm_bf16_wgrad_bf16out": dict(A=16, dC=32, off=64, dB=128, **ROW),
+    "gg_grouped_gemm_mx4": dict(Aq=16, a_scale=32, Bq=48, b_scale=64, off=80, C=128, **ROW, bm=0),
+    "gg_grouped_gemm_mx4_bf16out": dict(Aq=16, a_scale=32, Bq=48, b_scale=64, off=80, C=128, **ROW, bm=0),
+    "gg_grouped_gemm_mx4_swiglu": dict(Aq=16, a_scale=32, Bq=48, b_scale=64, off=80, C=128, **ROW, bm=0),
+}
+
+
+def _status(lib, entry, **kw):
+    # fake, aligned addresses: every call is rejected on the host
+    args = dict(ENTRIES[entry])
+    args.update(kw)
+    return getattr(lib, entry)(*args.values(), None)
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_host_checks(lib, entry):
+    good = ENTRIES[entry]
+    for name in good:
+        if name in ("E", "K", "N", "M_cap", "bm", "acc", "H"):
+            continue
+        assert _status(lib, entry, **{name: 0}) == INVALID, name
+        assert _status(lib, entry, **{name: good[name] + 2}) == MISALIGNED, name
+        if name != "off":
+            assert _status(lib, entry, **{name: good[name] + 8}) == MISALIGNED, name
+    for kw in (dict(E=0), dict(E=-1), dict(K=0), dict(K=-8), dict(N=0), dict(M_cap=-1)):
+        assert _status(lib, entry, **kw) == INVALID, kw
+    for kw in (dict(E=1025), dict(M_cap=2 ** 31 - 100), dict(K=2 ** 24 + 256), dict(N=2 ** 24 + 256)):
+        assert _status(lib, entry, **kw) == UNSUPPORTED, kw
+    assert _status(lib, entry, N=100) == MISALIGNED
+    assert _status(lib, entry, K=100) == MISALIGNED
+    if "mx4" in entry:
+        assert _status(lib, entry, K=264) == MISALIGNED
+        assert _status(lib, entry, K=2 ** 22 + 32) == UNSUPPORTED
+    if "H" in good:
+        assert _status(lib, entry, H=136) == MISALIGNED
+    if "dgrad" in entry:
+        assert _status(lib, entry, N=2 ** 21 + 8) == UNSUPPORTED
+    if "wgrad" in entry:
+        assert _status(lib, entry, K=2 ** 22 + 8) == UNSUPPORTED
+        assert _status(lib, entry, N=2 ** 22 + 8) == UNSUPPORTED
+        assert _status(lib, entry, E=1024, K=2 ** 22, N=2 ** 22) == UNSUPPORTED  # tiles beyond the grid
+    else:
+        for bm in (8, 48, 512, -16):
+            assert _status(lib, entry, bm=bm) == INVALID
+        rows = {n: 0 for n in ("dC", "dA", "C", "H", "Aq", "a_scale") if n in good}
+        assert _status(lib, entry, M_cap=0) == 0
+        assert _status(lib, entry, M_cap=0, **rows) == 0, "arrays of no rows may be null"
+
+
+def test_mx4_row_host_checks(lib):
+    q = lambda X=16, c=32, s=48, rows=3, K=64: lib.gg_mx4_quantize(X, c, s, rows, K, None)  # noqa: E731
+    assert q(X=0) == q(c=0) == q(s=0) == q(rows=-1) == q(K=0) == INVALID
+    assert q(X=24) == q(c=40) == q(s=52) == q(K=40) == MISALIGNED
+    assert q(rows=2 ** 31) == q(K=2 ** 22 + 32) == q(rows=2 ** 31 - 1, K=2 ** 22) == UNSUPPORTED
+    assert q(rows=0) == q(rows=0, X=0, c=0, s=0) == 0
+    w = lambda B=16, c=32, s=48, E=2, K=64, N=8: lib.gg_mx4_quantize_weights(B, c, s, E, K, N, None)  # noqa: E731
+    assert w(B=0) == w(c=0) == w(s=0) == w(E=0) == w(K=0) == w(N=-8) == INVALID
+    assert w(B=24) == w(c=40) == w(s=52) == w(K=40) == w(N=12) == MISALIGNED
+    assert w(E=1025) == w(K=2 ** 22 + 32) == w(N=65535 * 256 + 8) == UNSUPPORTED
+    d = lambda c=16, s=32, Y=48, b=2, rows=3, K=64: lib.gg_mx4_dequantize(c, s, Y, b, rows, K, None)  # noqa: E731
+    assert d(c=0) == d(s=0) == d(Y=0) == d(b=-1) == d(rows=-1) == d(K=0) == INVALID
+    assert d(c=24) == d(s=40) == d(Y=56) == d(K=40) == MISALIGNED
+    assert d(b=65536) == d(rows=2 ** 31) == UNSUPPORTED
+    assert d(b=0) == d(rows=0) == 0
+
+
+# ------------------------------------------------------------ the binding
+
+def _bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def _u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+OFF = torch.zeros(3, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: gg.grouped_gemm_dgrad(torch.zeros(4, 8), _bf(2, 16, 8), OFF),
+    lambda: gg.grouped_gemm_dgrad(_bf(4, 8), _bf(2, 16, 8), OFF.long()),
+    lambda: gg.grouped_gemm_dgrad_swiglu(_bf(4, 8), _bf(2, 16, 8), OFF, torch.zeros(4, 32)),
+    lambda: gg.grouped_gemm_wgrad(_bf(4, 8), torch.zeros(4, 8), OFF),
+    lambda: gg.mx4_quantize(torch.zeros(4, 32)),
+    lambda: gg.mx4_quantize_weights(torch.zeros(1, 32, 8)),
+    lambda: gg.mx4_dequantize(torch.zeros(4, 16), _u8(1, 4, 8)),
+    lambda: gg.grouped_gemm_mx4(_u8(4, 16), _u8(1, 4, 8), _u8(2, 8, 16), _u8(2, 1, 8, 8).float(), OFF),
+])
+def test_wrong_types_are_refused(call):
+    with pytest.raises(TypeError):
+        call()
+
+
+@pytest.mark.parametrize("call", [
+    lambda: gg.grouped_gemm_dgrad(_bf(4, 8), _bf(2, 16, 8), OFF),
+    lambda: gg.grouped_gemm_dgrad(_bf(4), _bf(2, 16, 8), OFF),
+    lambda: gg.grouped_gemm_wgrad(_bf(4, 8), _bf(4, 8), OFF),
+    lambda: gg.mx4_quantize(_bf(4, 32)),
+    lambda: gg.mx4_dequantize(_u8(16), _u8(1, 8)),
+    lambda: gg.grouped_gemm_mx4_swiglu(_u8(4, 16), _u8(1, 4, 8), _u8(2, 8, 16), _u8(2, 1, 8, 8), OFF),
+])
+def test_host_tensors_and_wrong_ranks_are_refused(call):
+    with pytest.raises(ValueError):
+        call()
+
+
+# --------------------------------------------------------------- the build
+
+@pytest.mark.skipif(not os.path.exists(hb.HIPCC), reason="hipcc not available")
+@pytest.mark.parametrize("source", hb.OPERATOR_SOURCES, ids=os.path.basename)
+def test_kernels_neither_spill_nor_use_scratch(source):
+    cmd = [hb.HIPCC, *[f for f in hb.FLAGS if f != "-shared"], "--offload-device-only", "-c",
+           "-Rpass-analysis=kernel-resource-usage", "-o", os.devnull, source]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    kernels, cur = {}, None
+    for line in r.stderr.splitlines():
+        m = re.search(r"Function Name: (\S+)", line)
+        if m:
+            cur = kernels.setdefault(m.group(1), {})
+        m = re.search(r"remark:\s+([A-Za-z /\[\]]+?):\s+(\d+)", line)
+        if m and cur is not None:
+            cur[m.group(1).strip()] = int(m.group(2))
+    assert kernels
+    for name, u in kernels.items():
+        assert u["VGPRs Spill"] == 0 and u["ScratchSize [bytes/lane]"] == 0, (name, u)
+        # a few scalars kept in spare vector lanes, never in memory
+        assert u["SGPRs Spill"] <= 16, (name, u)
+        assert u["Occupancy [waves/SIMD]"] >= 2, (name, u)
