@@ -21,18 +21,20 @@ inline bool valid_bm(int bm) {
   return bm == 0 || bm == 16 || bm == 32 || bm == 64 || bm == 128 || bm == 256;
 }
 
-// Groups, rows and tile height; the upper bound of the tile count of a
-// product with `cols` output columns (narrowest tiles: `narrow` columns).
+// Groups, rows and tile height; upper bounds of the row tiles and of the tiles
+// of a product with `cols` output columns (narrowest tiles: `narrow` columns).
 inline gg_status_t check_groups(const int32_t *off, int E, int cols, int M_cap, int bm, int narrow,
-                                long long *bound) {
+                                int *row_tiles, long long *tiles) {
   if (off == nullptr || E < 1 || cols < 1 || M_cap < 0 || !valid_bm(bm)) return GG_ERR_INVALID_VALUE;
   if (E > kMaxExperts) return GG_ERR_UNSUPPORTED;
   if (!is_aligned(off, 4)) return GG_ERR_MISALIGNED;
   const long long hmin = bm ? bm : 16;
-  const long long b = ((long long)M_cap / hmin + E) * ((cols + (long long)narrow - 1) / narrow);
+  const long long m = (long long)M_cap / hmin + E;
+  const long long b = m * ((cols + (long long)narrow - 1) / narrow);
   // tile ids and rows + tile height must stay inside int32
   if (b > (1LL << 28) || (long long)M_cap + 256 > INT32_MAX) return GG_ERR_UNSUPPORTED;
-  *bound = b;
+  *row_tiles = (int)m;
+  *tiles = b;
   return GG_OK;
 }
 
@@ -41,6 +43,11 @@ inline gg_status_t check_groups(const int32_t *off, int E, int cols, int M_cap, 
 struct RingLaunch {
   int grid = 0;
   hipError_t err = hipSuccess;
+  // workgroups for at most `tiles` tiles: a multiple of the XCD count
+  int workgroups(long long tiles) const {
+    const long long g = tiles < grid ? tiles : grid;
+    return (int)((g + kRingXcds - 1) / kRingXcds * kRingXcds);
+  }
 };
 
 template <auto Kernel>

@@ -17,7 +17,11 @@
 //    as many slices in flight as LDS has room for. A lane out of the buffer's
 //    range writes zeros (checked by an in-bounds probe), which is the zero
 //    fill of padding rows, of columns past the end and of the last slice's
-//    tail.
+//    tail. Measured alone (8 x 1 KB a wave, two 64 KB groups in flight): 148
+//    bytes a ns and CU out of L2, 88 streaming on a quarter of the CUs, 6.1
+//    TB/s streaming on all; the swizzle below and the row pitch cost nothing,
+//    but a pitch that is no multiple of 128 makes every row's piece touch two
+//    lines.
 //  * The instruction writes lane l's 16 bytes at base + 16 l, so a swizzle has
 //    to be put into the global side: lane l of a wave's 8 x 128-byte piece
 //    loads row l / 8, chunk (l % 8) ^ (l / 8), and chunk c of row r then sits
@@ -26,6 +30,8 @@
 //  * S stages, one barrier a slice: the barrier that says "slice i has landed"
 //    also says "every wave is done with slice i - 1", whose stage is refilled
 //    at once with slice i + S - 1.
+//  * A persistent workgroup starts the next tile's first slices as soon as its
+//    last LDS read is done, before it stores the present tile.
 #pragma once
 
 #include "gg_common.h"
@@ -38,6 +44,8 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) u32x4 gbl_u32x4;
 typedef __attribute__((address_space(1))) u32x2 gbl_u32x2;
+
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // 16 bytes a lane, global -> LDS at dst + 16 * lane (dst is wave-uniform).
 template <int POLICY = kCacheDefault>
@@ -72,119 +80,125 @@ __device__ __forceinline__ void wg_barrier() {
 
 // ---------------------------------------------------------------- schedule
 //
-// The tile list of gg_schedule.h with one change: where every expert's tiles
-// are 16 rows high (the launch only streams weights), the tile width follows
-// from the number of tiles. Wide tiles move longer runs per barrier, but a
-// launch of a few tokens has too few of them to occupy the chip, so the
-// widest of 512, 256 and 128 columns is taken that still gives every
-// workgroup of the launch a tile.
+// The tile list of gg_schedule.h (expert by expert, heights by adaptive_bm or
+// fixed by the caller) with one width for the launch. A launch of few tiles
+// leaves CUs idle, and narrower tiles then finish sooner although they fetch A
+// more often. With T(w) tiles of width w on G workgroups and H the tallest
+// height, the width is the one with the smallest
+//   ceil(T(w) / G) * (H + w + 96),
+// rounds times the bytes of a slice plus a fixed share for what a tile repeats
+// whatever its size; the wider one at a tie.
 struct RingSched {
-  int start[kMaxExperts + 1];
-  long long wave_sum[kThreads / kWave];
-  int wave_tall[kThreads / kWave];
-  int width16;
+  int start[kMaxExperts + 1];  // exclusive prefix of row tiles per expert
+  int wave_tiles[kThreads / kWave];
+  int wave_tallest[kThreads / kWave];
 };
 
-constexpr int kNarrowN = 128;
+constexpr int kNarrowestN = 64;
 
-__device__ __forceinline__ int build_ring_schedule(RingSched &s, const int32_t *__restrict__ off_g, int E,
-                                          int M_cap, int N, int bm_fixed, int tile_cap, int G) {
+struct RingGrid {
+  int total;  // tiles of the launch
+  int width;  // columns of each
+};
+
+// All threads of the workgroup must call this. tile_cap: the host's bound of
+// row tiles; overlapping (malformed) groups that exceed it schedule nothing.
+__device__ __forceinline__ RingGrid build_ring_schedule(RingSched &s,
+                                                        const int32_t *__restrict__ off_g, int E,
+                                                        int M_cap, int N, int bm_fixed,
+                                                        int tile_cap, int G) {
   const int tid = threadIdx.x;
   constexpr int kRun = kMaxExperts / kThreads;
   const int e0 = tid * kRun;
-  int rows[kRun], height[kRun];
-  int tall = 0;
-  long long m16 = 0;  // 16-row tiles of this run, a column apart
+  int cnt[kRun], local = 0, tallest = 16;
   int lo = e0 < E ? clamp_off(off_g, e0, M_cap) : 0;
 #pragma unroll
   for (int j = 0; j < kRun; ++j) {
     const int e = e0 + j;
-    rows[j] = 0;
-    height[j] = 16;
+    cnt[j] = 0;
     if (e < E) {
       const int hi = clamp_off(off_g, e + 1, M_cap);
-      rows[j] = hi > lo ? hi - lo : 0;
-      height[j] = bm_fixed ? bm_fixed : adaptive_bm(rows[j]);
-      tall |= rows[j] > 0 && height[j] > 16;
-      m16 += cdiv(rows[j], 16);
+      const int rows = max(hi - lo, 0);
+      const int h = bm_fixed ? bm_fixed : adaptive_bm(rows);
+      cnt[j] = cdiv(rows, h);
+      if (rows > 0) tallest = max(tallest, h);
+      local += cnt[j];
       lo = hi;
     }
   }
+  // Counts are below 2^27 a thread and 2^31 / 16 a group, so a wave's sum may
+  // pass 32 bits only for malformed offsets: sums saturate far above any
+  // tile_cap instead (a group counts at most 2^27 tiles, tile_cap is at most
+  // 2^28).
+  constexpr int kMost = 1 << 29;
   const int lane = tid % kWave, wave = tid / kWave;
-  const bool any = __any(tall);
-#pragma unroll
-  for (int d = kWave / 2; d > 0; d /= 2) m16 += __shfl_xor(m16, d, kWave);
-  if (lane == 0) {
-    s.wave_tall[wave] = any;
-    s.wave_sum[wave] = m16;
-  }
-  __syncthreads();
-  bool any_tall = false;
-  long long all16 = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / kWave; ++w) {
-    any_tall |= s.wave_tall[w] != 0;
-    all16 += s.wave_sum[w];
-  }
-  int width16 = kTileN;
-  if (!any_tall)
-    width16 = all16 * cdiv(N, kWideN) >= G ? kWideN : (all16 * cdiv(N, kTileN) >= G ? kTileN : kNarrowN);
-  __syncthreads();  // wave_sum is written again below
-  long long cnt[kRun];
-  long long local = 0;
-#pragma unroll
-  for (int j = 0; j < kRun; ++j) {
-    cnt[j] = rows[j] > 0 ? (long long)cdiv(rows[j], height[j]) *
-                               cdiv(N, height[j] == 16 ? width16 : kTileN)
-                         : 0;
-    local += cnt[j];
-  }
-  long long incl = local;
+  int incl = local;
 #pragma unroll
   for (int d = 1; d < kWave; d *= 2) {
-    const long long y = __shfl_up(incl, d, kWave);
-    if (lane >= d) incl += y;
+    const int y = __shfl_up(incl, d, kWave);
+    if (lane >= d) incl = min(incl + y, kMost);
+    tallest = max(tallest, __shfl_xor(tallest, d, kWave));
   }
-  if (lane == kWave - 1) s.wave_sum[wave] = incl;
+  if (lane == kWave - 1) {
+    s.wave_tiles[wave] = incl;
+    s.wave_tallest[wave] = tallest;
+  }
   __syncthreads();
-  long long before = 0, total = 0;
+  int before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / kWave; ++w) {
-    if (w < wave) before += s.wave_sum[w];
-    total += s.wave_sum[w];
+    if (w < wave) before = min(before + s.wave_tiles[w], kMost);
+    total = min(total + s.wave_tiles[w], kMost);
+    tallest = max(tallest, s.wave_tallest[w]);
   }
-  if (total > tile_cap) total = 0;  // overlapping malformed segments: no tiles
-  long long run = before + incl - local;
+  if (total > tile_cap) total = 0;
+  int run = min(before + incl, kMost) - local;
 #pragma unroll
   for (int j = 0; j < kRun; ++j) {
     const int e = e0 + j;
-    if (e < E) s.start[e] = total ? (int)run : 0;
+    if (e < E) s.start[e] = total ? run : 0;
     run += cnt[j];
   }
-  if (tid == 0) {
-    s.start[E] = (int)total;
-    s.width16 = width16;
-  }
+  if (tid == 0) s.start[E] = total;
   __syncthreads();
-  return (int)total;
+  int best = kTileN;
+  long long best_cost = 0;
+#pragma unroll
+  for (int w = kTileN; w >= kNarrowestN; w /= 2) {
+    if (w < 128 && tallest == 16) break;  // eight waves side by side, 16 columns each
+    const long long tiles = (long long)total * cdiv(N, w);
+    const long long cost = (tiles + G - 1) / G * (tallest + w + 96);
+    if (w == kTileN || cost < best_cost) { best = w; best_cost = cost; }
+  }
+  // the host's bounds keep total * ceil(N / 64) within 31 bits
+  return RingGrid{scalar(total * cdiv(N, best)), scalar(best)};
 }
 
-// Tile t of the list (0 <= t < total).
-__device__ __forceinline__ Tile decode_ring_tile(const RingSched &s,
-                                                 const int32_t *__restrict__ off_g, int t, int E,
-                                                 int M_cap, int N, int bm_fixed) {
+// A device offset through the scalar cache: its wait does not count against
+// the loads and stores in flight.
+typedef __attribute__((address_space(4))) const int32_t cst_i32;
+__device__ __forceinline__ int clamp_off_s(const int32_t *off_g, int e, int M_cap) {
+  const int v = ((cst_i32 *)off_g)[e];
+  return min(max(v, 0), M_cap);
+}
+
+// Tile t of the list (0 <= t < total), wave-uniform.
+__device__ __forceinline__ Tile decode_ring_tile(const RingSched &s, const int32_t *off_g, int t,
+                                                 int E, int M_cap, int N, int bm_fixed, int bn) {
+  const int NT = cdiv(N, bn);
+  const int m_index = t / NT;  // row tiles lie in expert order, NT tiles each
   int lo = 0, hi = E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (s.start[mid] <= t) lo = mid; else hi = mid;
+    if (s.start[mid] <= m_index) lo = mid; else hi = mid;
   }
-  const int r0 = clamp_off(off_g, lo, M_cap);
-  const int m = clamp_off(off_g, lo + 1, M_cap) - r0;
+  lo = scalar(lo);
+  const int first = scalar(s.start[lo]);
+  const int r0 = clamp_off_s(off_g, lo, M_cap);
+  const int m = clamp_off_s(off_g, lo + 1, M_cap) - r0;
   const int b = bm_fixed ? bm_fixed : adaptive_bm(m);
-  const int bn = b == 16 ? s.width16 : kTileN;
-  const int NT = cdiv(N, bn);
   const int n_mt = cdiv(m, b);
-  const int local = t - s.start[lo];
+  const int local = t - first * NT;
   // groups of kGroupM M tiles; N outer, M inner inside a group
   const int per_group = kGroupM * NT;
   const int grp = local / per_group;
@@ -194,7 +208,8 @@ __device__ __forceinline__ Tile decode_ring_tile(const RingSched &s,
   const int mt = grp * kGroupM + (r - nt * gm);
   Tile tl;
   tl.expert = lo;
-  tl.bm = b;
+  // eight waves of 16 columns each do not fit 64: 32 rows, half of them padding
+  tl.bm = bn == 64 ? max(b, 32) : b;
   tl.bn = bn;
   tl.row0 = r0 + mt * b;
   tl.rows = min(b, m - mt * b);
@@ -205,112 +220,113 @@ __device__ __forceinline__ Tile decode_ring_tile(const RingSched &s,
 // ------------------------------------------------------------------- tiles
 
 constexpr int kRowBytes = 128;  // bytes of a row in one slice
+constexpr int kRingBytes = 155 * 1024;  // LDS for the stages (the schedule takes 4.2 KB more)
 
-// MX: 4-bit operands with a scale byte per 32 values, 8 of them per row and
-// slice, kept beside the slice they belong to.
-template <int BM_, int BN_, int WM_, int WN_, int S_, bool MX_>
+// Bytes of a stage: A's rows, B's rows, then (MX: 4-bit operands with a scale
+// byte per 32 values) 8 scale bytes per row of A and of B.
+__host__ __device__ constexpr int ring_stage(int BM, int BN, bool MX) {
+  return (BM + BN) * (kRowBytes + (MX ? 8 : 0));
+}
+// As many stages as fit, up to 6 (96 KB and more in flight).
+__host__ __device__ constexpr int ring_stages(int BM, int BN, bool MX) {
+  const int s = kRingBytes / ring_stage(BM, BN, MX);
+  return s < 6 ? s : 6;
+}
+
+template <int BM_, int BN_, int WM_, int WN_, bool MX_>
 struct RingCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr bool MX = MX_;
   static_assert(WM * WN == kThreads / kWave, "one wave per wave tile");
   static constexpr int WTM = BM / WM, WTN = BN / WN;
   static_assert(WTM % 16 == 0 && WTN % 16 == 0, "16x16 blocks");
   static constexpr int MI = WTM / 16, NI = WTN / 16;
   static constexpr int A_BYTES = BM * kRowBytes, B_BYTES = BN * kRowBytes;
-  static constexpr int AS_BYTES = MX ? BM * 8 : 0, BS_BYTES = MX ? BN * 8 : 0;
-  static constexpr int STAGE = A_BYTES + B_BYTES + AS_BYTES + BS_BYTES;
-  // Loads a wave issues per slice. Tiles of fewer than 64 rows use only the
-  // first BM lanes of one instruction, so that every wave issues the same
-  // number and waits on the same count.
-  static constexpr int A_INSTR = BM >= 64 ? BM / 64 : 1;
-  static constexpr int A_LANES = BM >= 64 ? 64 : BM;
-  static constexpr int B_INSTR = BN / 64;
-  static constexpr int LPS = A_INSTR + B_INSTR + (MX ? 1 : 0);
-  static constexpr int LDS_BYTES = S * STAGE;
+  static constexpr int STAGE = ring_stage(BM, BN, MX), S = ring_stages(BM, BN, MX);
+  // loads a wave issues per slice (ring_issue)
+  static constexpr int LPS = (BM >= 64 ? BM / 64 : 1) + BN / 64 + (MX ? 1 : 0);
   static_assert(S >= 2 && (S - 2) * LPS < 64, "loads in flight");
+  static_assert(S * STAGE <= kRingBytes, "LDS");
 };
 
 struct RingTile {
   const char *A;          // row 0 of the tile
   const char *B;          // weight row (output column) 0 of the tile
   const char *As, *Bs;    // MX: scale bytes of the first slice, row 0 / column 0
-  size_t as_step, bs_step;  // MX: bytes from a slice's scales to the next one's
+  uint64_t as_step, bs_step;  // MX: bytes from a slice's scales to the next one's
   uint32_t pitch;         // bytes of a row of A and of B
   int rows, ncols;        // valid rows and columns
-  int tid;
 };
 
-// Per-lane constants of a tile's loads. The chunk is the same for all of a
-// lane's loads (a row's place in its group of 8 is l / 8 throughout).
-template <class C>
-struct RingLoads {
-  uint32_t a_off[C::A_INSTR], b_off[C::B_INSTR];
-  uint32_t chunk;  // byte position of this lane's 16 bytes in a slice row
-  // MX: what this wave brings of the scales, waves 0-3 of A's, waves 4-7 of
-  // B's: the first slice's, bytes to the next slice's, and their size
-  uint64_t s_base, s_step;
-  uint32_t s_bytes;
-};
-
-template <class C>
-__device__ __forceinline__ RingLoads<C> ring_loads(const RingTile &t, int wave) {
-  RingLoads<C> L;
-  const int l = t.tid % kWave;
-  const uint32_t r = l / 8;
-  L.chunk = 16u * ((l % 8) ^ r);
-#pragma unroll
-  for (int i = 0; i < C::A_INSTR; ++i)
-    L.a_off[i] = ((i * 8 + wave) * (C::A_LANES / 8) + r) * t.pitch + L.chunk;
-#pragma unroll
-  for (int i = 0; i < C::B_INSTR; ++i) L.b_off[i] = ((i * 8 + wave) * 8 + r) * t.pitch + L.chunk;
-  if constexpr (C::MX) {
-    const uint64_t as = (uint64_t)t.As, bs = (uint64_t)t.Bs;
-    const uint64_t as_step = t.as_step, bs_step = t.bs_step;
-    const int rows = t.rows, ncols = t.ncols;
-    L.s_base = wave >= 4 ? bs : as;
-    L.s_step = wave >= 4 ? bs_step : as_step;
-    L.s_bytes = 8u * (uint32_t)(wave >= 4 ? ncols : rows);
-  }
-  return L;
-}
-
-// Issues this wave's loads of slice k into one stage. Where rows of A take
-// fewer than 8 lanes' worth of an instruction, a row's place in its group of
-// 8 is not l / 8 alone; 16- and 32-row tiles therefore load 2 or 4 rows a
-// wave and swizzle by the row's own place (a_row8 below).
-template <class C, int B_POLICY>
-__device__ __forceinline__ void ring_issue(const RingTile &t, const RingLoads<C> &L, lds_u8 *stage,
-                                           int k, int wave, int lane) {
+// Issues this wave's loads of slice k into one stage of a BM x BN tile. Each
+// load takes rows in groups of 8 (of BM / 8 where the tile has fewer than 64
+// rows, on the first BM lanes, so that every wave issues the same number of
+// loads and waits on the same count).
+//
+// Weights are loaded as streaming data (nt) where each row's piece is whole
+// lines: each weight byte feeds the few tiles of one column slice, which run
+// side by side. Measured on 64 x 256 rows, K = 1024, N = 2688: 111 -> 98 us.
+// Where pieces straddle lines, nt drops the line whose other half the next
+// slice needs: 12 x 65 rows, K = 712, N = 1000: 17.0 us without, 20.4 with.
+template <bool MX>
+__device__ __forceinline__ void ring_issue(const RingTile &t, int BM, int BN, lds_u8 *stage, int k,
+                                           int wave, int lane) {
   const uint32_t k0 = (uint32_t)k * kRowBytes;
   const buf_rsrc ra = make_buf(t.A + k0, (uint32_t)t.rows * t.pitch - k0);
   const buf_rsrc rb = make_buf(t.B + k0, (uint32_t)t.ncols * t.pitch - k0);
   const uint32_t left = t.pitch - k0;  // bytes of a row from this slice on
-  const bool b_in = L.chunk < left;
-  if constexpr (C::A_LANES == 64) {
+  const int lr = lane / 8;
+  const uint32_t chunk = 16u * ((lane % 8) ^ lr);
+  if (BM >= 64) {
 #pragma unroll
-    for (int i = 0; i < C::A_INSTR; ++i)
-      dma16(ra, stage + (i * 8 + wave) * 1024, b_in ? L.a_off[i] : kOob);
+    for (int i = 0; i < 4; ++i)
+      if (i < BM / 64) {
+        const int r = (i * 8 + wave) * 8;
+        dma16(ra, stage + r * kRowBytes, chunk < left ? (uint32_t)(r + lr) * t.pitch + chunk : kOob);
+      }
   } else {
-    // rows wave * (A_LANES / 8) + l / 8; their place in a group of 8
-    constexpr int kR = C::A_LANES / 8;
-    const uint32_t r8 = (wave * kR + lane / 8) % 8;
-    const uint32_t chunk = 16u * ((lane % 8) ^ r8);
-    const uint32_t off = (wave * kR + lane / 8) * t.pitch + chunk;
-    if (lane < C::A_LANES)
-      dma16(ra, stage + wave * (16 * C::A_LANES), chunk < left ? off : kOob);
+    const int r = wave * (BM / 8), lr8 = (r + lr) % 8;
+    const uint32_t c = 16u * ((lane % 8) ^ lr8);
+    if (lane < BM)
+      dma16(ra, stage + r * kRowBytes, c < left ? (uint32_t)(r + lr) * t.pitch + c : kOob);
   }
+  lds_u8 *const bst = stage + BM * kRowBytes;
+  auto weights = [&](auto policy) {
 #pragma unroll
-  for (int i = 0; i < C::B_INSTR; ++i)
-    dma16<B_POLICY>(rb, stage + C::A_BYTES + (i * 8 + wave) * 1024, b_in ? L.b_off[i] : kOob);
-  if constexpr (C::MX) {
-    // scale bytes: 16, two rows' worth, a lane
+    for (int i = 0; i < 4; ++i)
+      if (i < BN / 64) {
+        const int r = (i * 8 + wave) * 8;
+        dma16<decltype(policy)::value>(rb, bst + r * kRowBytes,
+                                       chunk < left ? (uint32_t)(r + lr) * t.pitch + chunk : kOob);
+      }
+  };
+  if (t.pitch % kRowBytes == 0) weights(std::integral_constant<int, kCacheStream>{});
+  else weights(std::integral_constant<int, kCacheDefault>{});
+  if constexpr (MX) {
+    // scale bytes: 16, two rows' worth, a lane; waves 0-3 take A's, 4-7 B's
     const bool is_b = wave >= 4;
-    const int n = is_b ? C::BN / 8 : C::BM / 8;  // lanes of this wave
+    const int n = is_b ? BN / 8 : BM / 8;  // lanes of this wave
     const int at = 16 * (wave % 4) * n;
-    const buf_rsrc rs = make_buf((const void *)(L.s_base + (uint64_t)k * L.s_step), L.s_bytes);
-    lds_u8 *const dst = stage + C::A_BYTES + C::B_BYTES + (is_b ? C::AS_BYTES : 0) + at;
+    const uint64_t as = (uint64_t)t.As + (uint64_t)k * t.as_step;
+    const uint64_t bs = (uint64_t)t.Bs + (uint64_t)k * t.bs_step;
+    const int rows = t.rows, ncols = t.ncols;
+    const buf_rsrc rs = make_buf((const void *)(is_b ? bs : as), 8u * (uint32_t)(is_b ? ncols : rows));
+    lds_u8 *const dst = stage + (BM + BN) * kRowBytes + (is_b ? BM * 8 : 0) + at;
     if (lane < n) dma16(rs, dst, (uint32_t)(at + 16 * lane));
   }
+}
+
+__device__ __forceinline__ int ring_slices(const RingTile &t) {
+  return (int)((t.pitch + kRowBytes - 1) / kRowBytes);
+}
+
+// The first slices of a tile, as many as the ring takes ahead of the products.
+template <bool MX>
+__device__ __forceinline__ void ring_prologue(const RingTile &t, int BM, int BN, lds_u8 *lds,
+                                              int wave, int lane) {
+  const int n = min(ring_stages(BM, BN, MX) - 1, ring_slices(t)), bytes = ring_stage(BM, BN, MX);
+#pragma unroll 1
+  for (int k = 0; k < n; ++k) ring_issue<MX>(t, BM, BN, lds + k * bytes, k, wave, lane);
 }
 
 // The products of one slice. Two matrix steps; lane group g takes 16-byte
@@ -335,7 +351,7 @@ __device__ __forceinline__ void ring_mma(f32x4 (&acc)[C::NI][C::MI],
     const lds_u8 *const sc = stage + C::A_BYTES + C::B_BYTES + 2 * g;
 #pragma unroll
     for (int ni = 0; ni < C::NI; ++ni)
-      sb[ni] = mask & *(const lds_u16 *)(sc + C::AS_BYTES + 8 * (wn0 + ni * 16 + s));
+      sb[ni] = mask & *(const lds_u16 *)(sc + C::BM * 8 + 8 * (wn0 + ni * 16 + s));
 #pragma unroll
     for (int mi = 0; mi < C::MI; ++mi)
       sa[mi] = mask & *(const lds_u16 *)(sc + 8 * (wm0 + mi * 16 + s));
@@ -378,12 +394,12 @@ __device__ __forceinline__ void ring_mma(f32x4 (&acc)[C::NI][C::MI],
 // The two stages are distinct memory (__restrict__): without that the
 // compiler would hold back the reads of one until the loads into the other
 // have landed.
-template <class C, int B_POLICY>
+template <class C>
 __device__ __forceinline__ void ring_step(f32x4 (&acc)[C::NI][C::MI], const RingTile &t,
-                                          const RingLoads<C> &L, const lds_u8 *__restrict__ cur,
+                                          const lds_u8 *__restrict__ cur,
                                           lds_u8 *__restrict__ nxt, int k_next, int KT, int wave,
                                           int lane, int wm0, int wn0, int blocks_left) {
-  if (k_next < KT) ring_issue<C, B_POLICY>(t, L, nxt, k_next, wave, lane);
+  if (k_next < KT) ring_issue<C::MX>(t, C::BM, C::BN, nxt, k_next, wave, lane);
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_setprio(1);
   ring_mma<C>(acc, cur, wm0, wn0, lane, blocks_left, [](int) {});
@@ -391,56 +407,117 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[C::NI][C::MI], const Ring
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// A whole tile. n_blocks: 32-value blocks of a row (MX only). epi(mi) stores
-// row block mi of acc. Ends with a barrier after the last LDS read, so that
-// the next tile may fill the ring.
-template <class C, int B_POLICY, class Epi>
-__device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds,
-                                              f32x4 (&acc)[C::NI][C::MI], int n_blocks, Epi &&epi) {
-  const int wave = __builtin_amdgcn_readfirstlane(t.tid / kWave);
-  const int lane = t.tid % kWave;
+// A whole tile whose prologue has been issued. n_blocks: 32-value blocks of a
+// row (MX only). epi.begin() runs before the last slice's products,
+// epi.block(acc, mi) stores row block mi. next() runs between the last LDS
+// read of the tile and its stores (or, for tiles of at most 4 row blocks a
+// wave, which store during the last slice, after them): it issues the next
+// tile's prologue.
+template <class C, class Epi, class Next>
+__device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, int tid,
+                                              int n_blocks, Epi &&epi, Next &&next) {
+  const int wave = scalar(tid / kWave);
+  const int lane = tid % kWave;
   const int wm0 = (wave / C::WN) * C::WTM, wn0 = (wave % C::WN) * C::WTN;
+  f32x4 acc[C::NI][C::MI];
 #pragma unroll
   for (int ni = 0; ni < C::NI; ++ni)
 #pragma unroll
     for (int mi = 0; mi < C::MI; ++mi) acc[ni][mi] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int KT = (int)((t.pitch + kRowBytes - 1) / kRowBytes);
-  const RingLoads<C> L = ring_loads<C>(t, wave);
-#pragma unroll 1
-  for (int k = 0; k < C::S - 1; ++k)
-    if (k < KT) ring_issue<C, B_POLICY>(t, L, lds + k * C::STAGE, k, wave, lane);
+  const int KT = ring_slices(t);
   int cur = 0, nxt = C::S - 1;  // stages of slice k and of slice k + S - 1
   for (int k = 0; k < KT - 1; ++k) {
     // slices k + 1 .. min(k + S - 2, KT - 1) stay in flight
     wait_slices<C>(min(C::S - 2, KT - 1 - k));
     wg_barrier();
-    ring_step<C, B_POLICY>(acc, t, L, lds + cur * C::STAGE, lds + nxt * C::STAGE, k + C::S - 1, KT,
-                           wave, lane, wm0, wn0, n_blocks - 8 * k);
+    ring_step<C>(acc, t, lds + cur * C::STAGE, lds + nxt * C::STAGE, k + C::S - 1, KT, wave, lane,
+                 wm0, wn0, n_blocks - 8 * k);
     cur = cur + 1 == C::S ? 0 : cur + 1;
     nxt = nxt + 1 == C::S ? 0 : nxt + 1;
   }
   wait_loads<0>();
   wg_barrier();
+  epi.begin();
   // Row block mi is final. The empty asm keeps its products ahead of the
   // epilogue's branches (the compiler would move them into those).
   auto final_block = [&](int mi) {
 #pragma unroll
     for (int ni = 0; ni < C::NI; ++ni) asm volatile("" : "+v"(acc[ni][mi]));
-    if constexpr (C::MI <= 4) epi(mi);
+    if constexpr (C::MI <= 4) epi.block(acc, mi);
   };
   ring_mma<C>(acc, lds + cur * C::STAGE, wm0, wn0, lane, n_blocks - 8 * (KT - 1), final_block);
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   wg_barrier();
+  next();
   if constexpr (C::MI > 4) {
 #pragma unroll
     for (int mi = 0; mi < C::MI; ++mi) {
-      epi(mi);
+      epi.block(acc, mi);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
 
 static_assert(kThreads / kWave == 8, "eight waves share a slice's loads");
+
+// The tiles of one workgroup, one after the other. make(tile) gives a
+// RingTile, run(cfg, ring tile, tile, next) runs one with the configuration
+// cfg, a default-constructed RingCfg.
+template <bool MX, class Make, class Run>
+__device__ __forceinline__ void run_ring_tiles(const RingSched &sched, const RingGrid &grid,
+                                               const int32_t *off, int E, int M_cap, int N,
+                                               int bm_fixed, lds_u8 *lds, Make &&make, Run &&run) {
+  const int G = gridDim.x, b = blockIdx.x;
+  // contiguous tiles on one XCD (workgroup ids go round-robin to the XCDs)
+  int t = (b % 8) * (G / 8) + b / 8;
+  if (t >= grid.total) return;
+  Tile tl = decode_ring_tile(sched, off, t, E, M_cap, N, bm_fixed, grid.width);
+  RingTile rt = make(tl);
+  {
+    const int tid = threadIdx.x;
+    ring_prologue<MX>(rt, tl.bm, tl.bn, lds, scalar(tid / kWave), tid % kWave);
+  }
+  for (;;) {
+    const int t2 = t + G;
+    const bool more = t2 < grid.total;
+    Tile ntl = tl;
+    if (more) ntl = decode_ring_tile(sched, off, t2, E, M_cap, N, bm_fixed, grid.width);
+    const RingTile nrt = make(ntl);
+    auto next = [&] {
+      int tid = threadIdx.x;
+      asm volatile("" : "+v"(tid));
+      if (more) ring_prologue<MX>(nrt, ntl.bm, ntl.bn, lds, scalar(tid / kWave), tid % kWave);
+    };
+    if (tl.bn == 256) {
+      switch (tl.bm) {
+        case 16: run(RingCfg<16, 256, 1, 8, MX>{}, rt, tl, next); break;
+        case 32: run(RingCfg<32, 256, 1, 8, MX>{}, rt, tl, next); break;
+        case 64: run(RingCfg<64, 256, 1, 8, MX>{}, rt, tl, next); break;
+        case 128: run(RingCfg<128, 256, 2, 4, MX>{}, rt, tl, next); break;
+        default: run(RingCfg<256, 256, 2, 4, MX>{}, rt, tl, next); break;
+      }
+    } else if (tl.bn == 128) {
+      switch (tl.bm) {
+        case 16: run(RingCfg<16, 128, 1, 8, MX>{}, rt, tl, next); break;
+        case 32: run(RingCfg<32, 128, 1, 8, MX>{}, rt, tl, next); break;
+        case 64: run(RingCfg<64, 128, 2, 4, MX>{}, rt, tl, next); break;
+        case 128: run(RingCfg<128, 128, 2, 4, MX>{}, rt, tl, next); break;
+        default: run(RingCfg<256, 128, 4, 2, MX>{}, rt, tl, next); break;
+      }
+    } else {
+      switch (tl.bm) {
+        case 32: run(RingCfg<32, 64, 2, 4, MX>{}, rt, tl, next); break;
+        case 64: run(RingCfg<64, 64, 2, 4, MX>{}, rt, tl, next); break;
+        case 128: run(RingCfg<128, 64, 4, 2, MX>{}, rt, tl, next); break;
+        default: run(RingCfg<256, 64, 4, 2, MX>{}, rt, tl, next); break;
+      }
+    }
+    if (!more) break;
+    t = t2;
+    tl = ntl;
+    rt = nrt;
+  }
+}
 
 // --------------------------------------------------------------- epilogues
 //
@@ -459,7 +536,59 @@ __device__ __forceinline__ u32x4 swap_pair(u32x2 a, u32x2 b) {
   return u32x4{p[0], q[0], p[1], q[1]};
 }
 
+// Rows m0 .. m0 + 15 of a row-major array as a buffer from the tile's first
+// column on; rows past the tile's valid ones are outside it, so that a store
+// there is dropped and a load reads zeros, without a branch. base: row 0 of
+// the tile, its first column; col_bytes: that column's place in the row. 16
+// rows stay below 2^31 bytes (columns <= 2^24 of 4 bytes).
+__device__ __forceinline__ buf_rsrc row_block(const void *base, int m0, int rows, size_t row_bytes,
+                                              size_t col_bytes) {
+  const int n = min(max(rows - m0, 0), 16);
+  return make_buf((const char *)base + (size_t)m0 * row_bytes,
+                  n > 0 ? (uint32_t)((size_t)n * row_bytes - col_bytes) : 0u);
+}
+
+__device__ __forceinline__ void st_buf16(buf_rsrc r, uint32_t off, u32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+}
+__device__ __forceinline__ void st_buf8(buf_rsrc r, uint32_t off, u32x2 v) {
+  __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, 0);
+}
+__device__ __forceinline__ void st_buf4(buf_rsrc r, uint32_t off, uint32_t v) {
+  __builtin_amdgcn_raw_buffer_store_b32(v, r, off, 0, 0);
+}
+
+// One row block of a wave tile as fp32 or bf16. row_bytes: of a row of the
+// output; base: its first row and column of the tile; ncols: valid columns.
+template <class C, bool BF16>
+__device__ __forceinline__ void store_block(const f32x4 (&acc)[C::NI][C::MI], int mi, void *base,
+                                            int wm0, int wn0, int lane, int rows, int ncols,
+                                            size_t row_bytes, size_t col_bytes) {
+  const int g = lane / 16, s = lane % 16;
+  const buf_rsrc r = row_block(base, wm0 + mi * 16, rows, row_bytes, col_bytes);
+  const uint32_t row = (uint32_t)s * (uint32_t)row_bytes;
+  if constexpr (!BF16) {
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ++ni) {
+      const int n = wn0 + ni * 16 + 4 * g;
+      st_buf16(r, n < ncols ? row + 4u * n : kOob, __builtin_bit_cast(u32x4, acc[ni][mi]));
+    }
+  } else if constexpr (C::NI % 2 == 0) {
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ni += 2) {
+      const int n = wn0 + (ni + g % 2) * 16 + 8 * (g / 2);
+      st_buf16(r, n < ncols ? row + 2u * n : kOob,
+               swap_pair(pack_bf16(acc[ni][mi]), pack_bf16(acc[ni + 1][mi])));
+    }
+  } else {
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ++ni) {
+      const int n = wn0 + ni * 16 + 4 * g;
+      st_buf8(r, n < ncols ? row + 2u * n : kOob, pack_bf16(acc[ni][mi]));
+    }
+  }
+}
+
 __device__ __forceinline__ void st_g16u(void *p, u32x4 v) { *(gbl_u32x4 *)p = v; }
-__device__ __forceinline__ void st_g8u(void *p, u32x2 v) { *(gbl_u32x2 *)p = v; }
 
 }  // namespace gg

@@ -218,170 +218,100 @@ struct Mx4Params {
   int bm_fixed, tile_cap;
 };
 
-// Tile heights as in gg_mainloop.h, eight waves, and the deepest ring that
-// 160 KB of LDS hold.
-using M16 = RingCfg<16, 128, 1, 8, 6, true>;
-using M16M = RingCfg<16, 256, 1, 8, 4, true>;
-using M16W = RingCfg<16, 512, 1, 8, 2, true>;
-using M32 = RingCfg<32, 256, 1, 8, 4, true>;
-using M64 = RingCfg<64, 256, 1, 8, 3, true>;
-using M128 = RingCfg<128, 256, 2, 4, 3, true>;
-using M256 = RingCfg<256, 256, 2, 4, 2, true>;
-
 __device__ __forceinline__ uint32_t swiglu_pair(f32x4 v) {
   const f32x2 h = {silu(v.x) * v.y, silu(v.z) * v.w};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(h, bf16x2));
 }
 
+// The epilogue of one tile; row0, col0: its first row and output column.
 template <class C, MOut O>
-__device__ __forceinline__ void mx4_tile(const Mx4Params &p, const Tile &tl, lds_u8 *lds) {
-  const int row0 = __builtin_amdgcn_readfirstlane(tl.row0);
-  const int col0 = __builtin_amdgcn_readfirstlane(tl.col0);
-  const int expert = __builtin_amdgcn_readfirstlane(tl.expert);
-  // sizes the compiler cannot see through: what it derives from them is then
-  // computed per tile instead of being kept (and spilled) across tiles
-  int K_ = p.K, N_ = p.N, M_ = p.M_cap;
-  asm volatile("" : "+s"(K_), "+s"(N_), "+s"(M_));
-  const int slices = cdiv(K_, kSliceK);
-  RingTile t;
-  t.pitch = (uint32_t)K_ / 2;
-  t.A = p.A + (size_t)row0 * t.pitch;
-  t.B = p.B + ((size_t)expert * N_ + col0) * t.pitch;
-  t.as_step = (size_t)M_ * kSliceBlocks;
-  t.bs_step = (size_t)N_ * kSliceBlocks;
-  t.As = p.As + (size_t)row0 * kSliceBlocks;
-  t.Bs = p.Bs + (size_t)expert * slices * t.bs_step + (size_t)col0 * kSliceBlocks;
-  t.rows = __builtin_amdgcn_readfirstlane(tl.rows);
-  t.ncols = min(C::BN, N_ - col0);
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));  // keep per-tile index arithmetic inside the tile
-  t.tid = tid;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
-  const int wm0 = (wave / C::WN) * C::WTM, wn0 = (wave % C::WN) * C::WTN;
-  const int g = lane / 16, s = lane % 16;
-  const size_t N = N_;
-  f32x4 acc[C::NI][C::MI];
-  auto epi = [&](int mi) {
-    const int m = wm0 + mi * 16 + s;
-    const size_t row = (size_t)(row0 + m);
-    const bool in = m < t.rows;
-    if constexpr (O == MOut::F32) {
-#pragma unroll
-      for (int ni = 0; ni < C::NI; ++ni) {
-        const int n = wn0 + ni * 16 + 4 * g;
-        if (in && n < t.ncols) st_g16((float *)p.C + row * N + col0 + n, acc[ni][mi]);
-      }
-    } else if constexpr (O == MOut::BF16) {
-      uint16_t *const out = (uint16_t *)p.C + row * N + col0;
-      if constexpr (C::NI % 2 == 0) {
-#pragma unroll
-        for (int ni = 0; ni < C::NI; ni += 2) {
-          const u32x4 v = swap_pair(pack_bf16(acc[ni][mi]), pack_bf16(acc[ni + 1][mi]));
-          const int n = wn0 + (ni + g % 2) * 16 + 8 * (g / 2);
-          if (in && n < t.ncols) st_g16u(out + n, v);
-        }
-      } else {
-#pragma unroll
-        for (int ni = 0; ni < C::NI; ++ni) {
-          const int n = wn0 + ni * 16 + 4 * g;
-          if (in && n < t.ncols) st_g8u(out + n, pack_bf16(acc[ni][mi]));
-        }
-      }
+struct Mx4Epi {
+  const Mx4Params &p;
+  int row0, col0, rows, ncols, wm0, wn0, lane;
+  __device__ __forceinline__ void begin() {}
+  __device__ __forceinline__ void block(const f32x4 (&acc)[C::NI][C::MI], int mi) {
+    if constexpr (O != MOut::SwiGlu) {
+      const size_t es = O == MOut::F32 ? 4 : 2;
+      store_block<C, O == MOut::BF16>(acc, mi, (char *)p.C + ((size_t)row0 * p.N + col0) * es, wm0,
+                                      wn0, lane, rows, ncols, p.N * es, col0 * es);
     } else {
-      // two activations a block and lane: columns n, n + 1 and n + 2, n + 3
-      uint16_t *const out = (uint16_t *)p.C + row * (N / 2) + col0 / 2;
+      // two activations a block and lane (columns n, n + 1 and n + 2, n + 3):
+      // one bf16 each, so a byte of output per column of the product
+      const int g = lane / 16, s = lane % 16;
+      const buf_rsrc r = row_block((char *)p.C + (size_t)row0 * p.N + col0, wm0 + mi * 16, rows,
+                                   p.N, col0);
+      const uint32_t row = (uint32_t)s * (uint32_t)p.N;
       if constexpr (C::NI % 2 == 0) {
 #pragma unroll
         for (int ni = 0; ni < C::NI; ni += 2) {
           const auto h = __builtin_amdgcn_permlane16_swap(swiglu_pair(acc[ni][mi]),
                                                           swiglu_pair(acc[ni + 1][mi]), false, false);
           const int n = wn0 + (ni + g % 2) * 16 + 8 * (g / 2);
-          if (in && n < t.ncols) st_g8u(out + n / 2, u32x2{h[0], h[1]});
+          st_buf8(r, n < ncols ? row + n : kOob, u32x2{h[0], h[1]});
         }
       } else {
 #pragma unroll
         for (int ni = 0; ni < C::NI; ++ni) {
           const int n = wn0 + ni * 16 + 4 * g;
-          if (in && n < t.ncols)
-            *(__attribute__((address_space(1))) uint32_t *)(out + n / 2) = swiglu_pair(acc[ni][mi]);
+          st_buf4(r, n < ncols ? row + n : kOob, swiglu_pair(acc[ni][mi]));
         }
       }
     }
-  };
-  run_ring_tile<C, kCacheStream>(t, lds, acc, K_ / kBlockK, epi);
-}
+  }
+};
 
-template <int MASK>
-constexpr int mx4_lds() {
-  int m = 0;
-  const int b[] = {M16::LDS_BYTES, M16M::LDS_BYTES, M16W::LDS_BYTES};
-  if (MASK & 1)
-    for (int v : b) m = m > v ? m : v;
-  if (MASK & 2) m = m > M32::LDS_BYTES ? m : M32::LDS_BYTES;
-  if (MASK & 4) m = m > M64::LDS_BYTES ? m : M64::LDS_BYTES;
-  if (MASK & 8) m = m > M128::LDS_BYTES ? m : M128::LDS_BYTES;
-  if (MASK & 16) m = m > M256::LDS_BYTES ? m : M256::LDS_BYTES;
-  return m;
-}
+constexpr int kMx4Lds = kRingBytes + (int)sizeof(RingSched);
+static_assert(kMx4Lds <= 160 * 1024, "LDS budget");
 
-// MASK bit c compiles in tile height 16 << c.
-template <int MASK, MOut O>
+template <MOut O>
 __global__ __launch_bounds__(kThreads, 1) void mx4_product_kernel(Mx4Params p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds_dyn[];
   lds_u8 *const lds = (lds_u8 *)lds_dyn;
-  RingSched &sched = *(RingSched *)(lds_dyn + mx4_lds<MASK>());
-  const int G = gridDim.x, b = blockIdx.x;
-  const int total = build_ring_schedule(sched, p.off, p.E, p.M_cap, p.N, p.bm_fixed, p.tile_cap, G);
-  // contiguous tiles on one XCD (workgroup ids go round-robin to the XCDs)
-  const int slot = (b % kRingXcds) * (G / kRingXcds) + b / kRingXcds;
-  for (int base = 0; base < total; base += G) {
-    const int t = base + slot;
-    if (t >= total) break;
-    const Tile tl = decode_ring_tile(sched, p.off, t, p.E, p.M_cap, p.N, p.bm_fixed);
-    switch (tl.bm) {
-      case 16:
-        if constexpr (MASK & 1) {
-          if (tl.bn == kWideN) mx4_tile<M16W, O>(p, tl, lds);
-          else if (tl.bn == kTileN) mx4_tile<M16M, O>(p, tl, lds);
-          else mx4_tile<M16, O>(p, tl, lds);
-        }
-        break;
-      case 32: if constexpr (MASK & 2) mx4_tile<M32, O>(p, tl, lds); break;
-      case 64: if constexpr (MASK & 4) mx4_tile<M64, O>(p, tl, lds); break;
-      case 128: if constexpr (MASK & 8) mx4_tile<M128, O>(p, tl, lds); break;
-      default: if constexpr (MASK & 16) mx4_tile<M256, O>(p, tl, lds); break;
-    }
-  }
-}
-
-static_assert(mx4_lds<31>() + sizeof(RingSched) <= 160 * 1024, "LDS budget");
-
-template <int MASK, MOut O>
-static gg_status_t launch_mx4(const Mx4Params &p, long long bound, hipStream_t stream) {
-  constexpr int lds = mx4_lds<MASK>() + (int)sizeof(RingSched);
-  int dev = 0;
-  if (!current_device(&dev)) return GG_ERR_LAUNCH;
-  const RingLaunch li = ring_launch<mx4_product_kernel<MASK, O>>(dev, lds);
-  if (li.err != hipSuccess) return GG_ERR_LAUNCH;
-  long long g = bound < li.grid ? bound : li.grid;
-  g = (g + kRingXcds - 1) / kRingXcds * kRingXcds;
-  hipLaunchKernelGGL((mx4_product_kernel<MASK, O>), dim3((unsigned)g), dim3(kThreads), lds, stream,
-                     p);
-  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+  RingSched &sched = *(RingSched *)(lds_dyn + kRingBytes);
+  const RingGrid grid = build_ring_schedule(sched, p.off, p.E, p.M_cap, p.N, p.bm_fixed, p.tile_cap,
+                                            gridDim.x);
+  auto make = [&](const Tile &tl) {
+    // sizes the compiler cannot see through: what it derives from them is then
+    // computed per tile instead of being kept (and spilled) across tiles
+    int K = p.K, N = p.N, M = p.M_cap;
+    asm volatile("" : "+s"(K), "+s"(N), "+s"(M));
+    RingTile t;
+    t.pitch = (uint32_t)K / 2;
+    t.A = p.A + (size_t)tl.row0 * t.pitch;
+    t.B = p.B + ((size_t)tl.expert * N + tl.col0) * t.pitch;
+    t.as_step = (uint64_t)M * kSliceBlocks;
+    t.bs_step = (uint64_t)N * kSliceBlocks;
+    t.As = p.As + (size_t)tl.row0 * kSliceBlocks;
+    t.Bs = p.Bs + (size_t)tl.expert * cdiv(K, kSliceK) * t.bs_step + (size_t)tl.col0 * kSliceBlocks;
+    t.rows = tl.rows;
+    t.ncols = min(tl.bn, N - tl.col0);
+    return t;
+  };
+  auto run = [&](auto cfg, const RingTile &t, const Tile &tl, auto &next) {
+    using C = decltype(cfg);
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // keep per-tile index arithmetic inside the tile
+    const int wave = scalar(tid / kWave);
+    Mx4Epi<C, O> epi{p, tl.row0, tl.col0, t.rows, t.ncols, (wave / C::WN) * C::WTM,
+                     (wave % C::WN) * C::WTN, tid % kWave};
+    run_ring_tile<C>(t, lds, tid, p.K / kBlockK, epi, next);
+  };
+  run_ring_tiles<true>(sched, grid, p.off, p.E, p.M_cap, p.N, p.bm_fixed, lds, make, run);
 }
 
 template <MOut O>
 static gg_status_t mx4_product(const void *Aq, const void *a_scale, const void *Bq,
                                const void *b_scale, const int32_t *off, void *C, int E, int K,
                                int N, int M_cap, int bm, void *stream) {
-  long long bound = 0;
-  gg_status_t st = check_groups(off, E, N, M_cap, bm, kNarrowN, &bound);
+  int tile_cap = 0;
+  long long tiles = 0;
+  gg_status_t st = check_groups(off, E, N, M_cap, bm, kNarrowestN, &tile_cap, &tiles);
   if (st != GG_OK) return st;
   if (Bq == nullptr || b_scale == nullptr || K < 1) return GG_ERR_INVALID_VALUE;
   // arrays of no rows may be null
   if (M_cap > 0 && (Aq == nullptr || a_scale == nullptr || C == nullptr)) return GG_ERR_INVALID_VALUE;
   if (K % kBlockK != 0 || N % 8 != 0) return GG_ERR_MISALIGNED;
-  // a tile's weight rows, 512 * K / 2 bytes, stay within 32-bit offsets
+  // a tile's weight rows, 256 * K / 2 bytes, stay within 32-bit offsets
   if (K > GG_MAX_K || N > GG_MAX_N) return GG_ERR_UNSUPPORTED;
   if (!is_aligned(Aq, 16) || !is_aligned(a_scale, 16) || !is_aligned(Bq, 16) ||
       !is_aligned(b_scale, 16) || !is_aligned(C, 16))
@@ -389,16 +319,14 @@ static gg_status_t mx4_product(const void *Aq, const void *a_scale, const void *
   if (M_cap == 0) return GG_OK;
   const Mx4Params p{static_cast<const char *>(Aq), static_cast<const char *>(a_scale),
                     static_cast<const char *>(Bq), static_cast<const char *>(b_scale), off, C, E, K,
-                    N, M_cap, bm, (int)bound};
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  switch (bm) {
-    case 16: return launch_mx4<1, O>(p, bound, s);
-    case 32: return launch_mx4<2, O>(p, bound, s);
-    case 64: return launch_mx4<4, O>(p, bound, s);
-    case 128: return launch_mx4<8, O>(p, bound, s);
-    case 256: return launch_mx4<16, O>(p, bound, s);
-    default: return launch_mx4<31, O>(p, bound, s);
-  }
+                    N, M_cap, bm, tile_cap};
+  int dev = 0;
+  if (!current_device(&dev)) return GG_ERR_LAUNCH;
+  const RingLaunch li = ring_launch<mx4_product_kernel<O>>(dev, kMx4Lds);
+  if (li.err != hipSuccess) return GG_ERR_LAUNCH;
+  hipLaunchKernelGGL((mx4_product_kernel<O>), dim3((unsigned)li.workgroups(tiles)), dim3(kThreads),
+                     kMx4Lds, static_cast<hipStream_t>(stream), p);
+  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
 }
 
 // Sizes of the row kernels: blocks of a launch, within the grid's limit.
