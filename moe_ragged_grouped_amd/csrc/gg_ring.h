@@ -243,8 +243,16 @@ struct RingCfg {
   static constexpr int MI = WTM / 16, NI = WTN / 16;
   static constexpr int A_BYTES = BM * kRowBytes, B_BYTES = BN * kRowBytes;
   static constexpr int STAGE = ring_stage(BM, BN, MX), S = ring_stages(BM, BN, MX);
-  // loads a wave issues per slice (ring_issue)
-  static constexpr int LPS = (BM >= 64 ? BM / 64 : 1) + BN / 64 + (MX ? 1 : 0);
+  // loads a wave issues per slice: of A, and of the weights and the scales
+  static constexpr int NA = BM >= 64 ? BM / 64 : 1, NB = BN / 64 + (MX ? 1 : 0), LPS = NA + NB;
+  // Two stages are all that the tallest tile leaves room for, and one slice
+  // ahead is too little for weights that come from HBM (measured: 2.3 us a
+  // slice against 1.5 for its products alone). But a wave takes all column
+  // fragments and scales of a slice into registers before its second row
+  // block, so the weights' half of the stage is free almost a slice early and
+  // is refilled two slices ahead; A, which the tiles of a row block share, is
+  // mostly in L2.
+  static constexpr bool EARLY_B = S == 2;
   static_assert(S >= 2 && (S - 2) * LPS < 64, "loads in flight");
   static_assert(S * STAGE <= kRingBytes, "LDS");
 };
@@ -258,63 +266,109 @@ struct RingTile {
   int rows, ncols;        // valid rows and columns
 };
 
-// Issues this wave's loads of slice k into one stage of a BM x BN tile. Each
-// load takes rows in groups of 8 (of BM / 8 where the tile has fewer than 64
-// rows, on the first BM lanes, so that every wave issues the same number of
-// loads and waits on the same count).
+// Rows of a tile of fewer than 64: BM / 8 of them a wave, on its first BM
+// lanes, so that every wave issues the same number of loads and waits on the
+// same count. left: bytes of a row from this slice on.
+__device__ __forceinline__ void ring_short_rows(buf_rsrc ra, int BM, lds_u8 *stage, uint32_t pitch,
+                                                uint32_t left, int wave, int lane) {
+  const int r = wave * (BM / 8), lr = lane / 8;
+  const uint32_t c = 16u * ((lane % 8) ^ ((r + lr) % 8));
+  if (lane < BM)
+    dma16(ra, stage + r * kRowBytes, c < left ? (uint32_t)(r + lr) * pitch + c : kOob);
+}
+
+// Scale bytes: 16, two rows' worth, a lane; waves 0-3 take A's, waves 4-7 B's.
+__device__ __forceinline__ buf_rsrc ring_scales(const RingTile &t, int k, int wave) {
+  const uint64_t as = (uint64_t)t.As + (uint64_t)k * t.as_step;
+  const uint64_t bs = (uint64_t)t.Bs + (uint64_t)k * t.bs_step;
+  const int rows = t.rows, ncols = t.ncols;
+  return make_buf((const void *)(wave >= 4 ? bs : as), 8u * (uint32_t)(wave >= 4 ? ncols : rows));
+}
+__device__ __forceinline__ void ring_scale_rows(buf_rsrc rs, int BM, int BN, lds_u8 *stage, int wave,
+                                                int lane) {
+  const bool is_b = wave >= 4;
+  const int n = is_b ? BN / 8 : BM / 8;  // lanes of this wave
+  const int at = 16 * (wave % 4) * n;
+  lds_u8 *const dst = stage + (BM + BN) * kRowBytes + (is_b ? BM * 8 : 0) + at;
+  if (lane < n) dma16(rs, dst, (uint32_t)(at + 16 * lane));
+}
+
+// This wave's loads of slice k of a BM x BN tile into one stage, a group of 8
+// rows to a load: of A, and of the weights with all scales.
 //
 // Weights are loaded as streaming data (nt) where each row's piece is whole
 // lines: each weight byte feeds the few tiles of one column slice, which run
 // side by side. Measured on 64 x 256 rows, K = 1024, N = 2688: 111 -> 98 us.
 // Where pieces straddle lines, nt drops the line whose other half the next
 // slice needs: 12 x 65 rows, K = 712, N = 1000: 17.0 us without, 20.4 with.
-template <bool MX>
-__device__ __forceinline__ void ring_issue(const RingTile &t, int BM, int BN, lds_u8 *stage, int k,
-                                           int wave, int lane) {
-  const uint32_t k0 = (uint32_t)k * kRowBytes;
-  const buf_rsrc ra = make_buf(t.A + k0, (uint32_t)t.rows * t.pitch - k0);
-  const buf_rsrc rb = make_buf(t.B + k0, (uint32_t)t.ncols * t.pitch - k0);
-  const uint32_t left = t.pitch - k0;  // bytes of a row from this slice on
+__device__ __forceinline__ uint32_t ring_row_off(const RingTile &t, int r, int k, int lane) {
   const int lr = lane / 8;
   const uint32_t chunk = 16u * ((lane % 8) ^ lr);
-  if (BM >= 64) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < BM / 64) {
-        const int r = (i * 8 + wave) * 8;
-        dma16(ra, stage + r * kRowBytes, chunk < left ? (uint32_t)(r + lr) * t.pitch + chunk : kOob);
-      }
-  } else {
-    const int r = wave * (BM / 8), lr8 = (r + lr) % 8;
-    const uint32_t c = 16u * ((lane % 8) ^ lr8);
-    if (lane < BM)
-      dma16(ra, stage + r * kRowBytes, c < left ? (uint32_t)(r + lr) * t.pitch + c : kOob);
-  }
-  lds_u8 *const bst = stage + BM * kRowBytes;
-  auto weights = [&](auto policy) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < BN / 64) {
-        const int r = (i * 8 + wave) * 8;
-        dma16<decltype(policy)::value>(rb, bst + r * kRowBytes,
-                                       chunk < left ? (uint32_t)(r + lr) * t.pitch + chunk : kOob);
-      }
-  };
-  if (t.pitch % kRowBytes == 0) weights(std::integral_constant<int, kCacheStream>{});
-  else weights(std::integral_constant<int, kCacheDefault>{});
-  if constexpr (MX) {
-    // scale bytes: 16, two rows' worth, a lane; waves 0-3 take A's, 4-7 B's
-    const bool is_b = wave >= 4;
-    const int n = is_b ? BN / 8 : BM / 8;  // lanes of this wave
-    const int at = 16 * (wave % 4) * n;
-    const uint64_t as = (uint64_t)t.As + (uint64_t)k * t.as_step;
-    const uint64_t bs = (uint64_t)t.Bs + (uint64_t)k * t.bs_step;
-    const int rows = t.rows, ncols = t.ncols;
-    const buf_rsrc rs = make_buf((const void *)(is_b ? bs : as), 8u * (uint32_t)(is_b ? ncols : rows));
-    lds_u8 *const dst = stage + (BM + BN) * kRowBytes + (is_b ? BM * 8 : 0) + at;
-    if (lane < n) dma16(rs, dst, (uint32_t)(at + 16 * lane));
-  }
+  // a chunk past the row's end is out of range, as are rows past the last
+  return chunk < t.pitch - (uint32_t)k * kRowBytes ? (uint32_t)(r + lr) * t.pitch + chunk : kOob;
 }
+__device__ __forceinline__ buf_rsrc ring_rows(const char *base, int rows, const RingTile &t, int k) {
+  const uint32_t k0 = (uint32_t)k * kRowBytes;
+  return make_buf(base + k0, (uint32_t)rows * t.pitch - k0);
+}
+__device__ __forceinline__ void ring_load_a(const RingTile &t, buf_rsrc ra, int BM, lds_u8 *stage,
+                                            int i, int k, int wave, int lane) {
+  const int r = (i * 8 + wave) * 8;
+  if (BM >= 64) dma16(ra, stage + r * kRowBytes, ring_row_off(t, r, k, lane));
+  else ring_short_rows(ra, BM, stage, t.pitch, t.pitch - (uint32_t)k * kRowBytes, wave, lane);
+}
+__device__ __forceinline__ void ring_load_b(const RingTile &t, buf_rsrc rb, int BM, lds_u8 *stage,
+                                            int i, int k, int wave, int lane) {
+  const int r = (i * 8 + wave) * 8;
+  lds_u8 *const dst = stage + (BM + r) * kRowBytes;
+  if (t.pitch % kRowBytes == 0) dma16<kCacheStream>(rb, dst, ring_row_off(t, r, k, lane));
+  else dma16(rb, dst, ring_row_off(t, r, k, lane));
+}
+__device__ __forceinline__ void ring_issue_a(const RingTile &t, int BM, lds_u8 *stage, int k, int wave,
+                                             int lane) {
+  const buf_rsrc ra = ring_rows(t.A, t.rows, t, k);
+  const int n = BM >= 64 ? BM / 64 : 1;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) ring_load_a(t, ra, BM, stage, i, k, wave, lane);
+}
+template <bool MX>
+__device__ __forceinline__ void ring_issue_b(const RingTile &t, int BM, int BN, lds_u8 *stage, int k,
+                                             int wave, int lane) {
+  const buf_rsrc rb = ring_rows(t.B, t.ncols, t, k);
+#pragma unroll 1
+  for (int i = 0; i < BN / 64; ++i) ring_load_b(t, rb, BM, stage, i, k, wave, lane);
+  if constexpr (MX) ring_scale_rows(ring_scales(t, k, wave), BM, BN, stage, wave, lane);
+}
+
+// The same loads as pieces, to be issued between matrix instructions: a CU's
+// memory pipeline stays full, so a wave that issues its loads in a row blocks
+// on them before it multiplies. A of slice ka into stage sa (pieces 0 .. NA -
+// 1), weights and scales of slice kb into stage sb (the rest).
+template <class C>
+struct RingPieces {
+  const RingTile &t;
+  buf_rsrc ra, rb, rs;
+  lds_u8 *sa, *sb;
+  int ka, kb, KT, wave, lane;
+
+  __device__ __forceinline__ RingPieces(const RingTile &t_, lds_u8 *sa_, int ka_, lds_u8 *sb_, int kb_,
+                                        int KT_, int wave_, int lane_)
+      : t(t_), sa(sa_), sb(sb_), ka(ka_), kb(kb_), KT(KT_), wave(wave_), lane(lane_) {
+    ra = ring_rows(t.A, t.rows, t, ka);
+    rb = ring_rows(t.B, t.ncols, t, kb);
+    if constexpr (C::MX) rs = ring_scales(t, kb, wave);
+  }
+  template <int J>
+  __device__ __forceinline__ void issue() const {
+    if constexpr (J < C::NA) {
+      if (ka < KT) ring_load_a(t, ra, C::BM, sa, J, ka, wave, lane);
+    } else if constexpr (J < C::NA + C::BN / 64) {
+      if (kb < KT) ring_load_b(t, rb, C::BM, sb, J - C::NA, kb, wave, lane);
+    } else {
+      if (kb < KT) ring_scale_rows(rs, C::BM, C::BN, sb, wave, lane);
+    }
+  }
+};
 
 __device__ __forceinline__ int ring_slices(const RingTile &t) {
   return (int)((t.pitch + kRowBytes - 1) / kRowBytes);
@@ -326,29 +380,52 @@ __device__ __forceinline__ void ring_prologue(const RingTile &t, int BM, int BN,
                                               int wave, int lane) {
   const int n = min(ring_stages(BM, BN, MX) - 1, ring_slices(t)), bytes = ring_stage(BM, BN, MX);
 #pragma unroll 1
-  for (int k = 0; k < n; ++k) ring_issue<MX>(t, BM, BN, lds + k * bytes, k, wave, lane);
+  for (int k = 0; k < n; ++k) {
+    ring_issue_a(t, BM, lds + k * bytes, k, wave, lane);
+    ring_issue_b<MX>(t, BM, BN, lds + k * bytes, k, wave, lane);
+  }
+  if (ring_stages(BM, BN, MX) == 2 && ring_slices(t) > 1)  // EARLY_B
+    ring_issue_b<MX>(t, BM, BN, lds + bytes, 1, wave, lane);
 }
 
 // The products of one slice. Two matrix steps; lane group g takes 16-byte
 // chunk 4 ks + g of a row (bf16: l = 32 ks + 8 g ..) or 2 g + ks (4-bit: block
 // 2 g + ks of 32 values, so that a lane's two scale bytes are neighbours; the
 // matrix cores pair lane group with lane group, so any order that both
-// operands share is the same sum). blk(mi) runs after row block mi's last
-// product.
-template <class C, class Blk>
-__device__ __forceinline__ void ring_mma(f32x4 (&acc)[C::NI][C::MI],
-                                         const lds_u8 *__restrict__ stage, int wm0, int wn0,
-                                         int lane, int blocks_left, Blk &&blk) {
+// operands share is the same sum). A row block's fragment is read two blocks
+// ahead of its products and the second step's column fragments during the
+// first step, so that the matrix cores do not wait on LDS inside a slice.
+// mid(mi) runs after row block mi of the first step, blk(mi) after row block
+// mi's last product.
+template <class C, class Mid, class Blk>
+__device__ __forceinline__ void ring_mma(f32x4 (&acc)[C::NI][C::MI], const lds_u8 *a_stage,
+                                         const lds_u8 *b_stage, int wm0, int wn0, int lane,
+                                         int blocks_left, Mid &&mid, Blk &&blk) {
   const int g = lane / 16, s = lane % 16;
-  const lds_u8 *const ar = stage + (wm0 + s) * kRowBytes;
-  const lds_u8 *const br = stage + C::A_BYTES + (wn0 + s) * kRowBytes;
+  const lds_u8 *const ar = a_stage + (wm0 + s) * kRowBytes;
+  const lds_u8 *const br = b_stage + C::A_BYTES + (wn0 + s) * kRowBytes;
   int sa[C::MX ? C::MI : 1], sb[C::MX ? C::NI : 1];
+  const int c0 = 16 * ((C::MX ? 2 * g : g) ^ (s & 7));
+  const int c1 = 16 * ((C::MX ? 2 * g + 1 : 4 + g) ^ (s & 7));
+  u32x4 x[2][C::NI], y[3];
+  auto read_x = [&](auto ks) {
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ++ni)
+      x[ks][ni] = *(const lds_u32x4 *)(br + ni * 16 * kRowBytes + (ks ? c1 : c0));
+  };
+  auto read_y = [&](auto bc) {  // block b % MI of step b / MI
+    constexpr int b = decltype(bc)::value;
+    if constexpr (b < 2 * C::MI)
+      y[b % 3] = *(const lds_u32x4 *)(ar + b % C::MI * 16 * kRowBytes + (b / C::MI ? c1 : c0));
+  };
+  read_x(std::integral_constant<int, 0>{});
+  read_y(std::integral_constant<int, 0>{});
   if constexpr (C::MX) {
     // scale bytes past the row's last block are whatever memory holds there;
     // a zero byte (2^-127) times the zero values loaded there is zero
     const int v = blocks_left - 2 * g;
     const int mask = v >= 2 ? 0xffff : (v == 1 ? 0xff : 0);
-    const lds_u8 *const sc = stage + C::A_BYTES + C::B_BYTES + 2 * g;
+    const lds_u8 *const sc = b_stage + C::A_BYTES + C::B_BYTES + 2 * g;
 #pragma unroll
     for (int ni = 0; ni < C::NI; ++ni)
       sb[ni] = mask & *(const lds_u16 *)(sc + C::BM * 8 + 8 * (wn0 + ni * 16 + s));
@@ -356,55 +433,66 @@ __device__ __forceinline__ void ring_mma(f32x4 (&acc)[C::NI][C::MI],
     for (int mi = 0; mi < C::MI; ++mi)
       sa[mi] = mask & *(const lds_u16 *)(sc + 8 * (wm0 + mi * 16 + s));
   }
-  static_for<2>([&](auto ksc) {
-    constexpr int ks = decltype(ksc)::value;
-    const int c = 16 * ((C::MX ? 2 * g + ks : 4 * ks + g) ^ (s & 7));
-    u32x4 x[C::NI];
+  read_y(std::integral_constant<int, 1>{});
+  static_for<2 * C::MI>([&](auto bc) {
+    constexpr int b = decltype(bc)::value, ks = b / C::MI, mi = b % C::MI;
+    read_y(std::integral_constant<int, b + 2>{});
+    // (early where the weights' half of the stage is to be freed)
+    if constexpr (b == (C::EARLY_B || C::MI < 2 ? 0 : C::MI - 2)) read_x(std::integral_constant<int, 1>{});
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int ni = 0; ni < C::NI; ++ni) x[ni] = *(const lds_u32x4 *)(br + ni * 16 * kRowBytes + c);
-#pragma unroll
-    for (int mi = 0; mi < C::MI; ++mi) {
-      const u32x4 y = *(const lds_u32x4 *)(ar + mi * 16 * kRowBytes + c);
-#pragma unroll
-      for (int ni = 0; ni < C::NI; ++ni) {
-        if constexpr (C::MX) {
-          // formats 4, 4 = E2M1; a 4-bit operand is the low half of the eight
-          // registers, scale byte ks of each lane's scale register
-          const ring_i32x8 xv = __builtin_bit_cast(
-              ring_i32x8, __builtin_shufflevector(x[ni], x[ni], 0, 1, 2, 3, -1, -1, -1, -1));
-          const ring_i32x8 yv = __builtin_bit_cast(
-              ring_i32x8, __builtin_shufflevector(y, y, 0, 1, 2, 3, -1, -1, -1, -1));
-          acc[ni][mi] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              xv, yv, acc[ni][mi], 4, 4, ks, sb[ni], ks, sa[mi]);
-        } else {
-          acc[ni][mi] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, x[ni]), __builtin_bit_cast(bf16x8, y), acc[ni][mi], 0, 0,
-              0);
-        }
+    for (int ni = 0; ni < C::NI; ++ni) {
+      if constexpr (C::MX) {
+        // formats 4, 4 = E2M1; a 4-bit operand is the low half of the eight
+        // registers, scale byte ks of each lane's scale register
+        const ring_i32x8 xv = __builtin_bit_cast(
+            ring_i32x8, __builtin_shufflevector(x[ks][ni], x[ks][ni], 0, 1, 2, 3, -1, -1, -1, -1));
+        const ring_i32x8 yv = __builtin_bit_cast(
+            ring_i32x8, __builtin_shufflevector(y[b % 3], y[b % 3], 0, 1, 2, 3, -1, -1, -1, -1));
+        acc[ni][mi] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xv, yv, acc[ni][mi], 4, 4, ks,
+                                                                       sb[ni], ks, sa[mi]);
+      } else {
+        acc[ni][mi] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, x[ks][ni]), __builtin_bit_cast(bf16x8, y[b % 3]),
+            acc[ni][mi], 0, 0, 0);
       }
-      if constexpr (ks == 1) blk(mi);
     }
-    // one step at a time: the next step's fragments, read above this step's
-    // products, would need registers on top of the accumulators
+    if constexpr (ks == 0) mid(std::integral_constant<int, mi>{});
+    else blk(mi);
     __builtin_amdgcn_sched_barrier(0);
   });
 }
 
-// One step: refill the stage that slice k - 1 left, then multiply slice k.
-// The two stages are distinct memory (__restrict__): without that the
-// compiler would hold back the reads of one until the loads into the other
-// have landed.
+// One step: multiply slice k out of its stage (a_cur and b_cur, both its
+// start) and meanwhile refill the stage that slice k - 1 left: a_nxt is that
+// stage, b_nxt too, or with EARLY_B the present one, whose weights are read
+// by then. What is read and what is loaded into are passed as distinct memory
+// (__restrict__): without that the compiler would hold back every LDS read
+// until all loads into LDS have landed. The barrier in mid() keeps the one
+// pair that does meet, the reads of b_cur and the loads into b_nxt, in order.
 template <class C>
 __device__ __forceinline__ void ring_step(f32x4 (&acc)[C::NI][C::MI], const RingTile &t,
-                                          const lds_u8 *__restrict__ cur,
-                                          lds_u8 *__restrict__ nxt, int k_next, int KT, int wave,
-                                          int lane, int wm0, int wn0, int blocks_left) {
-  if (k_next < KT) ring_issue<C::MX>(t, C::BM, C::BN, nxt, k_next, wave, lane);
-  __builtin_amdgcn_sched_barrier(0);
+                                          const lds_u8 *__restrict__ a_cur,
+                                          const lds_u8 *__restrict__ b_cur,
+                                          lds_u8 *__restrict__ a_nxt, lds_u8 *__restrict__ b_nxt,
+                                          int ka, int kb, int KT, int wave, int lane, int wm0, int wn0,
+                                          int blocks_left) {
+  const RingPieces<C> loads(t, a_nxt, ka, b_nxt, kb, KT, wave, lane);
+  auto mid = [&](auto mc) {
+    constexpr int mi = decltype(mc)::value, j0 = mi * C::LPS / C::MI, j1 = (mi + 1) * C::LPS / C::MI;
+    static_for<j1 - j0>([&](auto jc) {
+      constexpr int j = j0 + decltype(jc)::value;
+      if constexpr (C::EARLY_B && j == C::NA) {
+        // every wave has its column fragments and scales
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wg_barrier();
+      }
+      loads.template issue<j>();
+    });
+  };
   __builtin_amdgcn_s_setprio(1);
-  ring_mma<C>(acc, cur, wm0, wn0, lane, blocks_left, [](int) {});
+  ring_mma<C>(acc, a_cur, b_cur, wm0, wn0, lane, blocks_left, mid, [](int) {});
   __builtin_amdgcn_s_setprio(0);
-  __builtin_amdgcn_sched_barrier(0);
 }
 
 // A whole tile whose prologue has been issued. n_blocks: 32-value blocks of a
@@ -427,11 +515,12 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
   const int KT = ring_slices(t);
   int cur = 0, nxt = C::S - 1;  // stages of slice k and of slice k + S - 1
   for (int k = 0; k < KT - 1; ++k) {
-    // slices k + 1 .. min(k + S - 2, KT - 1) stay in flight
-    wait_slices<C>(min(C::S - 2, KT - 1 - k));
+    if constexpr (C::EARLY_B) wait_loads<C::NB>();  // the weights of slice k + 1 stay in flight
+    else wait_slices<C>(min(C::S - 2, KT - 1 - k));  // slices k + 1 .. min(k + S - 2, KT - 1) do
     wg_barrier();
-    ring_step<C>(acc, t, lds + cur * C::STAGE, lds + nxt * C::STAGE, k + C::S - 1, KT, wave, lane,
-                 wm0, wn0, n_blocks - 8 * k);
+    lds_u8 *const c = lds + cur * C::STAGE, *const n = lds + nxt * C::STAGE;
+    ring_step<C>(acc, t, c, c, n, C::EARLY_B ? c : n, k + C::S - 1, k + C::S - (C::EARLY_B ? 0 : 1), KT,
+                 wave, lane, wm0, wn0, n_blocks - 8 * k);
     cur = cur + 1 == C::S ? 0 : cur + 1;
     nxt = nxt + 1 == C::S ? 0 : nxt + 1;
   }
@@ -445,7 +534,9 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
     for (int ni = 0; ni < C::NI; ++ni) asm volatile("" : "+v"(acc[ni][mi]));
     if constexpr (C::MI <= 4) epi.block(acc, mi);
   };
-  ring_mma<C>(acc, lds + cur * C::STAGE, wm0, wn0, lane, n_blocks - 8 * (KT - 1), final_block);
+  ring_mma<C>(
+      acc, lds + cur * C::STAGE, lds + cur * C::STAGE, wm0, wn0, lane, n_blocks - 8 * (KT - 1),
+      [](auto) {}, final_block);
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   wg_barrier();
   next();
