@@ -613,10 +613,28 @@ __device__ __forceinline__ void run_ring_tiles(const RingSched &sched, const Rin
 // --------------------------------------------------------------- epilogues
 //
 // Each 16 x 16 block leaves lane 16 g + s with columns 4 g .. 4 g + 3 of row
-// s. Outputs of 2 bytes would make 8-byte stores of that. Swapping lane
-// groups between two neighbouring blocks (v_permlane16_swap) instead gives
-// every lane 8 neighbouring columns, one 16-byte store: group g then holds
-// columns 8 (g / 2) .. + 7 of block (g % 2).
+// s: 64 bytes of each of 16 rows in one fp32 store instruction. Stores of
+// whole 128-byte lines are three times as fast (measured out of one
+// workgroup a CU into L2: 117 bytes a ns against 32 - 37; into HBM on the whole chip 5.5 - 6.0 TB/s
+// against 5.3 - 5.7), so neighbouring blocks trade halves first:
+//  * swap_rows: of two 16-byte pieces a (left) and b (right) of a row, lanes
+//    s < 8 keep a of row s and give b to lane s + 8, which gives its a. a then
+//    holds rows 0 .. 7, left in lanes s < 8 and right in lanes s >= 8, b rows 8
+//    .. 15 likewise: 8 rows x 128 bytes an instruction.
+//  * Outputs of 2 bytes first swap lane groups between two neighbouring blocks
+//    (v_permlane16_swap), which gives every lane 8 neighbouring columns: group
+//    g then holds columns 8 (g / 2) .. + 7 of block (g % 2).
+__device__ __forceinline__ void swap_rows(u32x4 &a, u32x4 &b) {
+  constexpr int kRor8 = 0x128;  // lane s reads lane (s + 8) % 16 of its 16
+  const u32x4 a0 = a, b0 = b;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int av = (int)a0[j], bv = (int)b0[j];
+    a[j] = (uint32_t)__builtin_amdgcn_update_dpp(av, bv, kRor8, 0xf, 0xc, false);
+    b[j] = (uint32_t)__builtin_amdgcn_update_dpp(bv, av, kRor8, 0xf, 0x3, false);
+  }
+}
+
 __device__ __forceinline__ u32x2 pack_bf16(f32x4 v) {
   return __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4));
 }
@@ -658,11 +676,33 @@ __device__ __forceinline__ void store_block(const f32x4 (&acc)[C::NI][C::MI], in
   const int g = lane / 16, s = lane % 16;
   const buf_rsrc r = row_block(base, wm0 + mi * 16, rows, row_bytes, col_bytes);
   const uint32_t row = (uint32_t)s * (uint32_t)row_bytes;
-  if constexpr (!BF16) {
+  const uint32_t row8 = (uint32_t)(s % 8) * (uint32_t)row_bytes, down8 = 8u * (uint32_t)row_bytes;
+  if constexpr (!BF16 && C::NI % 2 == 0) {
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ni += 2) {
+      u32x4 a = __builtin_bit_cast(u32x4, acc[ni][mi]), b = __builtin_bit_cast(u32x4, acc[ni + 1][mi]);
+      swap_rows(a, b);
+      const int n = wn0 + (ni + s / 8) * 16 + 4 * g;
+      const uint32_t at = row8 + 4u * n;
+      st_buf16(r, n < ncols ? at : kOob, a);
+      st_buf16(r, n < ncols ? at + down8 : kOob, b);
+    }
+  } else if constexpr (!BF16) {
 #pragma unroll
     for (int ni = 0; ni < C::NI; ++ni) {
       const int n = wn0 + ni * 16 + 4 * g;
       st_buf16(r, n < ncols ? row + 4u * n : kOob, __builtin_bit_cast(u32x4, acc[ni][mi]));
+    }
+  } else if constexpr (C::NI % 4 == 0) {
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ni += 4) {
+      u32x4 a = swap_pair(pack_bf16(acc[ni][mi]), pack_bf16(acc[ni + 1][mi]));
+      u32x4 b = swap_pair(pack_bf16(acc[ni + 2][mi]), pack_bf16(acc[ni + 3][mi]));
+      swap_rows(a, b);
+      const int n = wn0 + (ni + 2 * (s / 8) + g % 2) * 16 + 8 * (g / 2);
+      const uint32_t at = row8 + 2u * n;
+      st_buf16(r, n < ncols ? at : kOob, a);
+      st_buf16(r, n < ncols ? at + down8 : kOob, b);
     }
   } else if constexpr (C::NI % 2 == 0) {
 #pragma unroll
@@ -679,7 +719,5 @@ __device__ __forceinline__ void store_block(const f32x4 (&acc)[C::NI][C::MI], in
     }
   }
 }
-
-__device__ __forceinline__ void st_g16u(void *p, u32x4 v) { *(gbl_u32x4 *)p = v; }
 
 }  // namespace gg

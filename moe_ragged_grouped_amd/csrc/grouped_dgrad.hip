@@ -59,9 +59,14 @@ struct DgradEpi {
     return row_block((const char *)base + row0 * bytes + 4 * (size_t)col0, wm0 + mi * 16, rows,
                      bytes, 4 * (size_t)col0);
   }
+  // Place of this lane's piece of block ni: row s, or (two blocks trading rows,
+  // swap_rows) row s % 8 of left and right, 8 rows further down for odd ni.
+  static constexpr bool kTrade = C::NI % 2 == 0;
   __device__ __forceinline__ uint32_t pair_off(int ni) const {
-    const int n = wn0 + ni * 16 + 4 * (lane / 16);
-    return n < ncols ? (uint32_t)(lane % 16) * 4u * (uint32_t)p.K + 4u * n : kOob;
+    const int g = lane / 16, s = lane % 16;
+    const int n = wn0 + (kTrade ? ni / 2 * 2 + s / 8 : ni) * 16 + 4 * g;
+    const int row = kTrade ? s % 8 + ni % 2 * 8 : s;
+    return n < ncols ? (uint32_t)row * 4u * (uint32_t)p.K + 4u * n : kOob;
   }
   __device__ __forceinline__ void load(int mi) {
     const buf_rsrc r = pairs(p.C, mi);
@@ -84,9 +89,13 @@ struct DgradEpi {
       if (mi + 1 < C::MI) load(mi + 1);
       const buf_rsrc r = pairs(p.out, mi);
       f32x4 h[C::NI][C::MI];
+      u32x4 d[C::NI];
+      if constexpr (kTrade) {
+#pragma unroll
+        for (int ni = 0; ni < C::NI; ni += 2) swap_rows(c[mi % 2][ni], c[mi % 2][ni + 1]);
+      }
 #pragma unroll
       for (int ni = 0; ni < C::NI; ++ni) {
-        u32x4 d;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t w = c[mi % 2][ni][j];
@@ -94,11 +103,16 @@ struct DgradEpi {
           const float sg = sigmoid(gate), dh = acc[ni][mi][j];
           const float act = gate * sg;
           const f32x2 dv = {dh * up * (sg * (1.0f + gate * (1.0f - sg))), dh * act};
-          d[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(dv, bf16x2));
+          d[ni][j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(dv, bf16x2));
           h[ni][mi][j] = act * up;
         }
-        st_buf16(r, pair_off(ni), d);
       }
+      if constexpr (kTrade) {
+#pragma unroll
+        for (int ni = 0; ni < C::NI; ni += 2) swap_rows(d[ni], d[ni + 1]);
+      }
+#pragma unroll
+      for (int ni = 0; ni < C::NI; ++ni) st_buf16(r, pair_off(ni), d[ni]);
       if (p.H != nullptr)
         store_block<C, true>(h, mi, p.H + (size_t)row0 * p.K + col0, wm0, wn0, lane, rows, ncols,
                              p.K * es, col0 * es);

@@ -152,71 +152,63 @@ __device__ __forceinline__ void wg_step(f32x4 (&acc)[C::NI][C::MI], const WgradT
   __builtin_amdgcn_s_setprio(0);
 }
 
-// The expert at position p of the order by size class, largest class first
-// and by index inside a class. Every thread of the workgroup calls this; all
-// workgroups find the same order.
-struct WgradOrder {
-  int count[kMaxExperts / kWave][32];  // experts of a class in each run of 64
-  int expert;
-};
-
 __device__ __forceinline__ int size_class(int rows) { return rows > 0 ? 32 - __builtin_clz(rows) : 0; }
 
-__device__ __forceinline__ int group_rows(const int32_t *off, int e, int M_cap) {
-  return max(0, clamp_off(off, e + 1, M_cap) - clamp_off(off, e, M_cap));
-}
-
-__device__ __forceinline__ int wgrad_expert(WgradOrder &o, const int32_t *__restrict__ off, int E, int M_cap,
-                                   int p) {
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+// The expert at position p of the order by size class (power of two of the
+// row count), largest class first and by index inside a class. Every wave
+// finds it for itself, with votes over 64 experts at a time and no LDS or
+// barrier, as every workgroup pays for it: the first form, which ranked all
+// experts through LDS, took 4.5 us a workgroup.
+__device__ __forceinline__ int wgrad_expert(const int32_t *__restrict__ off, int E, int M_cap, int p,
+                                            int *first, int *rows) {
+  const int lane = threadIdx.x % kWave;
+  constexpr int kRuns = kMaxExperts / kWave;
   const int runs = cdiv(E, kWave);
-  constexpr int kPer = kMaxExperts / kWThreads;  // runs of 64 a wave may own
-  int cls[kPer], rank[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int run = j * kWWaves + wave, e = run * kWave + lane;
-    cls[j] = -1;
-    rank[j] = 0;
-    if (run < runs) {
-      if (e < E) cls[j] = size_class(group_rows(off, e, M_cap));
-      for (int c = 0; c < 32; ++c) {
-        const unsigned long long b = __ballot(cls[j] == c);
-        if (cls[j] == c) rank[j] = __popcll(b & ((1ull << lane) - 1));
-        if (lane == 0) o.count[run][c] = __popcll(b);
+  auto look = [&](int run, int &lo, int &n) {
+    const int e = run * kWave + lane;
+    lo = n = 0;
+    if (e < E) {
+      lo = clamp_off(off, e, M_cap);
+      n = max(clamp_off(off, e + 1, M_cap) - lo, 0);
+    }
+    return e < E ? size_class(n) : -1;
+  };
+  int lo, n;
+  const int cls0 = look(0, lo, n);
+  for (int c = size_class(M_cap); c >= 0; --c) {
+    for (int run = 0; run < runs && run < kRuns; ++run) {
+      const int cls = run == 0 ? cls0 : look(run, lo, n);
+      const unsigned long long has = __ballot(cls == c);
+      const int count = __popcll(has);
+      if (p < count) {
+        if (run == 0) look(0, lo, n);
+        // the p-th lane of the vote
+        const int before = __popcll(has & ((1ull << lane) - 1));
+        const int src = __ffsll((long long)__ballot(cls == c && before == p)) - 1;
+        *first = __builtin_amdgcn_readlane(lo, src);
+        *rows = __builtin_amdgcn_readlane(n, src);
+        return run * kWave + src;
       }
+      p -= count;
     }
   }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    if (cls[j] < 0) continue;
-    const int run = j * kWWaves + wave;
-    int at = rank[j];
-    for (int q = 0; q < runs; ++q) {
-      for (int c = cls[j] + 1; c < 32; ++c) at += o.count[q][c];
-      if (q < run) at += o.count[q][cls[j]];
-    }
-    if (at == p) o.expert = run * kWave + lane;
-  }
-  __syncthreads();
-  return o.expert;
+  *first = *rows = 0;
+  return 0;  // not reached: the classes hold E > p experts
 }
 
 template <class C, WOut O>
 __global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds_dyn[];
   lds_u8 *const lds = (lds_u8 *)lds_dyn;
-  WgradOrder &order = *(WgradOrder *)(lds_dyn + C::LDS_BYTES);
   // tiles of one expert in runs of per_xcd to an XCD (workgroup ids go
   // round-robin to the XCDs), k inner: a run's dC columns stay in one L2
   const int xcd = blockIdx.x % kRingXcds, i = blockIdx.x / kRingXcds;
   const int pos = i / p.per_xcd, local = xcd * p.per_xcd + i % p.per_xcd;
   if (local >= p.tiles) return;
-  const int e = __builtin_amdgcn_readfirstlane(wgrad_expert(order, p.off, p.E, p.M_cap, pos));
+  int r0, rows;
+  const int e = scalar(wgrad_expert(p.off, p.E, p.M_cap, scalar(pos), &r0, &rows));
   const int KT_cols = cdiv(p.K, C::BM);
   const int nt = local / KT_cols, kt = local % KT_cols;
-  const int r0 = __builtin_amdgcn_readfirstlane(clamp_off(p.off, e, p.M_cap));
-  const int rows = __builtin_amdgcn_readfirstlane(group_rows(p.off, e, p.M_cap));
   if (O == WOut::AddF32 && rows == 0) return;  // nothing to add
 
   const int col_k = kt * C::BM, col_n = nt * C::BN;
@@ -253,32 +245,22 @@ __global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
     nxt = nxt + 1 == C::S ? 0 : nxt + 1;
   }
 
-  // lane 16 g + s holds columns 4 g .. 4 g + 3 of row s of every block
-  const int g = lane / 16, s = lane % 16;
-  const size_t base = ((size_t)e * p.K + col_k) * p.N + col_n;
-  const int k_in = p.K - col_k, n_in = p.N - col_n;
+  const int n_in = p.N - col_n;
+  constexpr size_t es = O == WOut::BF16 ? 2 : 4;
+  void *const base = (char *)p.dB + (((size_t)e * p.K + col_k) * p.N + col_n) * es;
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi) {
-    const int m = wm0 + mi * 16 + s;
-    const bool in = m < k_in;
-    if constexpr (O == WOut::BF16) {
-#pragma unroll
-      for (int ni = 0; ni < C::NI; ni += 2) {
-        const u32x4 v = swap_pair(pack_bf16(acc[ni][mi]), pack_bf16(acc[ni + 1][mi]));
-        const int n = wn0 + (ni + g % 2) * 16 + 8 * (g / 2);
-        if (in && n < n_in) st_g16u((uint16_t *)p.dB + base + (size_t)m * p.N + n, v);
-      }
-    } else {
+    if constexpr (O == WOut::AddF32) {
+      const buf_rsrc r = row_block(base, wm0 + mi * 16, p.K - col_k, p.N * es, col_n * es);
 #pragma unroll
       for (int ni = 0; ni < C::NI; ++ni) {
-        const int n = wn0 + ni * 16 + 4 * g;
-        float *const at = (float *)p.dB + base + (size_t)m * p.N + n;
-        if (in && n < n_in) {
-          if constexpr (O == WOut::AddF32) st_g16(at, acc[ni][mi] + ld_g16f(at));
-          else st_g16(at, acc[ni][mi]);
-        }
+        const int n = wn0 + ni * 16 + 4 * (lane / 16);
+        const uint32_t at = n < n_in ? (uint32_t)(lane % 16) * (uint32_t)(p.N * es) + 4u * n : kOob;
+        acc[ni][mi] += __builtin_bit_cast(f32x4, ld_buf16(r, at, 0));
       }
     }
+    store_block<C, O == WOut::BF16>(acc, mi, base, wm0, wn0, lane, p.K - col_k, n_in, p.N * es,
+                                    col_n * es);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -286,11 +268,11 @@ __global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
 using W128 = WgradCfg<128, 256, 2, 2, 32, 3>;  // wave tile 64 x 128
 using W64 = WgradCfg<64, 64, 2, 2, 32, 4>;     // wave tile 32 x 32
 
-static_assert(2 * (W128::LDS_BYTES + (int)sizeof(WgradOrder)) <= 160 * 1024, "two workgroups a CU");
+static_assert(2 * W128::LDS_BYTES <= 160 * 1024, "two workgroups a CU");
 
 template <class C, WOut O>
 static gg_status_t launch_wgrad(WgradParams p, hipStream_t stream) {
-  constexpr int lds = C::LDS_BYTES + (int)sizeof(WgradOrder);
+  constexpr int lds = C::LDS_BYTES;
   const long long tiles = ((p.K + (long long)C::BM - 1) / C::BM) * ((p.N + (long long)C::BN - 1) / C::BN);
   const long long per = (tiles + kRingXcds - 1) / kRingXcds;
   const long long grid = per * kRingXcds * p.E;
