@@ -398,23 +398,23 @@ def grouped_gemm_fp8_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
 
 # ---- gradients and 4-bit operators
 
-def _device_args(what, **tensors):
-    """Checks that every tensor (name=(tensor, dtypes, dims)) is contiguous, of
-    one of its dtypes and of its rank, and that all are on one device; returns
-    that device."""
-    dev = None
-    for name, (t, dtypes, dims) in tensors.items():
-        if t.dtype not in dtypes:
-            raise TypeError("%s: %s must be %s" % (what, name, " or ".join(str(d) for d in dtypes)))
+def _device_args(what, *tensors):
+    """Checks that every (name, tensor, dtype, rank) is a contiguous device
+    tensor of its dtype and rank, all on one device; returns that device."""
+    for name, t, dtype, dims in tensors:
+        if t.dtype is not dtype:
+            raise TypeError("%s: %s must be %s" % (what, name, dtype))
         if t.dim() != dims:
             raise ValueError("%s: %s must have %d dimensions, not %d" % (what, name, dims, t.dim()))
-    for name, (t, _, _) in tensors.items():
+    index = None
+    for name, t, _, _ in tensors:
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("%s: %s must be a contiguous device tensor" % (what, name))
-        if dev is not None and t.device != dev:
-            raise ValueError("%s: tensors are on %s and %s" % (what, dev, t.device))
-        dev = t.device
-    return dev
+        if index is None:
+            index = t.get_device()
+        elif t.get_device() != index:
+            raise ValueError("%s: %s is on device %d, others on %d" % (what, name, t.get_device(), index))
+    return tensors[0][1].device
 
 
 def _match(what, ok, *tensors):
@@ -422,22 +422,23 @@ def _match(what, ok, *tensors):
         raise ValueError("%s: shape mismatch: %s" % (what, ", ".join(str(tuple(t.shape)) for t in tensors)))
 
 
-def _out(what, out, shape, dtypes, dtype, dev, stream):
+def _out(what, out, shape, dtypes, dtype, like, stream):
     """The given output, checked, or a new one of ``dtype`` (default: the first
-    of ``dtypes``) whose memory belongs to the stream that writes it."""
-    import torch
+    of ``dtypes``) beside ``like``, its memory belonging to the stream that
+    writes it."""
     if dtype is not None and dtype not in dtypes:
         raise TypeError("%s: out_dtype must be %s" % (what, " or ".join(str(d) for d in dtypes)))
     if out is None:
         dtype = dtypes[0] if dtype is None else dtype
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
+            return like.new_empty(shape, dtype=dtype)
+        import torch
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=dev)
-    if (out.dtype not in dtypes or (dtype is not None and out.dtype != dtype)
-            or tuple(out.shape) != tuple(shape) or not out.is_contiguous() or out.device != dev):
+            return like.new_empty(shape, dtype=dtype)
+    if (out.dtype not in dtypes or (dtype is not None and out.dtype is not dtype)
+            or out.shape != shape or not out.is_contiguous() or out.device != like.device):
         raise ValueError("%s: out must be a contiguous %s %s tensor on %s" % (
-            what, " or ".join(str(d) for d in ([dtype] if dtype else dtypes)), list(shape), dev))
+            what, " or ".join(str(d) for d in ([dtype] if dtype else dtypes)), list(shape), like.device))
     return out
 
 
@@ -445,13 +446,19 @@ def _call(name, dev, stream, *args):
     """Calls one entry point on the tensors' device, whichever is current."""
     import torch
     fn = getattr(load_library(), name)
-    if stream is not None and stream.device != dev:
-        raise ValueError("%s: the stream is on %s, the tensors on %s" % (name, stream.device, dev))
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("%s: the stream is on %s, the tensors on %s" % (name, stream.device, dev))
+        handle = stream.cuda_stream
+    else:  # torch's current stream as a number: the Stream object costs 2 us
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, _stream_handle(dev, stream)), name)
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream_handle(dev, stream)), name)
+            st = fn(*args, handle)
+    if st != 0:
+        _check(st, name)
 
 
 def _ptr(t):
@@ -469,12 +476,12 @@ def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_d
     """
     import torch
     what = "grouped_gemm_dgrad"
-    dev = _device_args(what, dC=(dC, (torch.bfloat16,), 2), B=(B, (torch.bfloat16,), 3),
-                       offsets=(offsets, (torch.int32,), 1))
+    dev = _device_args(what, ("dC", dC, torch.bfloat16, 2), ("B", B, torch.bfloat16, 3),
+                       ("offsets", offsets, torch.int32, 1))
     E, K, N = B.shape
     M_cap = dC.shape[0]
     _match(what, dC.shape[1] == N and offsets.shape[0] == E + 1, dC, B, offsets)
-    out = _out(what, out, (M_cap, K), (torch.float32, torch.bfloat16), out_dtype, dev, stream)
+    out = _out(what, out, (M_cap, K), (torch.float32, torch.bfloat16), out_dtype, dC, stream)
     name = "gg_grouped_gemm_bf16_dgrad" + ("" if out.dtype == torch.float32 else "_bf16out")
     _call(name, dev, stream, dC.data_ptr(), B.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K,
           N, M_cap, int(bm))
@@ -495,17 +502,17 @@ def grouped_gemm_dgrad_swiglu(dY, B, offsets, C, out=None, out_h=None, with_h: b
     """
     import torch
     what = "grouped_gemm_dgrad_swiglu"
-    bf = (torch.bfloat16,)
-    dev = _device_args(what, dY=(dY, bf, 2), B=(B, bf, 3), offsets=(offsets, (torch.int32,), 1),
-                       C=(C, bf, 2))
+    bf = torch.bfloat16
+    dev = _device_args(what, ("dY", dY, bf, 2), ("B", B, bf, 3), ("offsets", offsets, torch.int32, 1),
+                       ("C", C, bf, 2))
     E, K, N = B.shape
     M_cap = dY.shape[0]
     _match(what, dY.shape[1] == N and offsets.shape[0] == E + 1
-           and tuple(C.shape) == (M_cap, 2 * K), dY, B, offsets, C)
-    out = _out(what, out, (M_cap, 2 * K), bf, None, dev, stream)
+           and C.shape == (M_cap, 2 * K), dY, B, offsets, C)
+    out = _out(what, out, (M_cap, 2 * K), (bf,), None, dY, stream)
     h = None
     if with_h or out_h is not None:
-        h = _out(what, out_h, (M_cap, K), bf, None, dev, stream)
+        h = _out(what, out_h, (M_cap, K), (bf,), None, dY, stream)
     _call("gg_grouped_gemm_bf16_dgrad_swiglu", dev, stream, dY.data_ptr(), B.data_ptr(),
           offsets.data_ptr(), C.data_ptr(), out.data_ptr(), _ptr(h), E, K, N, M_cap, int(bm))
     return out if h is None else (out, h)
@@ -524,15 +531,15 @@ def grouped_gemm_wgrad(A, dC, offsets, out=None, accumulate: bool = False, strea
     """
     import torch
     what = "grouped_gemm_wgrad"
-    dev = _device_args(what, A=(A, (torch.bfloat16,), 2), dC=(dC, (torch.bfloat16,), 2),
-                       offsets=(offsets, (torch.int32,), 1))
+    dev = _device_args(what, ("A", A, torch.bfloat16, 2), ("dC", dC, torch.bfloat16, 2),
+                       ("offsets", offsets, torch.int32, 1))
     M_cap, K = A.shape
     N = dC.shape[1]
     E = offsets.shape[0] - 1
     _match(what, dC.shape[0] == M_cap and E >= 1, A, dC, offsets)
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("%s: accumulate needs an fp32 out to add to" % what)
-    out = _out(what, out, (E, K, N), (torch.float32, torch.bfloat16), out_dtype, dev, stream)
+    out = _out(what, out, (E, K, N), (torch.float32, torch.bfloat16), out_dtype, A, stream)
     args = (A.data_ptr(), dC.data_ptr(), offsets.data_ptr(), out.data_ptr())
     if out.dtype == torch.float32:
         _call("gg_grouped_gemm_bf16_wgrad", dev, stream, *args, int(accumulate), E, K, N, M_cap)
@@ -557,11 +564,11 @@ def mx4_quantize(X, out=None, out_scale=None, stream=None):
     """
     import torch
     what = "mx4_quantize"
-    dev = _device_args(what, X=(X, (torch.bfloat16,), 2))
+    dev = _device_args(what, ("X", X, torch.bfloat16, 2))
     M, K = X.shape
     u8 = (torch.uint8,)
-    q = _out(what, out, (M, K // 2), u8, None, dev, stream)
-    s = _out(what, out_scale, (_mx4_slices(K), M, 8), u8, None, dev, stream)
+    q = _out(what, out, (M, K // 2), u8, None, X, stream)
+    s = _out(what, out_scale, (_mx4_slices(K), M, 8), u8, None, X, stream)
     _call("gg_mx4_quantize", dev, stream, X.data_ptr(), q.data_ptr(), s.data_ptr(), M, K)
     return q, s
 
@@ -574,11 +581,11 @@ def mx4_quantize_weights(B, out=None, out_scale=None, stream=None):
     """
     import torch
     what = "mx4_quantize_weights"
-    dev = _device_args(what, B=(B, (torch.bfloat16,), 3))
+    dev = _device_args(what, ("B", B, torch.bfloat16, 3))
     E, K, N = B.shape
     u8 = (torch.uint8,)
-    q = _out(what, out, (E, N, K // 2), u8, None, dev, stream)
-    s = _out(what, out_scale, (E, _mx4_slices(K), N, 8), u8, None, dev, stream)
+    q = _out(what, out, (E, N, K // 2), u8, None, B, stream)
+    s = _out(what, out_scale, (E, _mx4_slices(K), N, 8), u8, None, B, stream)
     _call("gg_mx4_quantize_weights", dev, stream, B.data_ptr(), q.data_ptr(), s.data_ptr(), E, K, N)
     return q, s
 
@@ -591,15 +598,14 @@ def mx4_dequantize(q, scales, out=None, stream=None):
     """
     import torch
     what = "mx4_dequantize"
-    u8 = (torch.uint8,)
     if q.dim() not in (2, 3):
         raise ValueError("%s: codes are [M, K/2] or [E, N, K/2]" % what)
-    dev = _device_args(what, q=(q, u8, q.dim()), scales=(scales, u8, q.dim() + 1))
+    dev = _device_args(what, ("q", q, torch.uint8, q.dim()), ("scales", scales, torch.uint8, q.dim() + 1))
     batch = q.shape[0] if q.dim() == 3 else 1
     rows, K = q.shape[-2], 2 * q.shape[-1]
     lead = (batch,) if q.dim() == 3 else ()
-    _match(what, tuple(scales.shape) == lead + (_mx4_slices(K), rows, 8), q, scales)
-    y = _out(what, out, lead + (rows, K), (torch.bfloat16,), None, dev, stream)
+    _match(what, scales.shape == lead + (_mx4_slices(K), rows, 8), q, scales)
+    y = _out(what, out, lead + (rows, K), (torch.bfloat16,), None, q, stream)
     _call("gg_mx4_dequantize", dev, stream, q.data_ptr(), scales.data_ptr(), y.data_ptr(), batch,
           rows, K)
     return y
@@ -607,14 +613,14 @@ def mx4_dequantize(q, scales, out=None, stream=None):
 
 def _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets):
     import torch
-    u8 = (torch.uint8,)
-    dev = _device_args(what, Aq=(Aq, u8, 2), a_scale=(a_scale, u8, 3), Bq=(Bq, u8, 3),
-                       b_scale=(b_scale, u8, 4), offsets=(offsets, (torch.int32,), 1))
+    u8 = torch.uint8
+    dev = _device_args(what, ("Aq", Aq, u8, 2), ("a_scale", a_scale, u8, 3), ("Bq", Bq, u8, 3),
+                       ("b_scale", b_scale, u8, 4), ("offsets", offsets, torch.int32, 1))
     E, N, half = Bq.shape
     M_cap, K = Aq.shape[0], 2 * half
     _match(what, Aq.shape[1] == half and offsets.shape[0] == E + 1
-           and tuple(a_scale.shape) == (_mx4_slices(K), M_cap, 8)
-           and tuple(b_scale.shape) == (E, _mx4_slices(K), N, 8), Aq, a_scale, Bq, b_scale, offsets)
+           and a_scale.shape == (_mx4_slices(K), M_cap, 8)
+           and b_scale.shape == (E, _mx4_slices(K), N, 8), Aq, a_scale, Bq, b_scale, offsets)
     return dev, E, K, N, M_cap
 
 
@@ -631,7 +637,7 @@ def grouped_gemm_mx4(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, s
     import torch
     what = "grouped_gemm_mx4"
     dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets)
-    out = _out(what, out, (M_cap, N), (torch.float32, torch.bfloat16), out_dtype, dev, stream)
+    out = _out(what, out, (M_cap, N), (torch.float32, torch.bfloat16), out_dtype, Aq, stream)
     name = "gg_grouped_gemm_mx4" + ("" if out.dtype == torch.float32 else "_bf16out")
     _call(name, dev, stream, Aq.data_ptr(), a_scale.data_ptr(), Bq.data_ptr(), b_scale.data_ptr(),
           offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap, int(bm))
@@ -647,7 +653,7 @@ def grouped_gemm_mx4_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
     import torch
     what = "grouped_gemm_mx4_swiglu"
     dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets)
-    out = _out(what, out, (M_cap, N // 2), (torch.bfloat16,), None, dev, stream)
+    out = _out(what, out, (M_cap, N // 2), (torch.bfloat16,), None, Aq, stream)
     _call("gg_grouped_gemm_mx4_swiglu", dev, stream, Aq.data_ptr(), a_scale.data_ptr(),
           Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap,
           int(bm))

@@ -657,8 +657,9 @@ __device__ __forceinline__ buf_rsrc row_block(const void *base, int m0, int rows
                   n > 0 ? (uint32_t)((size_t)n * row_bytes - col_bytes) : 0u);
 }
 
+template <int POLICY = kCacheDefault>
 __device__ __forceinline__ void st_buf16(buf_rsrc r, uint32_t off, u32x4 v) {
-  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, POLICY);
 }
 __device__ __forceinline__ void st_buf8(buf_rsrc r, uint32_t off, u32x2 v) {
   __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, 0);
@@ -669,7 +670,7 @@ __device__ __forceinline__ void st_buf4(buf_rsrc r, uint32_t off, uint32_t v) {
 
 // One row block of a wave tile as fp32 or bf16. row_bytes: of a row of the
 // output; base: its first row and column of the tile; ncols: valid columns.
-template <class C, bool BF16>
+template <class C, bool BF16, int POLICY = kCacheDefault>
 __device__ __forceinline__ void store_block(const f32x4 (&acc)[C::NI][C::MI], int mi, void *base,
                                             int wm0, int wn0, int lane, int rows, int ncols,
                                             size_t row_bytes, size_t col_bytes) {
@@ -684,14 +685,14 @@ __device__ __forceinline__ void store_block(const f32x4 (&acc)[C::NI][C::MI], in
       swap_rows(a, b);
       const int n = wn0 + (ni + s / 8) * 16 + 4 * g;
       const uint32_t at = row8 + 4u * n;
-      st_buf16(r, n < ncols ? at : kOob, a);
-      st_buf16(r, n < ncols ? at + down8 : kOob, b);
+      st_buf16<POLICY>(r, n < ncols ? at : kOob, a);
+      st_buf16<POLICY>(r, n < ncols ? at + down8 : kOob, b);
     }
   } else if constexpr (!BF16) {
 #pragma unroll
     for (int ni = 0; ni < C::NI; ++ni) {
       const int n = wn0 + ni * 16 + 4 * g;
-      st_buf16(r, n < ncols ? row + 4u * n : kOob, __builtin_bit_cast(u32x4, acc[ni][mi]));
+      st_buf16<POLICY>(r, n < ncols ? row + 4u * n : kOob, __builtin_bit_cast(u32x4, acc[ni][mi]));
     }
   } else if constexpr (C::NI % 4 == 0) {
 #pragma unroll
@@ -701,14 +702,14 @@ __device__ __forceinline__ void store_block(const f32x4 (&acc)[C::NI][C::MI], in
       swap_rows(a, b);
       const int n = wn0 + (ni + 2 * (s / 8) + g % 2) * 16 + 8 * (g / 2);
       const uint32_t at = row8 + 2u * n;
-      st_buf16(r, n < ncols ? at : kOob, a);
-      st_buf16(r, n < ncols ? at + down8 : kOob, b);
+      st_buf16<POLICY>(r, n < ncols ? at : kOob, a);
+      st_buf16<POLICY>(r, n < ncols ? at + down8 : kOob, b);
     }
   } else if constexpr (C::NI % 2 == 0) {
 #pragma unroll
     for (int ni = 0; ni < C::NI; ni += 2) {
       const int n = wn0 + (ni + g % 2) * 16 + 8 * (g / 2);
-      st_buf16(r, n < ncols ? row + 2u * n : kOob,
+      st_buf16<POLICY>(r, n < ncols ? row + 2u * n : kOob,
                swap_pair(pack_bf16(acc[ni][mi]), pack_bf16(acc[ni + 1][mi])));
     }
   } else {

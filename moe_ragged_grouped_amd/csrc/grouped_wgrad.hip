@@ -248,6 +248,12 @@ __global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
   const int n_in = p.N - col_n;
   constexpr size_t es = O == WOut::BF16 ? 2 : 4;
   void *const base = (char *)p.dB + (((size_t)e * p.K + col_k) * p.N + col_n) * es;
+  // The gradient is written once and far larger than what was read: stores of
+  // whole lines go out as streaming data, so that they do not displace the
+  // rows that the tiles of an expert share (64 x 256 rows, K = 1024, N = 2688:
+  // 250 -> 211 us in fp32, 167 -> 138 in bf16). Parts of lines are held back
+  // in the cache until the rest comes (streamed they halve the write rate).
+  const bool whole = (p.N * es) % 128 == 0 && (uintptr_t)p.dB % 128 == 0;
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi) {
     if constexpr (O == WOut::AddF32) {
@@ -259,8 +265,12 @@ __global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
         acc[ni][mi] += __builtin_bit_cast(f32x4, ld_buf16(r, at, 0));
       }
     }
-    store_block<C, O == WOut::BF16>(acc, mi, base, wm0, wn0, lane, p.K - col_k, n_in, p.N * es,
-                                    col_n * es);
+    if (whole)
+      store_block<C, O == WOut::BF16, kCacheStream>(acc, mi, base, wm0, wn0, lane, p.K - col_k, n_in,
+                                                    p.N * es, col_n * es);
+    else
+      store_block<C, O == WOut::BF16>(acc, mi, base, wm0, wn0, lane, p.K - col_k, n_in, p.N * es,
+                                      col_n * es);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
