@@ -405,9 +405,9 @@ gg_status_t gg_mx4_quantize(const void *X, void *q, void *scales, int64_t rows, 
 /*
  * gg_mx4_quantize_weights -- B bf16 [E][K][N] (the layout of the bf16 product)
  * to codes [E][N][K/2] and scales [E][ceil(K/256)][N][8], blocks along K, by the
- * rule of gg_mx4_quantize. N is a multiple of 8, at most GG_MAX_MX4_WEIGHT_N.
+ * rule of gg_mx4_quantize. N is a multiple of 8, at most GG_MAX_N; E * K * N at
+ * most 2^46.
  */
-#define GG_MAX_MX4_WEIGHT_N (65535 * 256)
 gg_status_t gg_mx4_quantize_weights(const void *B, void *q, void *scales, int32_t E, int32_t K,
                                     int32_t N, void *stream);
 

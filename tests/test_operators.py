@@ -169,7 +169,7 @@ def test_mx4_row_host_checks(lib):
     w = lambda B=16, c=32, s=48, E=2, K=64, N=8: lib.gg_mx4_quantize_weights(B, c, s, E, K, N, None)  # noqa: E731
     assert w(B=0) == w(c=0) == w(s=0) == w(E=0) == w(K=0) == w(N=-8) == INVALID
     assert w(B=24) == w(c=40) == w(s=52) == w(K=40) == w(N=12) == MISALIGNED
-    assert w(E=1025) == w(K=2 ** 22 + 32) == w(N=65535 * 256 + 8) == UNSUPPORTED
+    assert w(E=1025) == w(K=2 ** 22 + 32) == w(N=2 ** 24 + 8) == w(E=1024, K=2 ** 22, N=2 ** 24) == UNSUPPORTED
     d = lambda c=16, s=32, Y=48, b=2, rows=3, K=64: lib.gg_mx4_dequantize(c, s, Y, b, rows, K, None)  # noqa: E731
     assert d(c=0) == d(s=0) == d(Y=0) == d(b=-1) == d(rows=-1) == d(K=0) == INVALID
     assert d(c=24) == d(s=40) == d(Y=56) == d(K=40) == MISALIGNED
