@@ -155,45 +155,52 @@ __device__ __forceinline__ void wg_step(f32x4 (&acc)[C::NI][C::MI], const WgradT
 __device__ __forceinline__ int size_class(int rows) { return rows > 0 ? 32 - __builtin_clz(rows) : 0; }
 
 // The expert at position p of the order by size class (power of two of the
-// row count), largest class first and by index inside a class. Every wave
-// finds it for itself, with votes over 64 experts at a time and no LDS or
-// barrier, as every workgroup pays for it: the first form, which ranked all
-// experts through LDS, took 4.5 us a workgroup.
-__device__ __forceinline__ int wgrad_expert(const int32_t *__restrict__ off, int E, int M_cap, int p,
-                                            int *first, int *rows) {
+// row count), largest class first and by index inside a class; *first and
+// *rows are its rows. Every wave finds it for itself, with votes over RUNS x
+// 64 experts and no LDS or barrier, as every workgroup pays for it: the first
+// form, which ranked all experts through LDS, took 4.5 us a workgroup.
+template <int RUNS>
+__device__ __forceinline__ int find_expert(const int32_t *__restrict__ off, int E, int M_cap, int p,
+                                           int *first, int *rows) {
   const int lane = threadIdx.x % kWave;
-  constexpr int kRuns = kMaxExperts / kWave;
-  const int runs = cdiv(E, kWave);
-  auto look = [&](int run, int &lo, int &n) {
-    const int e = run * kWave + lane;
-    lo = n = 0;
-    if (e < E) {
-      lo = clamp_off(off, e, M_cap);
-      n = max(clamp_off(off, e + 1, M_cap) - lo, 0);
-    }
-    return e < E ? size_class(n) : -1;
-  };
-  int lo, n;
-  const int cls0 = look(0, lo, n);
+  int lo[RUNS], n[RUNS], cls[RUNS];
+#pragma unroll
+  for (int r = 0; r < RUNS; ++r) {  // all loads in flight together
+    const int e = min(r * kWave + lane, E - 1);
+    lo[r] = off[e];
+    n[r] = off[e + 1];
+  }
+#pragma unroll
+  for (int r = 0; r < RUNS; ++r) {
+    lo[r] = min(max(lo[r], 0), M_cap);
+    n[r] = max(min(max(n[r], 0), M_cap) - lo[r], 0);
+    cls[r] = r * kWave + lane < E ? size_class(n[r]) : -1;
+  }
   for (int c = size_class(M_cap); c >= 0; --c) {
-    for (int run = 0; run < runs && run < kRuns; ++run) {
-      const int cls = run == 0 ? cls0 : look(run, lo, n);
-      const unsigned long long has = __ballot(cls == c);
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      const unsigned long long has = __ballot(cls[r] == c);
       const int count = __popcll(has);
-      if (p < count) {
-        if (run == 0) look(0, lo, n);
+      if (p >= 0 && p < count) {
         // the p-th lane of the vote
         const int before = __popcll(has & ((1ull << lane) - 1));
-        const int src = __ffsll((long long)__ballot(cls == c && before == p)) - 1;
-        *first = __builtin_amdgcn_readlane(lo, src);
-        *rows = __builtin_amdgcn_readlane(n, src);
-        return run * kWave + src;
+        const int src = __ffsll((long long)__ballot(cls[r] == c && before == p)) - 1;
+        *first = __builtin_amdgcn_readlane(lo[r], src);
+        *rows = __builtin_amdgcn_readlane(n[r], src);
+        return r * kWave + src;
       }
       p -= count;
     }
   }
   *first = *rows = 0;
   return 0;  // not reached: the classes hold E > p experts
+}
+
+__device__ __forceinline__ int wgrad_expert(const int32_t *off, int E, int M_cap, int p, int *first,
+                                            int *rows) {
+  if (E <= kWave) return find_expert<1>(off, E, M_cap, p, first, rows);
+  if (E <= 4 * kWave) return find_expert<4>(off, E, M_cap, p, first, rows);
+  return find_expert<kMaxExperts / kWave>(off, E, M_cap, p, first, rows);
 }
 
 template <class C, WOut O>
@@ -253,7 +260,8 @@ __global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
   // rows that the tiles of an expert share (64 x 256 rows, K = 1024, N = 2688:
   // 250 -> 211 us in fp32, 167 -> 138 in bf16). Parts of lines are held back
   // in the cache until the rest comes (streamed they halve the write rate).
-  const bool whole = (p.N * es) % 128 == 0 && (uintptr_t)p.dB % 128 == 0;
+  constexpr bool kLines = C::NI % (O == WOut::BF16 ? 4 : 2) == 0;  // store_block's whole lines
+  const bool whole = kLines && (p.N * es) % 128 == 0 && (uintptr_t)p.dB % 128 == 0;
 #pragma unroll
   for (int mi = 0; mi < C::MI; ++mi) {
     if constexpr (O == WOut::AddF32) {

@@ -226,6 +226,59 @@ def test_wgrad_many_experts_and_ties(gg):
     assert (got == want).all()
 
 
+@pytest.mark.parametrize("E", [64, 65, 200, 256, 257])
+def test_wgrad_expert_counts(gg, E):
+    # one, two and more votes of 64 experts; large tiles
+    sizes = np.random.default_rng(E).integers(0, 20, size=E)
+    sizes[E // 2] = 300
+    got, want, _ = _wgrad_case(gg, sizes.tolist(), 256, 264, "fp32", 305, draw=ops.int_bits)
+    assert (got == want).all()
+
+
+@pytest.mark.parametrize("N", [256, 264])
+@pytest.mark.parametrize("out", DTYPES)
+def test_wgrad_output_off_a_line(gg, N, out):
+    # a gradient that starts 16 bytes into a line, as a part of a larger buffer
+    # does, with and without accumulation; its surroundings stay as they were
+    rng = np.random.default_rng(N)
+    sizes, K = [33, 0, 90] * 30, 136
+    off = ops.offsets_of(sizes)
+    A, dC = ops.int_bits(rng, int(off[-1]), K), ops.int_bits(rng, int(off[-1]), N)
+    want, _ = ref.wgrad(A, dC, off)
+    n, pad = want.size, 16 // _dt(out).itemsize
+    buf = torch.full((n + 2 * pad,), 3.0, dtype=_dt(out), device="cuda:0")
+    view = buf[pad:pad + n].view(want.shape)
+    assert view.data_ptr() % 128 == 16
+    args = [ops.to_dev(t) for t in (A, dC, off)]
+    gg.grouped_gemm_wgrad(*args, out=view)
+    got = ops.host(view)
+    assert (got == (want if out == "fp32" else oracle.round_to_bf16(want))).all()
+    if out == "fp32":
+        gg.grouped_gemm_wgrad(*args, out=view, accumulate=True)
+        assert (ops.host(view) == 2 * want).all()
+    assert (buf[:pad] == 3).all() and (buf[-pad:] == 3).all()
+
+
+def test_rows_beyond_4_gigabytes(gg):
+    # the last group's rows lie past 2^32 bytes of dC and past 2^31 of dA
+    M, N, K, last = 560_000, 4096, 64, 70
+    off = torch.tensor([0, M - last, M], dtype=torch.int32, device="cuda:0")
+    rng = np.random.default_rng(14)
+    dC = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda:0")
+    A = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda:0")
+    tail, a_tail, B = ops.int_bits(rng, last, N), ops.int_bits(rng, last, K), ops.int_bits(rng, 2, K, N)
+    dC[M - last:] = ops.to_dev(tail)
+    A[M - last:] = ops.to_dev(a_tail)
+    want, _ = ref.dgrad(tail, B[1:], np.array([0, last]))
+    for bm in (0, 16):
+        got = gg.grouped_gemm_dgrad(dC, ops.to_dev(B), off, bm=bm)
+        assert (ops.host(got[M - last:]) == want).all() and not got[:M - last].any()
+    dB = ops.host(gg.grouped_gemm_wgrad(A, dC, off))
+    assert (dB[1] == ref.wgrad(a_tail, tail, np.array([0, last]))[0][0]).all() and (dB[0] == 0).all()
+    del dC, A, got
+    torch.cuda.empty_cache()
+
+
 def test_wgrad_neighbours_rows_stay_out(gg):
     # NaN in an expert's rows reaches that expert's gradient only
     rng = np.random.default_rng(6)
@@ -346,6 +399,29 @@ def test_graph_replays_follow_the_offsets(gg):
         torch.cuda.synchronize()
         for got, want in zip(outs, step()):
             assert torch.equal(got, want)
+
+
+def test_two_streams_at_once(gg):
+    rng = np.random.default_rng(15)
+    sets = []
+    for seed in range(2):
+        off = ops.to_dev(ops.offsets_of([500 + seed, 12, 90]))
+        A, dC = ops.to_dev(ops.bits(rng, 602 + seed, 264)), ops.to_dev(ops.bits(rng, 602 + seed, 1032))
+        B, C = ops.to_dev(ops.bits(rng, 3, 264, 1032)), ops.to_dev(ops.bits(rng, 602 + seed, 528))
+        sets.append((A, dC, B, off, C))
+
+    def step(A, dC, B, off, C, s=None):
+        return (gg.grouped_gemm_dgrad(dC, B, off, stream=s), gg.grouped_gemm_wgrad(A, dC, off, stream=s),
+                *gg.grouped_gemm_dgrad_swiglu(dC, B, off, C, with_h=True, stream=s))
+
+    want = [step(*x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[step(*x, s=s) for x, s in zip(sets, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for turn in got:
+        for g, w in zip(turn, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
 
 
 def test_other_stream(gg):

@@ -210,6 +210,42 @@ def test_malformed_offsets_stay_inside(gg, offs):
         assert (buf[:32] == -7).all() and (buf[-32:] == -7).all()
 
 
+def test_swiglu_last_columns(gg):
+    # 8 columns past a block of 16 in every place of a wave's 64
+    for N in (8, 24, 40, 56, 72, 264, 280, 296, 312):
+        off, Aq, a_s, Bq, b_s = _codes(np.random.default_rng(N), [300, 5], 96, N, spare=1)
+        dev = [ops.to_dev(t) for t in (Aq, a_s, Bq, b_s, off)]
+        want, S = (t[:305] for t in ref.mx4_product(Aq, a_s, Bq, b_s, off))
+        for bm in (0, 256):
+            buf = torch.full((306 * (N // 2) + 16,), -7.0, dtype=torch.bfloat16, device="cuda:0")
+            gg.grouped_gemm_mx4_swiglu(*dev, out=buf[:306 * (N // 2)].view(306, N // 2), bm=bm)
+            got = ops.host(buf)
+            parity.check_swiglu_bf16(got[:305 * (N // 2)].reshape(305, -1), want, S, "N=%d" % N,
+                                     err=ops.sum_bound(3, S))
+            assert (got[305 * (N // 2):] == -7).all()
+
+
+def test_rows_beyond_4_gigabytes(gg):
+    # the last group's codes lie past 2^32 bytes, a slice's scales 2^24 apart
+    M, K, N, last = 2_150_000, 4096, 24, 40
+    rng = np.random.default_rng(9)
+    off, tq, ts, Bq, b_s = _codes(rng, [last, 0], K, N, 126, 129, spare=0)
+    Aq = torch.zeros((M, K // 2), dtype=torch.uint8, device="cuda:0")
+    a_s = torch.full((K // 256, M, 8), 127, dtype=torch.uint8, device="cuda:0")
+    Aq[M - last:] = ops.to_dev(tq)
+    a_s[:, M - last:] = ops.to_dev(ts)
+    offs = torch.tensor([0, M - last, M], dtype=torch.int32, device="cuda:0")
+    got = gg.grouped_gemm_mx4(Aq, a_s, ops.to_dev(Bq[::-1].copy()), ops.to_dev(b_s[::-1].copy()), offs)
+    want, _ = ref.mx4_product(tq, ts, Bq, b_s, off)
+    assert (ops.host(got[M - last:]) == want).all() and not got[:M - last].any()
+    # and there and back through the quantiser
+    back = gg.mx4_quantize(gg.mx4_dequantize(Aq, a_s))
+    tail = gg.mx4_quantize(gg.mx4_dequantize(ops.to_dev(tq), ops.to_dev(ts)))
+    assert torch.equal(back[0][M - last:], tail[0]) and torch.equal(back[1][:, M - last:], tail[1])
+    del Aq, a_s, got, back
+    torch.cuda.empty_cache()
+
+
 def test_serving_a_layer(gg):
     # a layer's weights laid out once, then rows through quantise -> gate/up with
     # SwiGLU -> quantise -> down, against the same steps in binary64
