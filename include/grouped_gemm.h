@@ -360,8 +360,8 @@ gg_status_t gg_grouped_gemm_bf16_dgrad_swiglu(const void *dY, const void *B,
  *       gg_grouped_gemm_bf16).
  *   K and N are multiples of 8, at most GG_MAX_K; E in [1, GG_MAX_EXPERTS];
  *   M_cap in [0, 2^31 - 257].
- * The sum over an expert's rows is taken in fp32 in the matrix cores, in the
- * order of the rows: no atomics, so equal inputs give equal bits.
+ * The sum over an expert's rows is taken in fp32 in the matrix cores, in an
+ * order that the sizes fix: no atomics, so equal inputs give equal bits.
  */
 gg_status_t gg_grouped_gemm_bf16_wgrad(const void *A, const void *dC,
                                        const int32_t *group_offsets, float *dB,

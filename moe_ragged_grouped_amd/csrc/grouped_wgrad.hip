@@ -11,8 +11,7 @@
 // The buffers end at the group's last row, so the rows of a slice past it
 // read as zeros in both operands.
 //
-// One workgroup per tile, four waves, two workgroups to a CU: while one
-// stores its tile the other multiplies. The tiles of all experts number
+// One workgroup per tile, four waves, two workgroups to a CU. The tiles of all experts number
 // E * ceil(K / BM) * ceil(N / BN) whatever the routing, so the grid is known on
 // the host and the hardware hands the next tile to whichever CU is free. A
 // launch ends with its longest tile, so experts come in the order of their
@@ -37,41 +36,43 @@ struct WgradParams {
   int per_xcd;      // ceil(tiles / 8)
 };
 
-constexpr int kWThreads = 256;
-constexpr int kWWaves = kWThreads / kWave;
-
-template <int BM_, int BN_, int WM_, int WN_, int RB_, int S_>
+// R > 1: R groups of waves share a tile's rows (slice k to group k % R), each
+// with a ring and accumulators of its own, and add up at the end.
+template <int BM_, int BN_, int WM_, int WN_, int RB_, int S_, int R_ = 1>
 struct WgradCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, RB = RB_, S = S_;
-  static_assert(WM * WN == kWWaves, "one wave per wave tile");
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, RB = RB_, S = S_, R = R_;
+  static constexpr int WAVES = WM * WN;  // of a group
+  static constexpr int THREADS = kWave * WAVES * R;
+  static_assert(R == 1 || WAVES == 1, "groups run at their own pace: no barrier between waves");
   static constexpr int WTM = BM / WM, WTN = BN / WN;
   static constexpr int MI = WTM / 16, NI = WTN / 16;
   static_assert(MI * 16 * WM == BM && NI * 16 * WN == BN && RB % 32 == 0, "16x16x32 blocks");
   static constexpr int A_ROW = 2 * BM, B_ROW = 2 * BN;  // bytes of a slice row
   static constexpr int A_BYTES = RB * A_ROW, B_BYTES = RB * B_ROW, STAGE = A_BYTES + B_BYTES;
-  static constexpr int A_INSTR = A_BYTES / (1024 * kWWaves), B_INSTR = B_BYTES / (1024 * kWWaves);
-  static_assert(A_INSTR * 1024 * kWWaves == A_BYTES && B_INSTR * 1024 * kWWaves == B_BYTES, "loads");
+  static constexpr int A_INSTR = A_BYTES / (1024 * WAVES), B_INSTR = B_BYTES / (1024 * WAVES);
+  static_assert(A_INSTR * 1024 * WAVES == A_BYTES && B_INSTR * 1024 * WAVES == B_BYTES, "loads");
   static constexpr int LPS = A_INSTR + B_INSTR;
-  static constexpr int LDS_BYTES = S * STAGE;
+  static constexpr int LDS_BYTES = R * S * STAGE;
 };
 
 // Chunk (16 bytes) c of slice row r sits at chunk c ^ swz(r). A transposing
 // read touches rows 8 g + k' (k' < 4) of every lane group g, 32 bytes each;
 // the XOR spreads those over the banks (for 512-byte rows: gg_mainloop.h).
-// 128-byte rows have 8 chunks, and neighbouring rows lie in different halves
-// of the banks already.
+// 128- and 64-byte rows have 8 and 4 chunks, and neighbouring rows lie in
+// different parts of the banks already.
 template <int ROW>
 __device__ __forceinline__ int wg_swz(int r) {
   if constexpr (ROW >= 256) return ((r & 3) << 1) | (((r >> 3) & 1) << 3);
-  else return (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2);
+  else if constexpr (ROW == 128) return (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2);
+  else return ((r >> 3) & 1) << 1;
 }
 
 // Byte offset of this lane's load i inside a slice of an operand of `pitch`
 // bytes a row; `col` gets the byte column it starts at.
-template <int ROW>
+template <int ROW, int WAVES>
 __device__ __forceinline__ uint32_t wg_off(int i, int wave, int lane, uint32_t pitch, uint32_t &col) {
   constexpr int kRows = 1024 / ROW;  // rows of one load instruction
-  const int r = (i * kWWaves + wave) * kRows + lane / (64 / kRows);
+  const int r = (i * WAVES + wave) * kRows + lane / (64 / kRows);
   const int c = (lane % (64 / kRows)) ^ wg_swz<ROW>(r);
   col = 16u * c;
   return (uint32_t)r * pitch + col;
@@ -97,14 +98,14 @@ __device__ __forceinline__ void wg_issue(const WgradTile<C> &t, lds_u8 *stage, i
 #pragma unroll
   for (int i = 0; i < C::A_INSTR; ++i) {
     uint32_t col;
-    const uint32_t off = wg_off<C::A_ROW>(i, wave, lane, t.a_pitch, col);
-    dma16(ra, stage + (i * kWWaves + wave) * 1024, col < t.a_cols ? off : kOob);
+    const uint32_t off = wg_off<C::A_ROW, C::WAVES>(i, wave, lane, t.a_pitch, col);
+    dma16(ra, stage + (i * C::WAVES + wave) * 1024, col < t.a_cols ? off : kOob);
   }
 #pragma unroll
   for (int i = 0; i < C::B_INSTR; ++i) {
     uint32_t col;
-    const uint32_t off = wg_off<C::B_ROW>(i, wave, lane, t.b_pitch, col);
-    dma16(rb, stage + C::A_BYTES + (i * kWWaves + wave) * 1024, col < t.b_cols ? off : kOob);
+    const uint32_t off = wg_off<C::B_ROW, C::WAVES>(i, wave, lane, t.b_pitch, col);
+    dma16(rb, stage + C::A_BYTES + (i * C::WAVES + wave) * 1024, col < t.b_cols ? off : kOob);
   }
 }
 
@@ -127,9 +128,9 @@ __device__ __forceinline__ int wg_frag_off(int lane, int col0) {
 template <class C>
 __device__ __forceinline__ void wg_step(f32x4 (&acc)[C::NI][C::MI], const WgradTile<C> &t,
                                         const lds_u8 *__restrict__ cur, lds_u8 *__restrict__ nxt,
-                                        int k_next, int KT, int wave, int lane, int a_off,
+                                        int k_next, int group, int KT, int wave, int lane, int a_off,
                                         int b_off) {
-  if (k_next < KT) wg_issue<C>(t, nxt, k_next, wave, lane);
+  if (k_next < KT) wg_issue<C>(t, nxt, k_next * C::R + group, wave, lane);
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_setprio(1);
   static_for<C::RB / 32>([&](auto ksc) {
@@ -203,8 +204,41 @@ __device__ __forceinline__ int wgrad_expert(const int32_t *off, int E, int M_cap
   return find_expert<kMaxExperts / kWave>(off, E, M_cap, p, first, rows);
 }
 
+// The groups' sums of one BM x BN tile, added in the order of the groups: a
+// thread per element, whole rows of the tile side by side.
 template <class C, WOut O>
-__global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
+__device__ __forceinline__ void add_groups(const WgradParams &p, const f32x4 (&acc)[C::NI][C::MI],
+                                           lds_u8 *lds, int e, int col_k, int col_n, int group,
+                                           int lane) {
+  constexpr int P = C::BN + 4;  // floats of a row
+  static_assert(C::R * C::BM * P * 4 <= 160 * 1024 && C::THREADS >= C::BM * C::BN, "one pass");
+  lds_f32 *const part = (lds_f32 *)lds;
+  __syncthreads();  // every group is done with its ring
+  const int g = lane / 16, s = lane % 16;
+#pragma unroll
+  for (int mi = 0; mi < C::MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ++ni)
+      *(lds_f32x4 *)(part + (group * C::BM + mi * 16 + s) * P + ni * 16 + 4 * g) = acc[ni][mi];
+  __syncthreads();
+  const int m = threadIdx.x / C::BN, n = threadIdx.x % C::BN;
+  if (m >= C::BM || col_k + m >= p.K || col_n + n >= p.N) return;
+  float v = 0.f;
+#pragma unroll
+  for (int r = 0; r < C::R; ++r) v += part[(r * C::BM + m) * P + n];
+  const size_t at = ((size_t)e * p.K + col_k + m) * p.N + col_n + n;
+  if constexpr (O == WOut::BF16) {
+    const bf16x2 w = __builtin_convertvector(f32x2{v, v}, bf16x2);
+    ((uint16_t *)p.dB)[at] = __builtin_bit_cast(uint16_t, w[0]);
+  } else if constexpr (O == WOut::AddF32) {
+    ((float *)p.dB)[at] += v;
+  } else {
+    ((float *)p.dB)[at] = v;
+  }
+}
+
+template <class C, WOut O>
+__global__ __launch_bounds__(C::THREADS, 2) void wgrad_kernel(WgradParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds_dyn[];
   lds_u8 *const lds = (lds_u8 *)lds_dyn;
   // tiles of one expert in runs of per_xcd to an XCD (workgroup ids go
@@ -228,7 +262,8 @@ __global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
   t.b_cols = t.b_pitch - 2u * (uint32_t)col_n;
   t.rows = rows;
   const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+  const int lane = tid % kWave, wave = scalar(tid / kWave) % C::WAVES;
+  const int group = scalar(tid / kWave) / C::WAVES;  // takes slices group, group + R, ...
   const int wm0 = (wave / C::WN) * C::WTM, wn0 = (wave % C::WN) * C::WTN;
   const int a_off = wg_frag_off<C::A_ROW>(lane, wm0), b_off = wg_frag_off<C::B_ROW>(lane, wn0);
 
@@ -237,19 +272,24 @@ __global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
   for (int ni = 0; ni < C::NI; ++ni)
 #pragma unroll
     for (int mi = 0; mi < C::MI; ++mi) acc[ni][mi] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int KT = cdiv(rows, C::RB);
+  const int KT = max(cdiv(cdiv(rows, C::RB) - group, C::R), 0);  // this group's slices
+  lds_u8 *const ring = lds + group * (C::S * C::STAGE);
 #pragma unroll
   for (int k = 0; k < C::S - 1; ++k)
-    if (k < KT) wg_issue<C>(t, lds + k * C::STAGE, k, wave, lane);
+    if (k < KT) wg_issue<C>(t, ring + k * C::STAGE, k * C::R + group, wave, lane);
   int cur = 0, nxt = C::S - 1;
   for (int k = 0; k < KT; ++k) {
-    // slices k + 1 .. min(k + S - 2, KT - 1) stay in flight
+    // this wave's slices k + 1 .. min(k + S - 2, KT - 1) stay in flight
     wait_slices<C>(min(C::S - 2, KT - 1 - k));
-    wg_barrier();
-    wg_step<C>(acc, t, lds + cur * C::STAGE, lds + nxt * C::STAGE, k + C::S - 1, KT, wave, lane,
-               a_off, b_off);
+    if constexpr (C::WAVES > 1) wg_barrier();
+    wg_step<C>(acc, t, ring + cur * C::STAGE, ring + nxt * C::STAGE, k + C::S - 1, group, KT, wave,
+               lane, a_off, b_off);
     cur = cur + 1 == C::S ? 0 : cur + 1;
     nxt = nxt + 1 == C::S ? 0 : nxt + 1;
+  }
+  if constexpr (C::R > 1) {
+    add_groups<C, O>(p, acc, lds, e, col_k, col_n, group, lane);
+    return;
   }
 
   const int n_in = p.N - col_n;
@@ -285,6 +325,8 @@ __global__ __launch_bounds__(kWThreads, 2) void wgrad_kernel(WgradParams p) {
 
 using W128 = WgradCfg<128, 256, 2, 2, 32, 3>;  // wave tile 64 x 128
 using W64 = WgradCfg<64, 64, 2, 2, 32, 4>;     // wave tile 32 x 32
+using W32 = WgradCfg<32, 32, 1, 1, 32, 2, 16>;  // 16 waves, each its own slices
+static_assert(W32::LDS_BYTES <= 160 * 1024 && 16 * 32 * 36 * 4 <= W32::LDS_BYTES, "LDS");
 
 static_assert(2 * W128::LDS_BYTES <= 160 * 1024, "two workgroups a CU");
 
@@ -300,7 +342,7 @@ static gg_status_t launch_wgrad(WgradParams p, hipStream_t stream) {
   if (ring_launch<wgrad_kernel<C, O>>(dev, lds).err != hipSuccess) return GG_ERR_LAUNCH;
   p.tiles = (int)tiles;
   p.per_xcd = (int)per;
-  hipLaunchKernelGGL((wgrad_kernel<C, O>), dim3((unsigned)grid), dim3(kWThreads), lds, stream, p);
+  hipLaunchKernelGGL((wgrad_kernel<C, O>), dim3((unsigned)grid), dim3(C::THREADS), lds, stream, p);
   return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
 }
 
@@ -319,7 +361,14 @@ static gg_status_t wgrad(const void *A, const void *dC, const int32_t *off, void
                 M_cap, 0, 0};
   hipStream_t s = static_cast<hipStream_t>(stream);
   const long long big = (long long)E * ((K + 127) / 128) * ((N + 255) / 256);
-  return big >= 256 ? launch_wgrad<W128, O>(p, s) : launch_wgrad<W64, O>(p, s);
+  const long long mid = (long long)E * ((K + 63) / 64) * ((N + 63) / 64);
+  // Large tiles where they give every CU one. Of the others, up to 64 tiles of
+  // 64 x 64 leave most CUs idle for the length of the rows: smaller tiles whose
+  // rows 16 waves share (us, W64 / W32: one expert of 16384 rows, 64 x 64: 100 /
+  // 23; 1024 x 256: 104 / 58; four of 2000 rows, 256 x 256: 15.9 / 9.9; beyond
+  // them, eight of 1000 rows, 256 x 512: 10.3 / 21).
+  if (big >= 256) return launch_wgrad<W128, O>(p, s);
+  return mid > 64 ? launch_wgrad<W64, O>(p, s) : launch_wgrad<W32, O>(p, s);
 }
 
 }  // namespace gg

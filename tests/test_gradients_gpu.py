@@ -191,7 +191,8 @@ def _wgrad_case(gg, sizes, K, N, out, seed, spare=3, draw=ops.bits, accumulate=F
 # K and N below, at and past the tiles' 64, 128 and 256; enough experts for the
 # large tiles in the last ones; row counts around the slices' 32
 WSHAPES = [([0, 1, 17, 130, 0, 300], 328, 392), ([5], 8, 8), ([1], 136, 72), ([31, 32, 33, 64, 65], 200, 264),
-           ([97], 1032, 16), ([3, 0, 40, 7] * 16, 264, 520), ([0] * 70 + [50, 1], 256, 776)]
+           ([97], 1032, 16), ([1000, 0, 333, 31], 72, 136),
+           ([3, 0, 40, 7] * 16, 264, 520), ([0] * 70 + [50, 1], 256, 776)]
 
 
 @pytest.mark.parametrize("out", DTYPES)
@@ -210,7 +211,7 @@ def test_wgrad_accumulate(gg, sizes, K, N):
     ops.check_f32(got, want, err, "wgrad accumulate")
 
 
-@pytest.mark.parametrize("sizes,K,N", [([5, 0, 40, 129, 16], 264, 512), ([9, 60, 0, 33] * 20, 256, 520)])
+@pytest.mark.parametrize("sizes,K,N", [([5, 0, 40, 129, 16], 264, 512), ([9, 60, 0, 33] * 20, 256, 520), ([777], 40, 72)])
 def test_wgrad_integers_are_exact(gg, sizes, K, N):
     got, want, _ = _wgrad_case(gg, sizes, K, N, "fp32", 302, draw=ops.int_bits)
     assert (got == want).all()
