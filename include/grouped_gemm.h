@@ -359,7 +359,8 @@ gg_status_t gg_grouped_gemm_bf16_dgrad_swiglu(const void *dY, const void *B,
  *       kernel read or write outside its arrays (they are clamped as in
  *       gg_grouped_gemm_bf16).
  *   K and N are multiples of 8, at most GG_MAX_K; E in [1, GG_MAX_EXPERTS];
- *   M_cap in [0, 2^31 - 257].
+ *   M_cap in [0, 2^31 - 257]; E * (ceil(K/128) * ceil(N/256) + 7) < 2^24
+ *   (GG_ERR_UNSUPPORTED beyond; a launch holds 2^32 threads).
  * The sum over an expert's rows is taken in fp32 in the matrix cores, in an
  * order that the sizes fix: no atomics, so equal inputs give equal bits.
  */
@@ -397,7 +398,8 @@ gg_status_t gg_grouped_gemm_bf16_wgrad_bf16out(const void *A, const void *dC,
  * format's own rule: the largest values of a block may be up to 8 scales). A
  * block of zeros gets scale byte 0. A block that holds an infinity or a NaN
  * gets scale byte 255 and codes 0, and so stands for NaN throughout.
- * X, q and scales are 16-byte aligned; rows in [0, 2^31 - 1], K <= GG_MAX_K.
+ * X, q and scales are 16-byte aligned; rows in [0, 2^31 - 1], K <= GG_MAX_K,
+ * rows * K < 2^37 (GG_ERR_UNSUPPORTED beyond; a launch holds 2^32 threads).
  */
 gg_status_t gg_mx4_quantize(const void *X, void *q, void *scales, int64_t rows, int32_t K,
                             void *stream);
@@ -405,8 +407,8 @@ gg_status_t gg_mx4_quantize(const void *X, void *q, void *scales, int64_t rows, 
 /*
  * gg_mx4_quantize_weights -- B bf16 [E][K][N] (the layout of the bf16 product)
  * to codes [E][N][K/2] and scales [E][ceil(K/256)][N][8], blocks along K, by the
- * rule of gg_mx4_quantize. N is a multiple of 8, at most GG_MAX_N; E * K * N at
- * most 2^46.
+ * rule of gg_mx4_quantize. N is a multiple of 8, at most GG_MAX_N, and E *
+ * ceil(K/256) * ceil(N/256) < 2^23.
  */
 gg_status_t gg_mx4_quantize_weights(const void *B, void *q, void *scales, int32_t E, int32_t K,
                                     int32_t N, void *stream);
@@ -417,7 +419,7 @@ gg_status_t gg_mx4_quantize_weights(const void *B, void *q, void *scales, int32_
  * [batch][ceil(K/256)][rows][8] (batch = E and rows = N for weights, batch = 1
  * for activations). Every such value is a bf16 value except 4 and 6 times
  * 2^127 (scale byte 254), which become infinite; scale byte 255 gives NaN.
- * batch in [0, 65535]; rows in [0, 2^31 - 1].
+ * batch in [0, 65535]; rows in [0, 2^31 - 1]; rows * K < 2^37.
  */
 gg_status_t gg_mx4_dequantize(const void *q, const void *scales, void *Y, int32_t batch,
                               int64_t rows, int32_t K, void *stream);

@@ -17,6 +17,11 @@ constexpr int kHostMaxDevices = 64;
 
 inline bool is_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// A dispatch counts its threads along x in 32 bits.
+inline bool launch_fits(long long workgroups, int threads) {
+  return workgroups <= UINT32_MAX / (uint32_t)threads;
+}
+
 inline bool valid_bm(int bm) {
   return bm == 0 || bm == 16 || bm == 32 || bm == 64 || bm == 128 || bm == 256;
 }

@@ -11,11 +11,22 @@
 // The buffers end at the group's last row, so the rows of a slice past it
 // read as zeros in both operands.
 //
-// One workgroup per tile, four waves, two workgroups to a CU. The tiles of all experts number
-// E * ceil(K / BM) * ceil(N / BN) whatever the routing, so the grid is known on
-// the host and the hardware hands the next tile to whichever CU is free. A
-// launch ends with its longest tile, so experts come in the order of their
-// size class (power of two of the row count), largest first.
+// One workgroup per tile, four waves, two workgroups to a CU. The tiles of all
+// experts number E * ceil(K / BM) * ceil(N / BN) whatever the routing, so the
+// grid is known on the host and the hardware hands the next tile to whichever
+// CU is free. A launch ends with its longest tile, so experts come in the
+// order of their size class (power of two of the row count), largest first.
+//
+// What bounds it. 64 experts x 256 rows, K = 1024, N = 2688, fp32 out: 220 us for
+// 826 MB (3.8 TB/s); bf16 139; 32 experts, 2048 skewed rows, K = 6144, N = 4096,
+// bf16: 362 us for 1.65 GB (4.6 TB/s, a plain copy moves 4.9). The gradient's
+// own bytes are most of it: writing it alone takes 118 - 130 us of the 220, the
+// loads and products without the stores 110, and the two add up rather than
+// overlap. A CU's vector memory path takes loads and stores in one order
+// (L1 is stalled on pending loads for 75% of the launch), and neither staggered
+// starts, nor stores spread over the next slices, nor more workgroups a CU
+// changed that; what helped is fewer and cheaper accesses: whole-line streamed
+// stores (store_block) and rows kept in L2.
 
 #include "gg_common.h"
 #include "gg_host.h"
@@ -336,7 +347,7 @@ static gg_status_t launch_wgrad(WgradParams p, hipStream_t stream) {
   const long long tiles = ((p.K + (long long)C::BM - 1) / C::BM) * ((p.N + (long long)C::BN - 1) / C::BN);
   const long long per = (tiles + kRingXcds - 1) / kRingXcds;
   const long long grid = per * kRingXcds * p.E;
-  if (grid > (1LL << 28)) return GG_ERR_UNSUPPORTED;
+  if (!launch_fits(grid, C::THREADS)) return GG_ERR_UNSUPPORTED;
   int dev = 0;
   if (!current_device(&dev)) return GG_ERR_LAUNCH;
   if (ring_launch<wgrad_kernel<C, O>>(dev, lds).err != hipSuccess) return GG_ERR_LAUNCH;

@@ -177,6 +177,15 @@ def test_mx4_row_host_checks(lib):
     assert d(b=0) == d(rows=0) == 0
 
 
+def test_launches_of_2_to_the_32_threads_are_refused(lib):
+    # 2^24 tiles of 128 x 256 (256 threads each); 2^24 pieces of 8192 values; 2^23 of 256 x 256
+    for entry in ("gg_grouped_gemm_bf16_wgrad", "gg_grouped_gemm_bf16_wgrad_bf16out"):
+        assert _status(lib, entry, E=1024, K=8, N=2 ** 22) == UNSUPPORTED
+    assert lib.gg_mx4_quantize(16, 32, 48, 2 ** 15, 2 ** 22, None) == UNSUPPORTED
+    assert lib.gg_mx4_dequantize(16, 32, 48, 1, 2 ** 15, 2 ** 22, None) == UNSUPPORTED
+    assert lib.gg_mx4_quantize_weights(16, 32, 48, 512, 2 ** 22, 8, None) == UNSUPPORTED
+
+
 # ------------------------------------------------------------ the binding
 
 def _bf(*shape):
@@ -274,3 +283,14 @@ def test_product_loops_hold_what_they_need(source, tmp_path):
         assert not any("v_readlane" in ln or "v_writelane" in ln or "scratch_" in ln for ln in body)
         for before, ln in zip(body, body[1:]):
             assert "vmcnt" not in ln or "#ASMSTART" in before, ln
+    # A 256-row tile's step has a second barrier, after which the weights and
+    # scales it multiplies are overwritten: every wave has read its own by then
+    # (2 x 4 column fragments; 8 + 4 scale reads) with 7 of its 16 row fragments.
+    tallest = [b for b in products if sum("s_barrier" in ln for ln in b) == 2]
+    assert len(tallest) == (0 if "wgrad" in source else 3)
+    for body in tallest:
+        first, second = (i for i, ln in enumerate(body) if "s_barrier" in ln)
+        reads = [i for i, ln in enumerate(body) if "ds_read_b128" in ln]
+        assert len(reads) == 24 and sum(first < i < second for i in reads) == 8 + 7
+        scales = [i for i, ln in enumerate(body) if "ds_read_u16" in ln]
+        assert len(scales) == (12 if "mx4" in source else 0) and all(first < i < second for i in scales)
