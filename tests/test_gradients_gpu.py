@@ -280,6 +280,46 @@ def test_rows_beyond_4_gigabytes(gg):
     torch.cuda.empty_cache()
 
 
+def _signs(*shape, seed):
+    g = torch.Generator(device="cuda:0").manual_seed(seed)
+    return torch.randint(-1, 2, shape, generator=g, device="cuda:0", dtype=torch.int8).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,K,N", [(3, 264, 2 ** 21), (300, 8, 2 ** 21), (20, 2 ** 24, 8)])
+def test_dgrad_longest_rows(gg, rows, K, N):
+    # -1, 0 and 1: sums of at most 2^21 of them are exact in fp32
+    dC, B = _signs(rows, N, seed=1), _signs(1, K, N, seed=2)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda:0")
+    want = dC.float() @ B[0].float().t()
+    for bm in (0, 256):
+        assert torch.equal(gg.grouped_gemm_dgrad(dC, B, off, bm=bm), want)
+    torch.cuda.empty_cache()
+
+
+def test_dgrad_swiglu_longest_rows(gg):
+    # gate 0 and up in -1, 0, 1: d gate = dH * up / 2 is a bf16 value, d up = 0
+    rows, K, N = 18, 2 ** 24, 8
+    dY, B, up = _signs(rows, N, seed=3), _signs(1, K, N, seed=4), _signs(rows, K, seed=5)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda:0")
+    C = torch.zeros((rows, K, 2), dtype=torch.bfloat16, device="cuda:0")
+    C[..., 1] = up
+    dC = gg.grouped_gemm_dgrad_swiglu(dY, B, off, C.view(rows, 2 * K)).view(rows, K, 2)
+    assert torch.equal(dC[..., 0].float(), (dY.float() @ B[0].float().t()) * up.float() / 2)
+    assert not dC[..., 1].any()
+    del C, dC
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("K,N", [(2 ** 22, 8), (8, 2 ** 22)])
+def test_wgrad_longest_rows(gg, K, N):
+    A, dC = _signs(70, K, seed=6), _signs(70, N, seed=7)
+    off = torch.tensor([0, 33, 70], dtype=torch.int32, device="cuda:0")
+    want = torch.stack([A[:33].float().t() @ dC[:33].float(), A[33:].float().t() @ dC[33:].float()])
+    for out in DTYPES:
+        assert torch.equal(gg.grouped_gemm_wgrad(A, dC, off, out_dtype=_dt(out)).float(), want)
+    torch.cuda.empty_cache()
+
+
 def test_wgrad_neighbours_rows_stay_out(gg):
     # NaN in an expert's rows reaches that expert's gradient only
     rng = np.random.default_rng(6)

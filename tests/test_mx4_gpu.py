@@ -246,6 +246,23 @@ def test_rows_beyond_4_gigabytes(gg):
     torch.cuda.empty_cache()
 
 
+def test_longest_rows(gg):
+    # K at its limit: values -1, 0 and 1 (codes 0 and +-4, scale 1/4), whose sums are exact
+    rows, K, N = 3, 2 ** 22, 264
+    g = torch.Generator(device="cuda:0").manual_seed(3)
+    x = torch.randint(-1, 2, (rows, K), generator=g, device="cuda:0", dtype=torch.int8).to(torch.bfloat16)
+    w = torch.randint(-1, 2, (1, K, N), generator=g, device="cuda:0", dtype=torch.int8).to(torch.bfloat16)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda:0")
+    a, b = gg.mx4_quantize(x), gg.mx4_quantize_weights(w)
+    assert torch.equal(gg.mx4_dequantize(*a), x)
+    assert torch.equal(gg.mx4_dequantize(*b)[0], w[0].t())
+    want = x.float() @ w[0].float()
+    for bm in (0, 256):
+        assert torch.equal(gg.grouped_gemm_mx4(*a, *b, off, bm=bm), want)
+    del x, w, a, b
+    torch.cuda.empty_cache()
+
+
 def test_serving_a_layer(gg):
     # a layer's weights laid out once, then rows through quantise -> gate/up with
     # SwiGLU -> quantise -> down, against the same steps in binary64
