@@ -63,7 +63,11 @@ struct WgradCfg {
   static constexpr int A_INSTR = A_BYTES / (1024 * WAVES), B_INSTR = B_BYTES / (1024 * WAVES);
   static_assert(A_INSTR * 1024 * WAVES == A_BYTES && B_INSTR * 1024 * WAVES == B_BYTES, "loads");
   static constexpr int LPS = A_INSTR + B_INSTR;
-  static constexpr int LDS_BYTES = R * S * STAGE;
+  static constexpr int RING_BYTES = R * S * STAGE;
+  static constexpr int PART_ROW = BN + 4;  // floats of a row of a group's sums (add_groups)
+  static constexpr int PART_BYTES = R > 1 ? R * BM * PART_ROW * 4 : 0;
+  static constexpr int LDS_BYTES = RING_BYTES > PART_BYTES ? RING_BYTES : PART_BYTES;
+  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
 };
 
 // Chunk (16 bytes) c of slice row r sits at chunk c ^ swz(r). A transposing
@@ -215,14 +219,14 @@ __device__ __forceinline__ int wgrad_expert(const int32_t *off, int E, int M_cap
   return find_expert<kMaxExperts / kWave>(off, E, M_cap, p, first, rows);
 }
 
-// The groups' sums of one BM x BN tile, added in the order of the groups: a
-// thread per element, whole rows of the tile side by side.
+// The groups' sums of one BM x BN tile, added in the order of the groups:
+// element by element, whole rows of the tile side by side.
 template <class C, WOut O>
 __device__ __forceinline__ void add_groups(const WgradParams &p, const f32x4 (&acc)[C::NI][C::MI],
                                            lds_u8 *lds, int e, int col_k, int col_n, int group,
                                            int lane) {
-  constexpr int P = C::BN + 4;  // floats of a row
-  static_assert(C::R * C::BM * P * 4 <= 160 * 1024 && C::THREADS >= C::BM * C::BN, "one pass");
+  constexpr int P = C::PART_ROW;
+  static_assert(C::BM * C::BN % C::THREADS == 0, "whole passes");
   lds_f32 *const part = (lds_f32 *)lds;
   __syncthreads();  // every group is done with its ring
   const int g = lane / 16, s = lane % 16;
@@ -232,19 +236,22 @@ __device__ __forceinline__ void add_groups(const WgradParams &p, const f32x4 (&a
     for (int ni = 0; ni < C::NI; ++ni)
       *(lds_f32x4 *)(part + (group * C::BM + mi * 16 + s) * P + ni * 16 + 4 * g) = acc[ni][mi];
   __syncthreads();
-  const int m = threadIdx.x / C::BN, n = threadIdx.x % C::BN;
-  if (m >= C::BM || col_k + m >= p.K || col_n + n >= p.N) return;
-  float v = 0.f;
 #pragma unroll
-  for (int r = 0; r < C::R; ++r) v += part[(r * C::BM + m) * P + n];
-  const size_t at = ((size_t)e * p.K + col_k + m) * p.N + col_n + n;
-  if constexpr (O == WOut::BF16) {
-    const bf16x2 w = __builtin_convertvector(f32x2{v, v}, bf16x2);
-    ((uint16_t *)p.dB)[at] = __builtin_bit_cast(uint16_t, w[0]);
-  } else if constexpr (O == WOut::AddF32) {
-    ((float *)p.dB)[at] += v;
-  } else {
-    ((float *)p.dB)[at] = v;
+  for (int i = 0; i < C::BM * C::BN / C::THREADS; ++i) {
+    const int el = i * C::THREADS + (int)threadIdx.x, m = el / C::BN, n = el % C::BN;
+    if (col_k + m >= p.K || col_n + n >= p.N) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int r = 0; r < C::R; ++r) v += part[(r * C::BM + m) * P + n];
+    const size_t at = ((size_t)e * p.K + col_k + m) * p.N + col_n + n;
+    if constexpr (O == WOut::BF16) {
+      const bf16x2 w = __builtin_convertvector(f32x2{v, v}, bf16x2);
+      ((uint16_t *)p.dB)[at] = __builtin_bit_cast(uint16_t, w[0]);
+    } else if constexpr (O == WOut::AddF32) {
+      ((float *)p.dB)[at] += v;
+    } else {
+      ((float *)p.dB)[at] = v;
+    }
   }
 }
 
@@ -336,9 +343,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void wgrad_kernel(WgradParams p) {
 
 using W128 = WgradCfg<128, 256, 2, 2, 32, 3>;  // wave tile 64 x 128
 using W64 = WgradCfg<64, 64, 2, 2, 32, 4>;     // wave tile 32 x 32
-using W32 = WgradCfg<32, 32, 1, 1, 32, 2, 16>;  // 16 waves, each its own slices
-static_assert(W32::LDS_BYTES <= 160 * 1024 && 16 * 32 * 36 * 4 <= W32::LDS_BYTES, "LDS");
-
+using W64R = WgradCfg<64, 64, 1, 1, 32, 2, 8>;  // 8 waves, each its own slices
+using W32 = WgradCfg<32, 32, 1, 1, 32, 2, 16>;  // 16 of them
 static_assert(2 * W128::LDS_BYTES <= 160 * 1024, "two workgroups a CU");
 
 template <class C, WOut O>
@@ -377,9 +383,15 @@ static gg_status_t wgrad(const void *A, const void *dC, const int32_t *off, void
   // 64 x 64 leave most CUs idle for the length of the rows: smaller tiles whose
   // rows 16 waves share (us, W64 / W32: one expert of 16384 rows, 64 x 64: 100 /
   // 23; 1024 x 256: 104 / 58; four of 2000 rows, 256 x 256: 15.9 / 9.9; beyond
-  // them, eight of 1000 rows, 256 x 512: 10.3 / 21).
+  // them, eight of 1000 rows, 256 x 512: 10.3 / 21). Up to one tile of 64 x 64 a
+  // CU, eight waves share long groups, of 3000 rows and more (W64 / W64R: one of
+  // 16384, 1024 x 1024: 100 / 64; one of 8000, 2048 x 512: 50.7 / 48.5; two of
+  // 3200, 2776 x 104: 28.8 / 23.9; shorter ones, eight of 1000, 256 x 512: 10.3 /
+  // 10.8; more tiles, four of 2000, 1024 x 512: 27.2 / 29.2).
   if (big >= 256) return launch_wgrad<W128, O>(p, s);
-  return mid > 64 ? launch_wgrad<W64, O>(p, s) : launch_wgrad<W32, O>(p, s);
+  if (mid <= 64) return launch_wgrad<W32, O>(p, s);
+  if (mid <= 256 && M_cap / E >= 3000) return launch_wgrad<W64R, O>(p, s);
+  return launch_wgrad<W64, O>(p, s);
 }
 
 }  // namespace gg

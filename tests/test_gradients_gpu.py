@@ -217,6 +217,20 @@ def test_wgrad_integers_are_exact(gg, sizes, K, N):
     assert (got == want).all()
 
 
+# long groups whose tiles of 64 x 64 are 65 to 256: waves share the rows
+LONG = [([3100], 600, 456), ([6200, 1], 264, 520), ([0, 9001, 0], 520, 200)]
+
+
+@pytest.mark.parametrize("out", DTYPES)
+@pytest.mark.parametrize("sizes,K,N", LONG)
+def test_wgrad_long_groups(gg, sizes, K, N, out):
+    got, want, err = _wgrad_case(gg, sizes, K, N, out, 306)
+    _check(out, got, want, err, "wgrad %s K=%d N=%d %s" % (sizes, K, N, out))
+    for accumulate in (False, True) if out == "fp32" else ():
+        got, want, err = _wgrad_case(gg, sizes, K, N, out, 307, draw=ops.int_bits, accumulate=accumulate)
+        assert (np.abs(got - want) <= (err if accumulate else 0)).all()
+
+
 def test_wgrad_many_experts_and_ties(gg):
     # 1024 experts of 0 .. 40 rows: the order by size has ties everywhere
     rng = np.random.default_rng(5)
