@@ -10,10 +10,10 @@
 // One persistent launch walks the tiles of all experts (the schedule of
 // gg_ring.h, K in the place of the output columns).
 //
-// What bounds it. 64 experts x 256 rows, K = 1024, N = 2688, bf16 out: 92 us,
-// 474 MB (5.1 TB/s, above the 4.9 TB/s of a plain copy, as most of it is read)
-// and 979 TFLOP/s; the bytes. Skewed routing of the same rows, K = 1344, N =
-// 1024, with the SwiGLU gradient and H: 123 us, 430 MB at 3.5 TB/s; rounds of
+// What bounds it. 64 experts x 256 rows, K = 1024, N = 2688, bf16 out: 91 us,
+// 474 MB (5.2 TB/s, above the 4.9 TB/s of a plain copy, as most of it is read)
+// and 988 TFLOP/s; the bytes. Skewed routing of the same rows, K = 1344, N =
+// 1024, with the SwiGLU gradient and H: 122 us, 430 MB at 3.5 TB/s; rounds of
 // 256-row tiles whose epilogue (a third of the bytes) follows their products.
 // Few tiles (12 experts, 777 rows, K = 712, N = 1000): 19 us, 16 slices one after
 // the other at about 0.6 us, and 5 us of launch and schedule.

@@ -10,9 +10,9 @@
 //
 // What bounds them. Quantisation and its inverse move bytes: 16384 x 6144 to 4
 // bits 44 us (5.8 TB/s), back 40 (6.3); weights [64][1024][2688] 73 (6.1), back
-// 64 (7.0). The product of 32 experts x 16 rows, K = 6144, N = 4096: 73 us for
+// 64 (7.0). The product of 32 experts x 16 rows, K = 6144, N = 4096: 72 us for
 // 438 MB (6.0 TB/s), the weights' bytes, a third of the 16-bit product's. 64
-// experts, 16384 skewed rows, K = 1024, N = 2688 with SwiGLU: 65 us for 147 MB
+// experts, 16384 skewed rows, K = 1024, N = 2688 with SwiGLU: 62 us for 147 MB
 // and 90 GFLOP; four slices a tile leave its start, its epilogue and the last
 // partly filled round of tiles uncovered. One row on each of 8 experts: 9.4
 // us, nearly all of it launch, schedule and the first loads' latency.

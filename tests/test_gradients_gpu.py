@@ -61,6 +61,17 @@ def test_dgrad(gg, sizes, K, N, bm):
         _check(out, got, want, ops.sum_bound(N, S), "dgrad %s bm=%d %s" % (sizes, bm, out))
 
 
+@pytest.mark.parametrize("copies", [1, 3, 4, 6, 12])
+def test_dgrad_heights_of_a_launch(gg, copies):
+    # heights of 16 to 256 together; from a few tiles, whose heights are cut to fill
+    # the CUs, over half a round of the narrowest to several rounds of the widest
+    sizes = [300, 20, 0, 700, 64, 130] * copies
+    got, want, _ = _dgrad_case(gg, sizes, 1032, 72, 0, "fp32", 8, draw=ops.int_bits)
+    assert (got == want).all()
+    got, want, _ = _dgrad_case(gg, sizes, 72, 136, 0, "bf16", 9, draw=ops.int_bits)
+    assert (got == oracle.round_to_bf16(want)).all()
+
+
 @pytest.mark.parametrize("bm", BMS)
 def test_dgrad_integers_are_exact(gg, bm):
     # every partial sum is an integer below 2^24

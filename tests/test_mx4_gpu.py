@@ -166,6 +166,18 @@ def test_product_exact(gg, bm):
     assert (got[:M] == want[:M]).all()
 
 
+@pytest.mark.parametrize("copies", [1, 3, 6, 12])
+def test_heights_of_a_launch(gg, copies):
+    # heights of 16 to 256 together, from a few tiles to several rounds of the widest;
+    # exact as above
+    sizes = [300, 20, 0, 700, 64, 130] * copies
+    off, Aq, a_s, Bq, b_s = _codes(np.random.default_rng(copies), sizes, 288, 1032, 126, 129)
+    M = int(off[-1])
+    got = ops.host(gg.grouped_gemm_mx4(*(ops.to_dev(t) for t in (Aq, a_s, Bq, b_s, off))))
+    want, _ = ref.mx4_product(Aq, a_s, Bq, b_s, off)
+    assert (got[:M] == want[:M]).all()
+
+
 def test_product_nan_scales_stay_in_their_row_and_column(gg):
     off, Aq, a_s, Bq, b_s = _codes(np.random.default_rng(4), [20, 30], 288, 136)
     a_s[0, 7, 3] = 255   # row 7
