@@ -110,7 +110,13 @@ struct DgradEpi {
           const float gate = lo_bf16(w), up = hi_bf16(w);
           const float sg = sigmoid(gate), dh = acc[ni][mi][j];
           const float act = gate * sg;
-          const f32x2 dv = {dh * up * (sg * (1.0f + gate * (1.0f - sg))), dh * act};
+          // sg * (1 + gate * (1 - sg)), the slope of the activation, goes to
+          // up first: dh * up alone may leave fp32's range where a small slope
+          // brings it back. slope * up does so only where H does too (a slope
+          // above 1 is below the activation itself); what subnormal numbers
+          // lose of it is at most 2^-149 |dh|.
+          const float slope = sg + act * (1.0f - sg);
+          const f32x2 dv = {dh * (slope * up), dh * act};
           d[ni][j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(dv, bf16x2));
           h[ni][mi][j] = act * up;
         }

@@ -157,6 +157,28 @@ def test_dgrad_swiglu_large_gates(gg):
     _swiglu_case(gg, [70, 9], 128, 64, 0, 203, True, gate_scale=60.0)
 
 
+def test_dgrad_swiglu_large_factors(gg):
+    # dH * up lies beyond fp32, the sigmoid's factor brings the gradient back: finite
+    # results are the formula's, and 0 where the sigmoid is 0 (gates below -87.3)
+    # (beside large values at the steepest slope, 1.0998 at 2.4)
+    big = 2.0 ** 126
+    gates = np.repeat([-100.0, -95.0, -60.0, -40.0, -60.0, -60.0, 2.40625, 2.40625], 8)
+    ups = np.repeat([2.0 ** 70, -2.0 ** 100, 2.0 ** 70, 2.0 ** 64, 2.0 ** 100, -2.0 ** 30, big, -big], 8)
+    dhs = np.repeat([2.0 ** 70, 2.0 ** 60, 2.0 ** 70, -2.0 ** 65, 2.0 ** 60, 2.0 ** 120, 2.0 ** -2, -2.0 ** -3], 8)
+    I = gates.size
+    C = wl.f32_to_bf16_bits(np.stack([gates, ups], axis=-1).reshape(1, 2 * I).astype(np.float32))
+    dY, eye = wl.f32_to_bf16_bits(dhs[None].astype(np.float32)), wl.f32_to_bf16_bits(np.eye(I, dtype=np.float32))
+    got = ops.host(gg.grouped_gemm_dgrad_swiglu(ops.to_dev(dY), ops.to_dev(eye[None]), ops.to_dev(ops.offsets_of([1])),
+                                                ops.to_dev(C))).astype(np.float64)
+    want, _ = ref.swiglu_grad(dhs[None], np.stack([gates, ups], axis=-1).reshape(1, 2 * I))
+    live = np.repeat(gates > -88, 2)[None]
+    # sigmoid is off by |gate| + 3 ulps, its complement's sum and the products by less than
+    # 8 more (62 * 2^-23 = 2^-17 at gate = -60, and 2^-17 covers the rest), then one rounding to bf16
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(want))[live].all()
+    assert (got[~live] == 0).all()
+
+
 def test_dgrad_swiglu_differences(gg):
     # the gradient against central differences of sum(dH * silu(gate) * up) in
     # binary64; K = N with identity weights, so that dH = dY
