@@ -96,7 +96,7 @@ gg_status_t gg_grouped_gemm_bf16(const void *A, const void *B, const int32_t *gr
  * gg_grouped_gemm_bf16 except C:
  *   C   bf16 [M_cap][N], row-major, 16-byte aligned. Each element is the fp32
  *       matrix-core result rounded once to the nearest bf16 (ties to even),
- *       so it is within half a bf16 unit (2^-9 relative) of the fp32 result
+ *       so it is within half a bf16 unit (2^-8 relative) of the fp32 result
  *       gg_grouped_gemm_bf16 returns for the same inputs, and equal to that
  *       result rounded to bf16.
  */
@@ -124,8 +124,8 @@ gg_status_t gg_grouped_gemm_bf16_bf16out(const void *A, const void *B,
  *       same inputs. The activation is evaluated in fp32 as
  *       x * rcp(1 + 2^(-x log2 e)) with the hardware exp2 and reciprocal,
  *       within (|gate| + 3.5) * 2^-23 of the exact value relative to first
- *       order (-0 where e^-gate overflows, for gate below about -88.7), and
- *       rounded once to the nearest bf16 (ties to even). Rows at or past
+ *       order (-0 for gate below about -87.3, where the reciprocal would be
+ *       subnormal: less than 1.1e-36 * |up| is lost), and rounded once to the nearest bf16 (ties to even). Rows at or past
  *       off[E] are not written.
  * A, group_offsets, E, K, N, M_cap, bm, the stream, the status codes and
  * the conditions for them are those of gg_grouped_gemm_bf16 (N a multiple
@@ -333,9 +333,9 @@ gg_status_t gg_grouped_gemm_bf16_dgrad_bf16out(const void *dC, const void *B,
  *       not stored. dC may be C itself. Rows at or beyond off[E] of C are not
  *       read, of dC and H not written. All are 16-byte aligned.
  * Everything is evaluated in fp32 (hardware exp2 and reciprocal, each within one
- * ulp) and rounded once to bf16 on its way out. s is 0 where e^-gate overflows
- * (gate below about -88.7), where dC and H then are 0 within 3e-37 relative to
- * |dH * up| and |up|; an infinite gate gives NaN. Sizes, offsets, bm, the
+ * ulp) and rounded once to bf16 on its way out. s is 0 where it would be subnormal
+ * (gate below about -87.3); dC and H then are 0, off by less than 1.1e-36 *
+ * |dH * up|, 1.1e-36 * |dH| and 1.1e-36 * |up|. An infinite gate gives NaN. Sizes, offsets, bm, the
  * stream and the status codes are those of gg_grouped_gemm_bf16_dgrad.
  */
 gg_status_t gg_grouped_gemm_bf16_dgrad_swiglu(const void *dY, const void *B,

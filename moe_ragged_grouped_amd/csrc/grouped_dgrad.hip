@@ -40,7 +40,7 @@ struct DgradParams {
 };
 
 // sigmoid(x) with the hardware exp2 and reciprocal (each within one ulp); 0
-// where e^-x overflows.
+// where it would be subnormal (x below about -87.3).
 __device__ __forceinline__ float sigmoid(float x) {
   constexpr float kLog2e = 1.4426950408889634f;
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * kLog2e));

@@ -72,8 +72,8 @@ def swiglu_grad_error(dH, dH_err, C):
     the reciprocal add one ulp at most each). 1 - s then is off by s (|g| + 3) u
     + u, so t = 1 + g (1 - s) by |g| (s (|g| + 3) + 1) u and two roundings of
     numbers up to 1 + |g|. The products add at most one ulp each. Twice the sum
-    of the first-order terms covers the higher ones. Where e^-g overflows s is
-    0 instead of less than 2^-127: 2^-100 of everything it multiplies.
+    of the first-order terms covers the higher ones. Where s is below
+    2^-126 it is 0 instead: 2^-100 of everything it multiplies.
     """
     u = 2.0 ** -23
     g, up = np.abs(C[:, 0::2]), np.abs(C[:, 1::2])

@@ -179,6 +179,22 @@ def test_dgrad_swiglu_large_factors(gg):
     assert (got[~live] == 0).all()
 
 
+def test_dgrad_swiglu_where_the_sigmoid_ends(gg):
+    # s of gates from -87.5 on would be subnormal and is 0; before that it is there
+    gates = np.array([-86.0, -86.5, -87.0, -87.5, -88.0, -88.5, -89.0, -100.0])
+    I, h = gates.size, 2.0 ** 60
+    C = wl.f32_to_bf16_bits(np.stack([gates, np.full(I, h)], axis=-1).reshape(1, 2 * I).astype(np.float32))
+    dY = wl.f32_to_bf16_bits(np.full((1, I), h, dtype=np.float32))
+    eye = wl.f32_to_bf16_bits(np.eye(I, dtype=np.float32))[None]
+    d, H = (ops.host(t).astype(np.float64)[0] for t in gg.grouped_gemm_dgrad_swiglu(
+        ops.to_dev(dY), ops.to_dev(eye), ops.to_dev(ops.offsets_of([1])), ops.to_dev(C), with_h=True))
+    want, want_h = ref.swiglu_grad(np.full((1, I), h), np.stack([gates, np.full(I, h)], axis=-1).reshape(1, 2 * I))
+    for got, exact, scale in ((d[0::2], want[0, 0::2], h * h), (d[1::2], want[0, 1::2], h), (H, want_h[0], h)):
+        assert (got[3:] == 0).all() and (np.abs(exact[3:]) < 1.1e-36 * scale).all()
+        # |gate| + 3 ulps of s and a few of the products, one rounding to bf16
+        assert (np.abs(got - exact)[:3] <= (2.0 ** -8 + 2.0 ** -16) * np.abs(exact[:3])).all()
+
+
 def test_dgrad_swiglu_differences(gg):
     # the gradient against central differences of sum(dH * silu(gate) * up) in
     # binary64; K = N with identity weights, so that dH = dY
