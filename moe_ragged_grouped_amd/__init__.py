@@ -119,6 +119,13 @@ def _check(status: int, what: str):
         raise GroupedGemmError("%s: status %d (%s)" % (what, status, msg))
 
 
+def _int32(what, sizes):
+    """Refuses what the C entry points, which count in int32, would see cut off.
+    sizes: all of them OR-ed together, which is one test for the lot."""
+    if sizes >> 31 not in (0, -1):
+        _check(3, what)  # GG_ERR_UNSUPPORTED
+
+
 def _stream_handle(device, stream):
     import torch
     if stream is None:
@@ -126,9 +133,9 @@ def _stream_handle(device, stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _grouped_args(A, B, offsets):
+def _grouped_args(A, B, offsets, bm):
     """Checks A bf16 [M_cap, K], B bf16 [E, K, N], offsets int32 [E+1] (device,
-    contiguous); returns E, K, N, M_cap."""
+    contiguous) and that all sizes fit int32; returns E, K, N, M_cap."""
     import torch
     if A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
         raise TypeError("A and B must be bfloat16")
@@ -145,6 +152,7 @@ def _grouped_args(A, B, offsets):
     if A.shape[1] != K or offsets.shape[0] != E + 1:
         raise ValueError("shape mismatch: A %s, B %s, offsets %s" % (tuple(A.shape), tuple(B.shape),
                                                                       tuple(offsets.shape)))
+    _int32("grouped_gemm", E | K | N | M_cap | int(bm))
     return E, K, N, M_cap
 
 
@@ -160,7 +168,7 @@ def grouped_gemm(A, B, offsets, out=None, bm: int = 0, stream=None, out_dtype=No
     """
     import torch
     lib = load_library()
-    E, K, N, M_cap = _grouped_args(A, B, offsets)
+    E, K, N, M_cap = _grouped_args(A, B, offsets, bm)
     if out is None:
         dt = torch.float32 if out_dtype is None else out_dtype
         if dt not in (torch.float32, torch.bfloat16):
@@ -187,7 +195,7 @@ def grouped_gemm_swiglu(A, B, offsets, out=None, bm: int = 0, stream=None):
     """
     import torch
     lib = load_library()
-    E, K, N, M_cap = _grouped_args(A, B, offsets)
+    E, K, N, M_cap = _grouped_args(A, B, offsets, bm)
     if out is None:
         out = torch.empty((M_cap, N // 2), dtype=torch.bfloat16, device=A.device)
     elif (out.dtype != torch.bfloat16 or tuple(out.shape) != (M_cap, N // 2)
@@ -228,6 +236,7 @@ def grouped_gemm_gather(X, src_rows, B, offsets, dst_rows=None, out=None, bm: in
     if X.shape[1] != K or offsets.shape[0] != E + 1 or (
             dst_rows is not None and dst_rows.shape[0] != M_cap):
         raise ValueError("shape mismatch")
+    _int32("grouped_gemm_gather", E | K | N | M_cap | n_src | int(bm))
     if out is None:
         out = torch.empty((M_cap, N), dtype=torch.float32, device=X.device)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M_cap, N) or not out.is_contiguous():
@@ -272,11 +281,13 @@ def grouped_gemm_gather_combine(X, src_rows, B, offsets, dst_rows, weights, out=
     if (X.shape[1] != K or offsets.shape[0] != E + 1 or dst_rows.shape[0] != M_cap
             or weights.shape[0] != M_cap):
         raise ValueError("shape mismatch")
+    _int32("grouped_gemm_gather_combine", E | K | N | M_cap | n_src | int(n_dst or 0) | int(bm))
     if out is None:
         out = torch.zeros((n_src if n_dst is None else int(n_dst), N), dtype=torch.float32,
                           device=X.device)
     elif out.dtype != torch.float32 or out.dim() != 2 or out.shape[1] != N or not out.is_contiguous():
         raise ValueError("out must be a contiguous fp32 [n_dst, N] tensor")
+    _int32("grouped_gemm_gather_combine", out.shape[0])
     st = lib.gg_grouped_gemm_bf16_gather_combine(
         X.data_ptr(), n_src, src_rows.data_ptr(), B.data_ptr(), offsets.data_ptr(),
         dst_rows.data_ptr(), weights.data_ptr(), out.data_ptr(), out.shape[0], E, K, N, M_cap,
@@ -306,6 +317,7 @@ def grouped_gemm_fp8w(A, Bq, b_scale, offsets, out=None, bm: int = 0, stream=Non
     M_cap = A.shape[0]
     if A.shape[1] != K or tuple(b_scale.shape) != (E, N) or offsets.shape[0] != E + 1:
         raise ValueError("shape mismatch")
+    _int32("grouped_gemm_fp8w", E | K | N | M_cap | int(bm))
     if out is None:
         out = torch.empty((M_cap, N), dtype=torch.float32, device=A.device)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M_cap, N) or not out.is_contiguous():
@@ -345,6 +357,7 @@ def grouped_gemm_fp8(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, s
     if (Aq.shape[1] != K or a_scale.shape[0] != M_cap or tuple(b_scale.shape) != (E, N)
             or offsets.shape[0] != E + 1):
         raise ValueError("shape mismatch")
+    _int32("grouped_gemm_fp8", E | K | N | M_cap | int(bm))
     if out is None:
         dt = torch.float32 if out_dtype is None else out_dtype
         if dt not in (torch.float32, torch.bfloat16):
@@ -384,6 +397,7 @@ def grouped_gemm_fp8_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
     if (Aq.dim() != 2 or Aq.shape[1] != K or tuple(a_scale.shape) != (M_cap,)
             or tuple(b_scale.shape) != (E, N) or tuple(offsets.shape) != (E + 1,)):
         raise ValueError("shape mismatch")
+    _int32("grouped_gemm_fp8_swiglu", E | K | N | M_cap | int(bm))
     if out is None:
         out = torch.empty((M_cap, N // 2), dtype=torch.bfloat16, device=Aq.device)
     elif (out.dtype != torch.bfloat16 or tuple(out.shape) != (M_cap, N // 2)
@@ -481,6 +495,7 @@ def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_d
     E, K, N = B.shape
     M_cap = dC.shape[0]
     _match(what, dC.shape[1] == N and offsets.shape[0] == E + 1, dC, B, offsets)
+    _int32(what, E | K | N | M_cap | int(bm))
     out = _out(what, out, (M_cap, K), (torch.float32, torch.bfloat16), out_dtype, dC, stream)
     name = "gg_grouped_gemm_bf16_dgrad" + ("" if out.dtype == torch.float32 else "_bf16out")
     _call(name, dev, stream, dC.data_ptr(), B.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K,
@@ -509,6 +524,7 @@ def grouped_gemm_dgrad_swiglu(dY, B, offsets, C, out=None, out_h=None, with_h: b
     M_cap = dY.shape[0]
     _match(what, dY.shape[1] == N and offsets.shape[0] == E + 1
            and C.shape == (M_cap, 2 * K), dY, B, offsets, C)
+    _int32(what, E | K | N | M_cap | int(bm))
     out = _out(what, out, (M_cap, 2 * K), (bf,), None, dY, stream)
     h = None
     if with_h or out_h is not None:
@@ -537,12 +553,13 @@ def grouped_gemm_wgrad(A, dC, offsets, out=None, accumulate: bool = False, strea
     N = dC.shape[1]
     E = offsets.shape[0] - 1
     _match(what, dC.shape[0] == M_cap and E >= 1, A, dC, offsets)
+    _int32(what, E | K | N | M_cap)
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("%s: accumulate needs an fp32 out to add to" % what)
     out = _out(what, out, (E, K, N), (torch.float32, torch.bfloat16), out_dtype, A, stream)
     args = (A.data_ptr(), dC.data_ptr(), offsets.data_ptr(), out.data_ptr())
     if out.dtype == torch.float32:
-        _call("gg_grouped_gemm_bf16_wgrad", dev, stream, *args, int(accumulate), E, K, N, M_cap)
+        _call("gg_grouped_gemm_bf16_wgrad", dev, stream, *args, int(bool(accumulate)), E, K, N, M_cap)
     else:
         _call("gg_grouped_gemm_bf16_wgrad_bf16out", dev, stream, *args, E, K, N, M_cap)
     return out
@@ -566,6 +583,7 @@ def mx4_quantize(X, out=None, out_scale=None, stream=None):
     what = "mx4_quantize"
     dev = _device_args(what, ("X", X, torch.bfloat16, 2))
     M, K = X.shape
+    _int32(what, K)
     u8 = (torch.uint8,)
     q = _out(what, out, (M, K // 2), u8, None, X, stream)
     s = _out(what, out_scale, (_mx4_slices(K), M, 8), u8, None, X, stream)
@@ -583,6 +601,7 @@ def mx4_quantize_weights(B, out=None, out_scale=None, stream=None):
     what = "mx4_quantize_weights"
     dev = _device_args(what, ("B", B, torch.bfloat16, 3))
     E, K, N = B.shape
+    _int32(what, E | K | N)
     u8 = (torch.uint8,)
     q = _out(what, out, (E, N, K // 2), u8, None, B, stream)
     s = _out(what, out_scale, (E, _mx4_slices(K), N, 8), u8, None, B, stream)
@@ -603,6 +622,7 @@ def mx4_dequantize(q, scales, out=None, stream=None):
     dev = _device_args(what, ("q", q, torch.uint8, q.dim()), ("scales", scales, torch.uint8, q.dim() + 1))
     batch = q.shape[0] if q.dim() == 3 else 1
     rows, K = q.shape[-2], 2 * q.shape[-1]
+    _int32(what, batch | K)
     lead = (batch,) if q.dim() == 3 else ()
     _match(what, scales.shape == lead + (_mx4_slices(K), rows, 8), q, scales)
     y = _out(what, out, lead + (rows, K), (torch.bfloat16,), None, q, stream)
@@ -611,7 +631,7 @@ def mx4_dequantize(q, scales, out=None, stream=None):
     return y
 
 
-def _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets):
+def _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets, bm):
     import torch
     u8 = torch.uint8
     dev = _device_args(what, ("Aq", Aq, u8, 2), ("a_scale", a_scale, u8, 3), ("Bq", Bq, u8, 3),
@@ -621,6 +641,7 @@ def _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets):
     _match(what, Aq.shape[1] == half and offsets.shape[0] == E + 1
            and a_scale.shape == (_mx4_slices(K), M_cap, 8)
            and b_scale.shape == (E, _mx4_slices(K), N, 8), Aq, a_scale, Bq, b_scale, offsets)
+    _int32(what, E | K | N | M_cap | bm)
     return dev, E, K, N, M_cap
 
 
@@ -636,7 +657,7 @@ def grouped_gemm_mx4(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, s
     """
     import torch
     what = "grouped_gemm_mx4"
-    dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets)
+    dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets, int(bm))
     out = _out(what, out, (M_cap, N), (torch.float32, torch.bfloat16), out_dtype, Aq, stream)
     name = "gg_grouped_gemm_mx4" + ("" if out.dtype == torch.float32 else "_bf16out")
     _call(name, dev, stream, Aq.data_ptr(), a_scale.data_ptr(), Bq.data_ptr(), b_scale.data_ptr(),
@@ -652,7 +673,7 @@ def grouped_gemm_mx4_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
     """
     import torch
     what = "grouped_gemm_mx4_swiglu"
-    dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets)
+    dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets, int(bm))
     out = _out(what, out, (M_cap, N // 2), (torch.bfloat16,), None, Aq, stream)
     _call("gg_grouped_gemm_mx4_swiglu", dev, stream, Aq.data_ptr(), a_scale.data_ptr(),
           Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap,
@@ -670,6 +691,7 @@ def tile_schedule(offsets, N: int, M_cap: int, bm: int = 0, max_tiles: int = Non
     if max_tiles is None:
         hmin = bm if bm else BM_CHOICES[0]
         max_tiles = (M_cap // hmin + E) * (-(-N // TILE_N))
+    _int32("tile_schedule", E | N | M_cap | int(bm) | int(max_tiles))
     tiles = torch.empty((max(max_tiles, 1), 5), dtype=torch.int32, device=offsets.device)
     n = torch.zeros(1, dtype=torch.int32, device=offsets.device)
     st = lib.gg_tile_schedule(offsets.data_ptr(), E, N, M_cap, int(bm), tiles.data_ptr(), n.data_ptr(),
@@ -716,7 +738,8 @@ def traced_grouped_gemm(A, B, offsets, max_tiles: int, out=None, bm: int = 0, st
     """
     import torch
     lib = load_trace_library()
-    E, K, N, M_cap = _grouped_args(A, B, offsets)
+    E, K, N, M_cap = _grouped_args(A, B, offsets, bm)
+    _int32("traced_grouped_gemm", int(max_tiles))
     if out is None:
         out = torch.empty((M_cap, N), dtype=torch.float32, device=A.device)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M_cap, N) or not out.is_contiguous():

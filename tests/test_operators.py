@@ -227,6 +227,50 @@ def test_host_tensors_and_wrong_ranks_are_refused(call):
         call()
 
 
+BIG = 2 ** 32 + 32  # what is left of it in 32 bits is a size like any other
+
+
+def _fake(kind, *shape):
+    dt = {"bf": torch.bfloat16, "u8": torch.uint8, "i": torch.int32, "f": torch.float32}[kind]
+    return torch.empty(shape, dtype=dt, device="cuda")
+
+
+@pytest.mark.parametrize("call", [
+    lambda t: gg.grouped_gemm_dgrad(t("bf", BIG, 8), t("bf", 2, 8, 8), t("i", 3)),
+    lambda t: gg.grouped_gemm_dgrad(t("bf", 4, BIG), t("bf", 2, 8, BIG), t("i", 3)),
+    lambda t: gg.grouped_gemm_dgrad(t("bf", 4, 8), t("bf", 2, BIG, 8), t("i", 3)),
+    lambda t: gg.grouped_gemm_dgrad(t("bf", 4, 8), t("bf", 2, 8, 8), t("i", 3), bm=2 ** 32 + 16),
+    lambda t: gg.grouped_gemm_dgrad(t("bf", 4, 8), t("bf", 2, 8, 8), t("i", 3), bm=16 - 2 ** 32),
+    lambda t: gg.grouped_gemm_dgrad_swiglu(t("bf", BIG, 8), t("bf", 2, 8, 8), t("i", 3), t("bf", BIG, 16)),
+    lambda t: gg.grouped_gemm_wgrad(t("bf", BIG, 8), t("bf", BIG, 8), t("i", 3)),
+    lambda t: gg.grouped_gemm_wgrad(t("bf", 4, BIG), t("bf", 4, 8), t("i", 3)),
+    lambda t: gg.grouped_gemm_wgrad(t("bf", 4, 8), t("bf", 4, 8), t("i", BIG + 1)),
+    lambda t: gg.mx4_quantize(t("bf", 1, BIG)),
+    lambda t: gg.mx4_quantize_weights(t("bf", 1, 32, BIG)),
+    lambda t: gg.mx4_quantize_weights(t("bf", BIG, 32, 8)),
+    lambda t: gg.mx4_dequantize(t("u8", 1, BIG // 2), t("u8", BIG // 256 + 1, 1, 8)),
+    lambda t: gg.grouped_gemm_mx4(t("u8", BIG, 16), t("u8", 1, BIG, 8), t("u8", 2, 8, 16), t("u8", 2, 1, 8, 8), t("i", 3)),
+    lambda t: gg.grouped_gemm_mx4_swiglu(t("u8", 4, 16), t("u8", 1, 4, 8), t("u8", 2, BIG, 16), t("u8", 2, 1, BIG, 8),
+                                         t("i", 3)),
+    lambda t: gg.grouped_gemm(t("bf", BIG, 8), t("bf", 2, 8, 8), t("i", 3)),
+    lambda t: gg.grouped_gemm_swiglu(t("bf", 4, 8), t("bf", 2, 8, BIG), t("i", 3)),
+    lambda t: gg.grouped_gemm_gather(t("bf", BIG, 8), t("i", 4), t("bf", 2, 8, 8), t("i", 3)),
+    lambda t: gg.grouped_gemm_gather_combine(t("bf", 4, 8), t("i", 4), t("bf", 2, 8, 8), t("i", 3), t("i", 4), t("f", 4),
+                                             n_dst=BIG),
+    lambda t: gg.grouped_gemm_gather_combine(t("bf", 4, 8), t("i", 4), t("bf", 2, 8, 8), t("i", 3), t("i", 4), t("f", 4),
+                                             out=t("f", BIG, 8)),
+    lambda t: gg.grouped_gemm_fp8w(t("bf", 4, BIG), t("u8", 2, BIG, 8), t("f", 2, 8), t("i", 3)),
+    lambda t: gg.grouped_gemm_fp8(t("u8", BIG, 16), t("f", BIG), t("u8", 2, 16, 16), t("f", 2, 16), t("i", 3)),
+    lambda t: gg.grouped_gemm_fp8_swiglu(t("u8", 4, 16), t("f", 4), t("u8", 2, 16, BIG), t("f", 2, BIG), t("i", 3)),
+    lambda t: gg.tile_schedule(t("i", 3), 8, BIG),
+])
+def test_sizes_beyond_int32_are_refused(lib, call):
+    # shapes only: neither memory nor a GPU stands behind these tensors
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode(), pytest.raises(gg.GroupedGemmError, match="status 3"):
+        call(_fake)
+
+
 # --------------------------------------------------------------- the build
 
 @pytest.mark.skipif(not os.path.exists(hb.HIPCC), reason="hipcc not available")
