@@ -30,6 +30,9 @@
  *    overlap; if the tiles of all groups then outnumber what M_cap rows can
  *    produce with nondecreasing offsets, ((M_cap / h) + E) * ceil(N / 256)
  *    for the smallest height h in use, the call computes nothing at all.
+ *  - An output may not share memory with another array of the call (the
+ *    gradients and the 4-bit entry points return GG_ERR_INVALID_VALUE; the one
+ *    exception is named there).
  *  - Calls on different streams may run concurrently; the library holds no
  *    mutable state besides a per-device cache of launch limits.
  */
@@ -330,7 +333,7 @@ gg_status_t gg_grouped_gemm_bf16_dgrad_bf16out(const void *dC, const void *B,
  *       gg_grouped_gemm_bf16_bf16out gives them;
  *   dC  bf16 [M_cap][2K], and H bf16 [M_cap][K] or NULL: the operand of the down
  *       projection's weight gradient, which a forward pass that kept only C has
- *       not stored. dC may be C itself. Rows at or beyond off[E] of C are not
+ *       not stored. dC may be C itself, from its start. Rows at or beyond off[E] of C are not
  *       read, of dC and H not written. All are 16-byte aligned.
  * Everything is evaluated in fp32 (hardware exp2 and reciprocal, each within one
  * ulp) and rounded once to bf16 on its way out. s is 0 where it would be subnormal

@@ -26,6 +26,24 @@ inline bool valid_bm(int bm) {
   return bm == 0 || bm == 16 || bm == 32 || bm == 64 || bm == 128 || bm == 256;
 }
 
+// An array of a call: its memory. Tiles are stored while others still read, so
+// an output that shares memory with anything else of the call would race.
+struct Span {
+  const void *p;
+  unsigned long long bytes;
+};
+inline Span span(const void *p, long long n, long long m, long long bytes) {
+  return Span{p, p == nullptr ? 0ull : (unsigned long long)n * (unsigned long long)m * bytes};
+}
+inline bool apart(Span a, Span b) {
+  const unsigned long long x = (uintptr_t)a.p, y = (uintptr_t)b.p;  // sizes are below 2^60
+  return a.bytes == 0 || b.bytes == 0 || x + a.bytes <= y || y + b.bytes <= x;
+}
+template <class... S>
+inline bool apart(Span a, Span b, S... others) {
+  return apart(a, b) && apart(a, others...);
+}
+
 // Groups, rows and tile height; upper bounds of the row tiles and of the tiles
 // of a product with `cols` output columns (narrowest tiles: `narrow` columns).
 inline gg_status_t check_groups(const int32_t *off, int E, int cols, int M_cap, int bm, int narrow,

@@ -187,6 +187,13 @@ static gg_status_t dgrad(DgradParams p, void *stream) {
   if (!is_aligned(p.dC, 16) || !is_aligned(p.B, 16) || !is_aligned(p.out, 16) ||
       !is_aligned(p.C, 16) || !is_aligned(p.H, 16))
     return GG_ERR_MISALIGNED;
+  const int out_bytes = O == DOut::BF16 ? 2 : 4;  // of an element, or a pair of columns
+  const Span dC = span(p.dC, p.M_cap, p.N, 2), B = span(p.B, (long long)p.E * p.K, p.N, 2),
+             off = span(p.off, p.E + 1, 1, 4), out = span(p.out, p.M_cap, p.K, out_bytes),
+             C = span(p.C, p.M_cap, p.K, 4), H = span(p.H, p.M_cap, p.K, 2);
+  // (each tile's columns of C are read before it stores them: in place is safe)
+  if (!apart(out, dC, B, off, H) || !apart(H, dC, B, off, C) || !(p.out == p.C || apart(out, C)))
+    return GG_ERR_INVALID_VALUE;
   if (p.M_cap == 0) return GG_OK;
   int dev = 0;
   if (!current_device(&dev)) return GG_ERR_LAUNCH;

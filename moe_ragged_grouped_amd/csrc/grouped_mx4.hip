@@ -373,6 +373,12 @@ static gg_status_t mx4_product(const void *Aq, const void *a_scale, const void *
   if (!is_aligned(Aq, 16) || !is_aligned(a_scale, 16) || !is_aligned(Bq, 16) ||
       !is_aligned(b_scale, 16) || !is_aligned(C, 16))
     return GG_ERR_MISALIGNED;
+  const long long slices = (K + (long long)kSliceK - 1) / kSliceK;
+  if (!apart(span(C, M_cap, O == MOut::SwiGlu ? N / 2 : N, O == MOut::F32 ? 4 : 2),
+             span(Aq, M_cap, K / 2, 1), span(a_scale, slices * M_cap, kSliceBlocks, 1),
+             span(Bq, (long long)E * N, K / 2, 1),
+             span(b_scale, (long long)E * N, slices * kSliceBlocks, 1), span(off, E + 1, 1, 4)))
+    return GG_ERR_INVALID_VALUE;
   if (M_cap == 0) return GG_OK;
   const Mx4Params p{static_cast<const char *>(Aq), static_cast<const char *>(a_scale),
                     static_cast<const char *>(Bq), static_cast<const char *>(b_scale), off, C, E, K,
@@ -384,6 +390,14 @@ static gg_status_t mx4_product(const void *Aq, const void *a_scale, const void *
   hipLaunchKernelGGL((mx4_product_kernel<O>), dim3((unsigned)li.workgroups(tiles)), dim3(kThreads),
                      kMx4Lds, static_cast<hipStream_t>(stream), p);
   return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+}
+
+// Full-width values, codes and scales of `rows` rows, none overlapping another.
+static bool rows_apart(const void *values, const void *q, const void *scales, long long rows,
+                       long long K) {
+  const Span v = span(values, rows, K, 2), c = span(q, rows, K / 2, 1),
+             s = span(scales, rows, (K + kSliceK - 1) / kSliceK * kSliceBlocks, 1);
+  return apart(v, c, s) && apart(c, s);
 }
 
 // Sizes of the row kernels: blocks of a launch, within the grid's limit.
@@ -408,6 +422,7 @@ extern "C" gg_status_t gg_mx4_quantize(const void *X, void *q, void *scales, int
   if (rows == 0) return GG_OK;
   if (X == nullptr || q == nullptr || scales == nullptr) return GG_ERR_INVALID_VALUE;
   if (!is_aligned(X, 16) || !is_aligned(q, 16) || !is_aligned(scales, 16)) return GG_ERR_MISALIGNED;
+  if (!rows_apart(X, q, scales, rows, K)) return GG_ERR_INVALID_VALUE;
   hipLaunchKernelGGL(mx4_rows_kernel, dim3((unsigned)blocks), dim3(kQThreads), 0,
                      static_cast<hipStream_t>(stream), static_cast<const u32x4 *>(X),
                      static_cast<u32x4 *>(q), static_cast<uint8_t *>(scales), (long long)rows, K);
@@ -425,6 +440,7 @@ extern "C" gg_status_t gg_mx4_quantize_weights(const void *B, void *q, void *sca
   if (E > kMaxExperts || K > GG_MAX_K || N > GG_MAX_N ||
       !launch_fits(slices * cols * E, kWqThreads))
     return GG_ERR_UNSUPPORTED;
+  if (!rows_apart(B, q, scales, (long long)E * N, K)) return GG_ERR_INVALID_VALUE;
   hipLaunchKernelGGL(mx4_weights_kernel, dim3((unsigned)(slices * cols * E)), dim3(kWqThreads), 0,
                      static_cast<hipStream_t>(stream), static_cast<const uint16_t *>(B),
                      static_cast<uint8_t *>(q), static_cast<uint8_t *>(scales), K, N, (int)slices,
@@ -442,6 +458,7 @@ extern "C" gg_status_t gg_mx4_dequantize(const void *q, const void *scales, void
   if (rows == 0 || batch == 0) return GG_OK;
   if (q == nullptr || scales == nullptr || Y == nullptr) return GG_ERR_INVALID_VALUE;
   if (!is_aligned(q, 16) || !is_aligned(scales, 16) || !is_aligned(Y, 16)) return GG_ERR_MISALIGNED;
+  if (!rows_apart(Y, q, scales, batch * rows, K)) return GG_ERR_INVALID_VALUE;
   hipLaunchKernelGGL(mx4_values_kernel, dim3((unsigned)blocks, (unsigned)batch), dim3(kQThreads), 0,
                      static_cast<hipStream_t>(stream), static_cast<const uint32_t *>(q),
                      static_cast<const uint8_t *>(scales), static_cast<u32x4 *>(Y),

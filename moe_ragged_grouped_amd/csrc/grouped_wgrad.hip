@@ -354,6 +354,9 @@ static gg_status_t launch_wgrad(WgradParams p, hipStream_t stream) {
   const long long per = (tiles + kRingXcds - 1) / kRingXcds;
   const long long grid = per * kRingXcds * p.E;
   if (!launch_fits(grid, C::THREADS)) return GG_ERR_UNSUPPORTED;
+  if (!apart(span(p.dB, (long long)p.E * p.K, p.N, O == WOut::BF16 ? 2 : 4), span(p.A, p.M_cap, p.K, 2),
+             span(p.dC, p.M_cap, p.N, 2), span(p.off, p.E + 1, 1, 4)))
+    return GG_ERR_INVALID_VALUE;
   int dev = 0;
   if (!current_device(&dev)) return GG_ERR_LAUNCH;
   if (ring_launch<wgrad_kernel<C, O>>(dev, lds).err != hipSuccess) return GG_ERR_LAUNCH;

@@ -415,6 +415,39 @@ def test_same_bits_twice(gg):
         assert torch.equal(f(), f())
 
 
+def test_arrays_side_by_side(gg):
+    # inputs and outputs that meet end to start inside one buffer are apart
+    rng = np.random.default_rng(16)
+    M, K, N, E = 40, 72, 136, 2
+    off = ops.to_dev(ops.offsets_of([33, 7]))
+    parts = [(M, N), (M, K), (E, K, N), (E, K, N), (M, 2 * K), (M, 2 * K), (M, K)]
+    dC, dA, B, dB, C, d, H = torch.zeros(sum(int(np.prod(p)) for p in parts), dtype=torch.bfloat16,
+                                         device="cuda:0").split([int(np.prod(p)) for p in parts])
+    dC, dA, B, dB, C, d, H = (t.view(p) for t, p in zip((dC, dA, B, dB, C, d, H), parts))
+    for t in (dC, B, C):
+        t.copy_(ops.to_dev(ops.bits(rng, *t.shape)))
+    want = gg.grouped_gemm_dgrad(dC, B, off, out_dtype=torch.bfloat16)
+    assert torch.equal(gg.grouped_gemm_dgrad(dC, B, off, out=dA), want)
+    want_d, want_h = gg.grouped_gemm_dgrad_swiglu(dC, B, off, C, with_h=True)
+    gg.grouped_gemm_dgrad_swiglu(dC, B, off, C, out=d, out_h=H)
+    assert torch.equal(d, want_d) and torch.equal(H, want_h)
+    want = gg.grouped_gemm_wgrad(dA, dC, off, out_dtype=torch.bfloat16)
+    assert torch.equal(gg.grouped_gemm_wgrad(dA, dC, off, out=dB), want)
+
+
+def test_outputs_over_inputs_are_refused(gg):
+    off = ops.to_dev(ops.offsets_of([40]))
+    X = torch.zeros((40, 64), dtype=torch.bfloat16, device="cuda:0")
+    B = torch.zeros((1, 64, 64), dtype=torch.bfloat16, device="cuda:0")
+    C = torch.zeros((41, 128), dtype=torch.bfloat16, device="cuda:0")
+    for call in (lambda: gg.grouped_gemm_dgrad(X, B, off, out=X),
+                 lambda: gg.grouped_gemm_dgrad_swiglu(X, B, off, C[:40], out=C[1:]),
+                 lambda: gg.grouped_gemm_dgrad_swiglu(X, B, off, C[:40], out_h=X),
+                 lambda: gg.grouped_gemm_wgrad(B[0][:40], X, off, out=B)):
+        with pytest.raises(gg.GroupedGemmError, match="status 1"):
+            call()
+
+
 @pytest.mark.parametrize("offs", [[0, 9, 4, 30], [-5, 10, 20, 30], [0, 10, 99, 30], [7, 7, 7, 7],
                                   [30, 20, 10, 0]])
 def test_malformed_offsets_stay_inside(gg, offs):

@@ -20,7 +20,7 @@ import oracle.operators as ref
 import workloads as wl
 from tests import operators as ops
 
-INVALID, MISALIGNED, UNSUPPORTED = 1, 2, 3
+INVALID, MISALIGNED, UNSUPPORTED, NO_DEVICE = 1, 2, 3, 4
 
 
 # ---------------------------------------------------------------- references
@@ -175,6 +175,46 @@ def test_mx4_row_host_checks(lib):
     assert d(c=24) == d(s=40) == d(Y=56) == d(K=40) == MISALIGNED
     assert d(b=65536) == d(rows=2 ** 31) == UNSUPPORTED
     assert d(b=0) == d(rows=0) == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: for hosts without a GPU")
+def test_overlapping_arrays_are_refused(lib):
+    # each output over the first and the last 16 bytes of every other array, all others
+    # 2^40 apart; every call is refused (an accepted one would end in a missing device here)
+    E, K, N, M = 4, 288, 136, 30
+    rows = 16 * 2
+    D = {"dC": M * N * 2, "B": E * K * N * 2, "off": rows, "A": M * K * 2, "C": M * K * 4, "H": M * K * 2,
+         "Aq": M * K // 2, "a_scale": 2 * M * 8, "Bq": E * N * K // 2, "b_scale": E * 2 * N * 8}
+    calls = {
+        "gg_grouped_gemm_bf16_dgrad": ("dC B off *", M * K * 4, (E, K, N, M, 0)),
+        "gg_grouped_gemm_bf16_dgrad_bf16out": ("dC B off *", M * K * 2, (E, K, N, M, 0)),
+        "gg_grouped_gemm_bf16_dgrad_swiglu": ("dC B off C * H", M * K * 4, (E, K, N, M, 0)),
+        "gg_grouped_gemm_bf16_wgrad": ("A dC off *", E * K * N * 4, (0, E, K, N, M)),
+        "gg_grouped_gemm_bf16_wgrad_bf16out": ("A dC off *", E * K * N * 2, (E, K, N, M)),
+        "gg_grouped_gemm_mx4": ("Aq a_scale Bq b_scale off *", M * N * 4, (E, K, N, M, 0)),
+        "gg_grouped_gemm_mx4_bf16out": ("Aq a_scale Bq b_scale off *", M * N * 2, (E, K, N, M, 0)),
+        "gg_grouped_gemm_mx4_swiglu": ("Aq a_scale Bq b_scale off *", M * N, (E, K, N, M, 0)),
+        "gg_mx4_quantize": ("A * a_scale", M * K // 2, (M, K)),
+        "gg_mx4_quantize_weights": ("B * b_scale", E * N * K // 2, (E, K, N)),
+        "gg_mx4_dequantize": ("Bq b_scale *", E * N * K * 2, (E, N, K)),
+    }
+    for entry, (names, out_bytes, sizes) in calls.items():
+        names = names.split()
+        size = dict(D, **{"*": out_bytes})
+        home = {n: (i + 1) << 40 for i, n in enumerate(names)}
+        args = [home[n] for n in names]
+        assert getattr(lib, entry)(*args, *sizes, None) == NO_DEVICE, entry
+        if "C" in names:  # in place
+            args[names.index("*")] = home["C"]
+            assert getattr(lib, entry)(*args, *sizes, None) == NO_DEVICE, entry
+        pairs = [("*", n) for n in names if n != "*"]
+        pairs += [("H", n) for n in names if n != "H"] if "H" in names else []
+        pairs += [(n, "*") for n in names if n.endswith("scale") and "quantize" in entry]
+        for moved, onto in pairs:
+            for at in (home[onto] + (16 if (moved, onto) == ("*", "C") else 0),
+                       home[onto] + (size[onto] - 1) // 16 * 16, home[onto] - (size[moved] - 1) // 16 * 16):
+                args = [at if n == moved else home[n] for n in names]
+                assert getattr(lib, entry)(*args, *sizes, None) == INVALID, (entry, moved, onto, at - home[onto])
 
 
 def test_launches_of_2_to_the_32_threads_are_refused(lib):
