@@ -456,8 +456,10 @@ def _out(what, out, shape, dtypes, dtype, like, stream):
     return out
 
 
-def _call(name, dev, stream, *args):
-    """Calls one entry point on the tensors' device, whichever is current."""
+def _call(name, dev, stream, tensors, *args):
+    """Calls one entry point on the tensors' device, whichever is current. On a
+    stream given by the caller the memory of all tensors is kept until that
+    stream has passed the call, so that they may be dropped at once."""
     import torch
     fn = getattr(load_library(), name)
     if stream is not None:
@@ -473,10 +475,9 @@ def _call(name, dev, stream, *args):
             st = fn(*args, handle)
     if st != 0:
         _check(st, name)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
 
 
 def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_dtype=None):
@@ -487,6 +488,11 @@ def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_d
     or bf16 [M_cap, K] (out_dtype, default fp32, when out is not given; bf16 is
     the fp32 sum rounded to nearest even). offsets, bm and stream as in
     grouped_gemm. Rows at or past offsets[E] are left as they were.
+
+    Here and below: with ``stream``, the call is ordered on that stream alone (it
+    waits for no other), the memory of its tensors is kept until it is done, and
+    a tensor made for the result belongs to that stream. An output may not share
+    memory with another argument.
     """
     import torch
     what = "grouped_gemm_dgrad"
@@ -498,8 +504,8 @@ def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_d
     _int32(what, E | K | N | M_cap | int(bm))
     out = _out(what, out, (M_cap, K), (torch.float32, torch.bfloat16), out_dtype, dC, stream)
     name = "gg_grouped_gemm_bf16_dgrad" + ("" if out.dtype == torch.float32 else "_bf16out")
-    _call(name, dev, stream, dC.data_ptr(), B.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K,
-          N, M_cap, int(bm))
+    _call(name, dev, stream, (dC, B, offsets, out), dC.data_ptr(), B.data_ptr(), offsets.data_ptr(),
+          out.data_ptr(), E, K, N, M_cap, int(bm))
     return out
 
 
@@ -529,8 +535,10 @@ def grouped_gemm_dgrad_swiglu(dY, B, offsets, C, out=None, out_h=None, with_h: b
     h = None
     if with_h or out_h is not None:
         h = _out(what, out_h, (M_cap, K), (bf,), None, dY, stream)
-    _call("gg_grouped_gemm_bf16_dgrad_swiglu", dev, stream, dY.data_ptr(), B.data_ptr(),
-          offsets.data_ptr(), C.data_ptr(), out.data_ptr(), _ptr(h), E, K, N, M_cap, int(bm))
+    outs = (out,) if h is None else (out, h)
+    _call("gg_grouped_gemm_bf16_dgrad_swiglu", dev, stream, (dY, B, offsets, C, *outs), dY.data_ptr(),
+          B.data_ptr(), offsets.data_ptr(), C.data_ptr(), out.data_ptr(),
+          None if h is None else h.data_ptr(), E, K, N, M_cap, int(bm))
     return out if h is None else (out, h)
 
 
@@ -557,7 +565,7 @@ def grouped_gemm_wgrad(A, dC, offsets, out=None, accumulate: bool = False, strea
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("%s: accumulate needs an fp32 out to add to" % what)
     out = _out(what, out, (E, K, N), (torch.float32, torch.bfloat16), out_dtype, A, stream)
-    args = (A.data_ptr(), dC.data_ptr(), offsets.data_ptr(), out.data_ptr())
+    args = ((A, dC, offsets, out), A.data_ptr(), dC.data_ptr(), offsets.data_ptr(), out.data_ptr())
     if out.dtype == torch.float32:
         _call("gg_grouped_gemm_bf16_wgrad", dev, stream, *args, int(bool(accumulate)), E, K, N, M_cap)
     else:
@@ -587,7 +595,7 @@ def mx4_quantize(X, out=None, out_scale=None, stream=None):
     u8 = (torch.uint8,)
     q = _out(what, out, (M, K // 2), u8, None, X, stream)
     s = _out(what, out_scale, (_mx4_slices(K), M, 8), u8, None, X, stream)
-    _call("gg_mx4_quantize", dev, stream, X.data_ptr(), q.data_ptr(), s.data_ptr(), M, K)
+    _call("gg_mx4_quantize", dev, stream, (X, q, s), X.data_ptr(), q.data_ptr(), s.data_ptr(), M, K)
     return q, s
 
 
@@ -605,7 +613,8 @@ def mx4_quantize_weights(B, out=None, out_scale=None, stream=None):
     u8 = (torch.uint8,)
     q = _out(what, out, (E, N, K // 2), u8, None, B, stream)
     s = _out(what, out_scale, (E, _mx4_slices(K), N, 8), u8, None, B, stream)
-    _call("gg_mx4_quantize_weights", dev, stream, B.data_ptr(), q.data_ptr(), s.data_ptr(), E, K, N)
+    _call("gg_mx4_quantize_weights", dev, stream, (B, q, s), B.data_ptr(), q.data_ptr(), s.data_ptr(), E,
+          K, N)
     return q, s
 
 
@@ -626,8 +635,8 @@ def mx4_dequantize(q, scales, out=None, stream=None):
     lead = (batch,) if q.dim() == 3 else ()
     _match(what, scales.shape == lead + (_mx4_slices(K), rows, 8), q, scales)
     y = _out(what, out, lead + (rows, K), (torch.bfloat16,), None, q, stream)
-    _call("gg_mx4_dequantize", dev, stream, q.data_ptr(), scales.data_ptr(), y.data_ptr(), batch,
-          rows, K)
+    _call("gg_mx4_dequantize", dev, stream, (q, scales, y), q.data_ptr(), scales.data_ptr(),
+          y.data_ptr(), batch, rows, K)
     return y
 
 
@@ -660,8 +669,8 @@ def grouped_gemm_mx4(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, s
     dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets, int(bm))
     out = _out(what, out, (M_cap, N), (torch.float32, torch.bfloat16), out_dtype, Aq, stream)
     name = "gg_grouped_gemm_mx4" + ("" if out.dtype == torch.float32 else "_bf16out")
-    _call(name, dev, stream, Aq.data_ptr(), a_scale.data_ptr(), Bq.data_ptr(), b_scale.data_ptr(),
-          offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap, int(bm))
+    _call(name, dev, stream, (Aq, a_scale, Bq, b_scale, offsets, out), Aq.data_ptr(), a_scale.data_ptr(),
+          Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap, int(bm))
     return out
 
 
@@ -675,9 +684,9 @@ def grouped_gemm_mx4_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
     what = "grouped_gemm_mx4_swiglu"
     dev, E, K, N, M_cap = _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets, int(bm))
     out = _out(what, out, (M_cap, N // 2), (torch.bfloat16,), None, Aq, stream)
-    _call("gg_grouped_gemm_mx4_swiglu", dev, stream, Aq.data_ptr(), a_scale.data_ptr(),
-          Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap,
-          int(bm))
+    _call("gg_grouped_gemm_mx4_swiglu", dev, stream, (Aq, a_scale, Bq, b_scale, offsets, out),
+          Aq.data_ptr(), a_scale.data_ptr(), Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(),
+          out.data_ptr(), E, K, N, M_cap, int(bm))
     return out
 
 

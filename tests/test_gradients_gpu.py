@@ -561,6 +561,65 @@ def test_two_streams_at_once(gg):
             assert all(torch.equal(a, b) for a, b in zip(g, w))
 
 
+def test_tensors_dropped_after_a_call_on_another_stream(gg):
+    # a busy stream runs the call long after its inputs and outputs were dropped and their
+    # memory could be handed out again: nothing of it may be, until the stream is through
+    s = torch.cuda.Stream()
+    off = ops.to_dev(ops.offsets_of([256, 256]))
+    ones = lambda *shape: torch.ones(shape, dtype=torch.bfloat16, device="cuda:0")  # noqa: E731
+    rows, weights = (lambda: ones(512, 512)), (lambda: ones(2, 512, 512))
+    codes = lambda: (*gg.mx4_quantize(rows()), *gg.mx4_quantize_weights(weights()))  # noqa: E731
+    calls = [
+        (lambda: (rows(), weights()), lambda a, b: gg.grouped_gemm_dgrad(a, b, off, stream=s), 512.0),
+        (lambda: (rows(), rows()), lambda a, b: gg.grouped_gemm_wgrad(a, b, off, stream=s), 256.0),
+        (lambda: (rows(), weights(), torch.zeros((512, 1024), dtype=torch.bfloat16, device="cuda:0")),
+         lambda a, b, c: gg.grouped_gemm_dgrad_swiglu(a, b, off, c, with_h=True, stream=s)[1], 0.0),
+        (lambda: (rows(),), lambda a: gg.mx4_dequantize(*gg.mx4_quantize(a, stream=s), stream=s), 1.0),
+        (lambda: (weights(),), lambda a: gg.mx4_dequantize(*gg.mx4_quantize_weights(a, stream=s), stream=s), 1.0),
+        (codes, lambda *c: gg.grouped_gemm_mx4(*c, off, stream=s), 512.0),
+        (codes, lambda *c: gg.grouped_gemm_mx4_swiglu(*c, off, stream=s), 512.0 ** 2)]
+    for make, call, want in calls:
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        args = make()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(30_000_000)
+        got = call(*args)
+        del args
+        spoil = [torch.full((2 ** 18,), 7.0, dtype=torch.bfloat16, device="cuda:0") for _ in range(24)]
+        torch.cuda.current_stream().synchronize()
+        assert not s.query(), "the stream was through before the memory was written"
+        s.synchronize()
+        assert (got == want).all()
+        del spoil
+
+
+def test_captured_with_the_stream_named(gg):
+    # the capturing stream passed by name, intermediate tensors dropped inside the capture
+    rng = np.random.default_rng(17)
+    off = ops.to_dev(ops.offsets_of([50, 14]))
+    A, dC = ops.to_dev(ops.bits(rng, 64, 136)), ops.to_dev(ops.bits(rng, 64, 264))
+    B = ops.to_dev(ops.bits(rng, 2, 136, 264))
+
+    def step(s=None):
+        d = gg.grouped_gemm_dgrad(dC, B, off, stream=s, out_dtype=torch.bfloat16)
+        return gg.grouped_gemm_wgrad(d, dC, off, stream=s), gg.grouped_gemm_wgrad(A, dC, off, stream=s)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(torch.cuda.current_stream())
+    for seed in (1, 2, 3):
+        dC.copy_(ops.to_dev(ops.bits(np.random.default_rng(seed), 64, 264)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(outs, step()):
+            assert torch.equal(got, want)
+
+
 def test_other_stream(gg):
     rng = np.random.default_rng(13)
     off = ops.to_dev(ops.offsets_of([50, 14]))
