@@ -133,6 +133,27 @@ def _stream_handle(device, stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _new(shape, dtype, like, stream, zero=False):
+    """A new tensor beside ``like`` for a call on ``stream`` to write: made (and
+    cleared) in that stream's order, and kept for the present stream too."""
+    import torch
+    if stream is None:
+        return like.new_zeros(shape, dtype=dtype) if zero else like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_zeros(shape, dtype=dtype) if zero else like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
+def _keep(stream, *tensors):
+    """Keeps the memory of a call's tensors until the stream that the caller named
+    has passed it, so that they may be dropped at once."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _grouped_args(A, B, offsets, bm):
     """Checks A bf16 [M_cap, K], B bf16 [E, K, N], offsets int32 [E+1] (device,
     contiguous) and that all sizes fit int32; returns E, K, N, M_cap."""
@@ -173,7 +194,7 @@ def grouped_gemm(A, B, offsets, out=None, bm: int = 0, stream=None, out_dtype=No
         dt = torch.float32 if out_dtype is None else out_dtype
         if dt not in (torch.float32, torch.bfloat16):
             raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
-        out = torch.empty((M_cap, N), dtype=dt, device=A.device)
+        out = _new((M_cap, N), dt, A, stream)
     elif (out.dtype not in (torch.float32, torch.bfloat16) or tuple(out.shape) != (M_cap, N)
           or not out.is_contiguous() or (out_dtype is not None and out.dtype != out_dtype)):
         raise ValueError("out must be a contiguous fp32 or bf16 [M_cap, N] tensor")
@@ -181,6 +202,7 @@ def grouped_gemm(A, B, offsets, out=None, bm: int = 0, stream=None, out_dtype=No
     st = fn(A.data_ptr(), B.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap, int(bm),
             _stream_handle(A.device, stream))
     _check(st, fn.__name__)
+    _keep(stream, A, B, offsets, out)
     return out
 
 
@@ -197,7 +219,7 @@ def grouped_gemm_swiglu(A, B, offsets, out=None, bm: int = 0, stream=None):
     lib = load_library()
     E, K, N, M_cap = _grouped_args(A, B, offsets, bm)
     if out is None:
-        out = torch.empty((M_cap, N // 2), dtype=torch.bfloat16, device=A.device)
+        out = _new((M_cap, N // 2), torch.bfloat16, A, stream)
     elif (out.dtype != torch.bfloat16 or tuple(out.shape) != (M_cap, N // 2)
           or not out.is_contiguous()):
         raise ValueError("out must be a contiguous bf16 [M_cap, N // 2] tensor")
@@ -205,6 +227,7 @@ def grouped_gemm_swiglu(A, B, offsets, out=None, bm: int = 0, stream=None):
                                          out.data_ptr(), E, K, N, M_cap, int(bm),
                                          _stream_handle(A.device, stream))
     _check(st, "gg_grouped_gemm_bf16_swiglu")
+    _keep(stream, A, B, offsets, out)
     return out
 
 
@@ -238,7 +261,7 @@ def grouped_gemm_gather(X, src_rows, B, offsets, dst_rows=None, out=None, bm: in
         raise ValueError("shape mismatch")
     _int32("grouped_gemm_gather", E | K | N | M_cap | n_src | int(bm))
     if out is None:
-        out = torch.empty((M_cap, N), dtype=torch.float32, device=X.device)
+        out = _new((M_cap, N), torch.float32, X, stream)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M_cap, N) or not out.is_contiguous():
         raise ValueError("out must be a contiguous fp32 [M_cap, N] tensor")
     st = lib.gg_grouped_gemm_bf16_gather(
@@ -246,6 +269,7 @@ def grouped_gemm_gather(X, src_rows, B, offsets, dst_rows=None, out=None, bm: in
         dst_rows.data_ptr() if dst_rows is not None else None, E, K, N, M_cap, int(bm),
         _stream_handle(X.device, stream))
     _check(st, "gg_grouped_gemm_bf16_gather")
+    _keep(stream, X, src_rows, B, offsets, dst_rows, out)
     return out
 
 
@@ -283,8 +307,7 @@ def grouped_gemm_gather_combine(X, src_rows, B, offsets, dst_rows, weights, out=
         raise ValueError("shape mismatch")
     _int32("grouped_gemm_gather_combine", E | K | N | M_cap | n_src | int(n_dst or 0) | int(bm))
     if out is None:
-        out = torch.zeros((n_src if n_dst is None else int(n_dst), N), dtype=torch.float32,
-                          device=X.device)
+        out = _new((n_src if n_dst is None else int(n_dst), N), torch.float32, X, stream, zero=True)
     elif out.dtype != torch.float32 or out.dim() != 2 or out.shape[1] != N or not out.is_contiguous():
         raise ValueError("out must be a contiguous fp32 [n_dst, N] tensor")
     _int32("grouped_gemm_gather_combine", out.shape[0])
@@ -293,6 +316,7 @@ def grouped_gemm_gather_combine(X, src_rows, B, offsets, dst_rows, weights, out=
         dst_rows.data_ptr(), weights.data_ptr(), out.data_ptr(), out.shape[0], E, K, N, M_cap,
         int(bm), _stream_handle(X.device, stream))
     _check(st, "gg_grouped_gemm_bf16_gather_combine")
+    _keep(stream, X, src_rows, B, offsets, dst_rows, weights, out)
     return out
 
 
@@ -319,13 +343,14 @@ def grouped_gemm_fp8w(A, Bq, b_scale, offsets, out=None, bm: int = 0, stream=Non
         raise ValueError("shape mismatch")
     _int32("grouped_gemm_fp8w", E | K | N | M_cap | int(bm))
     if out is None:
-        out = torch.empty((M_cap, N), dtype=torch.float32, device=A.device)
+        out = _new((M_cap, N), torch.float32, A, stream)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M_cap, N) or not out.is_contiguous():
         raise ValueError("out must be a contiguous fp32 [M_cap, N] tensor")
     st = lib.gg_grouped_gemm_fp8w(A.data_ptr(), Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(),
                                   out.data_ptr(), E, K, N, M_cap, int(bm),
                                   _stream_handle(A.device, stream))
     _check(st, "gg_grouped_gemm_fp8w")
+    _keep(stream, A, Bq, b_scale, offsets, out)
     return out
 
 
@@ -362,7 +387,7 @@ def grouped_gemm_fp8(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, s
         dt = torch.float32 if out_dtype is None else out_dtype
         if dt not in (torch.float32, torch.bfloat16):
             raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
-        out = torch.empty((M_cap, N), dtype=dt, device=Aq.device)
+        out = _new((M_cap, N), dt, Aq, stream)
     elif (out.dtype not in (torch.float32, torch.bfloat16) or tuple(out.shape) != (M_cap, N)
           or not out.is_contiguous() or (out_dtype is not None and out.dtype != out_dtype)):
         raise ValueError("out must be a contiguous fp32 or bf16 [M_cap, N] tensor")
@@ -371,6 +396,7 @@ def grouped_gemm_fp8(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, s
             offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap, int(bm),
             _stream_handle(Aq.device, stream))
     _check(st, fn.__name__)
+    _keep(stream, Aq, a_scale, Bq, b_scale, offsets, out)
     return out
 
 
@@ -399,7 +425,7 @@ def grouped_gemm_fp8_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
         raise ValueError("shape mismatch")
     _int32("grouped_gemm_fp8_swiglu", E | K | N | M_cap | int(bm))
     if out is None:
-        out = torch.empty((M_cap, N // 2), dtype=torch.bfloat16, device=Aq.device)
+        out = _new((M_cap, N // 2), torch.bfloat16, Aq, stream)
     elif (out.dtype != torch.bfloat16 or tuple(out.shape) != (M_cap, N // 2)
           or not out.is_contiguous()):
         raise ValueError("out must be a contiguous bf16 [M_cap, N // 2] tensor")
@@ -407,6 +433,7 @@ def grouped_gemm_fp8_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
                                         b_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(),
                                         E, K, N, M_cap, int(bm), _stream_handle(Aq.device, stream))
     _check(st, "gg_grouped_gemm_fp8_swiglu")
+    _keep(stream, Aq, a_scale, Bq, b_scale, offsets, out)
     return out
 
 
@@ -438,17 +465,11 @@ def _match(what, ok, *tensors):
 
 def _out(what, out, shape, dtypes, dtype, like, stream):
     """The given output, checked, or a new one of ``dtype`` (default: the first
-    of ``dtypes``) beside ``like``, its memory belonging to the stream that
-    writes it."""
+    of ``dtypes``) beside ``like``."""
     if dtype is not None and dtype not in dtypes:
         raise TypeError("%s: out_dtype must be %s" % (what, " or ".join(str(d) for d in dtypes)))
     if out is None:
-        dtype = dtypes[0] if dtype is None else dtype
-        if stream is None:
-            return like.new_empty(shape, dtype=dtype)
-        import torch
-        with torch.cuda.stream(stream):
-            return like.new_empty(shape, dtype=dtype)
+        return _new(shape, dtypes[0] if dtype is None else dtype, like, stream)
     if (out.dtype not in dtypes or (dtype is not None and out.dtype is not dtype)
             or out.shape != shape or not out.is_contiguous() or out.device != like.device):
         raise ValueError("%s: out must be a contiguous %s %s tensor on %s" % (
@@ -457,9 +478,7 @@ def _out(what, out, shape, dtypes, dtype, like, stream):
 
 
 def _call(name, dev, stream, tensors, *args):
-    """Calls one entry point on the tensors' device, whichever is current. On a
-    stream given by the caller the memory of all tensors is kept until that
-    stream has passed the call, so that they may be dropped at once."""
+    """Calls one entry point on the tensors' device, whichever is current."""
     import torch
     fn = getattr(load_library(), name)
     if stream is not None:
@@ -475,9 +494,7 @@ def _call(name, dev, stream, tensors, *args):
             st = fn(*args, handle)
     if st != 0:
         _check(st, name)
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+    _keep(stream, *tensors)
 
 
 def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_dtype=None):
@@ -490,9 +507,8 @@ def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_d
     grouped_gemm. Rows at or past offsets[E] are left as they were.
 
     Here and below: with ``stream``, the call is ordered on that stream alone (it
-    waits for no other), the memory of its tensors is kept until it is done, and
-    a tensor made for the result belongs to that stream. An output may not share
-    memory with another argument.
+    waits for no other), and the memory of its tensors is kept until it is done.
+    An output may not share memory with another argument.
     """
     import torch
     what = "grouped_gemm_dgrad"
@@ -701,12 +717,14 @@ def tile_schedule(offsets, N: int, M_cap: int, bm: int = 0, max_tiles: int = Non
         hmin = bm if bm else BM_CHOICES[0]
         max_tiles = (M_cap // hmin + E) * (-(-N // TILE_N))
     _int32("tile_schedule", E | N | M_cap | int(bm) | int(max_tiles))
-    tiles = torch.empty((max(max_tiles, 1), 5), dtype=torch.int32, device=offsets.device)
-    n = torch.zeros(1, dtype=torch.int32, device=offsets.device)
+    tiles = _new((max(max_tiles, 1), 5), torch.int32, offsets, stream)
+    n = _new((1,), torch.int32, offsets, stream, zero=True)
     st = lib.gg_tile_schedule(offsets.data_ptr(), E, N, M_cap, int(bm), tiles.data_ptr(), n.data_ptr(),
                               int(max_tiles), _stream_handle(offsets.device, stream))
     _check(st, "gg_tile_schedule")
-    count = int(n.item())
+    _keep(stream, offsets)
+    with torch.cuda.stream(stream):  # (None: the current one)
+        count = int(n.item())
     return tiles[:min(count, max_tiles)], count
 
 
@@ -750,12 +768,12 @@ def traced_grouped_gemm(A, B, offsets, max_tiles: int, out=None, bm: int = 0, st
     E, K, N, M_cap = _grouped_args(A, B, offsets, bm)
     _int32("traced_grouped_gemm", int(max_tiles))
     if out is None:
-        out = torch.empty((M_cap, N), dtype=torch.float32, device=A.device)
+        out = _new((M_cap, N), torch.float32, A, stream)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M_cap, N) or not out.is_contiguous():
         raise ValueError("out must be a contiguous fp32 [M_cap, N] tensor")
     shape = (TRACE_WORKGROUPS + int(max_tiles), TRACE_RECORD)
     if trace is None:
-        trace = torch.zeros(shape, dtype=torch.int64, device=A.device)
+        trace = _new(shape, torch.int64, A, stream, zero=True)
     elif (trace.dtype != torch.int64 or tuple(trace.shape) != shape or not trace.is_contiguous()
           or trace.device != A.device):
         raise ValueError("trace must be a contiguous int64 [%d, %d] tensor on A's device" % shape)
@@ -765,6 +783,7 @@ def traced_grouped_gemm(A, B, offsets, max_tiles: int, out=None, bm: int = 0, st
     if st != 0:
         raise GroupedGemmError("gg_trace_grouped_gemm_bf16: status %d (%s)"
                                % (st, lib.gg_status_string(st).decode()))
+    _keep(stream, A, B, offsets, out, trace)
     khz = ctypes.c_int32(0)
     st = lib.gg_trace_clock_khz(ctypes.byref(khz))
     if st != 0:

@@ -13,6 +13,7 @@ its interval, as rounding is monotone.
 """
 
 import numpy as np
+import pytest
 
 import oracle
 import workloads as wl
@@ -75,3 +76,18 @@ def bits_of(t):
     """The bf16 bit patterns of a device tensor."""
     import torch
     return t.detach().contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+SLEEP = 100_000_000  # cycles: tens of milliseconds
+
+
+def beside(attempt, tries=12):
+    """Runs attempt(stream) until it says that the stream and the present one ran beside
+    each other. (Streams share a few hardware queues, which the runtime deals out anew as
+    they fall idle: on one queue they run in turn, and the attempt shows nothing.)"""
+    import torch
+    for _ in range(tries):
+        torch.cuda.synchronize()
+        if attempt(torch.cuda.Stream()):
+            return
+    pytest.skip("no two streams ran beside each other")
