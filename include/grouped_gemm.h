@@ -298,9 +298,11 @@ gg_status_t gg_grouped_gemm_fp8_swiglu(const void *Aq, const float *a_scale, con
  *   dA  fp32 [M_cap][K], 16-byte aligned. Rows [0, off[E]) are overwritten;
  *       rows past them are not touched.
  * group_offsets, E, M_cap, bm, the stream, the status codes and the conditions
- * for them are those of gg_grouped_gemm_bf16 (arrays of no rows, M_cap = 0, may
- * be NULL here and below); K and N are multiples of 8, N <= GG_MAX_DGRAD_N
- * and K <= GG_MAX_N (the sum runs over N here).
+ * for them are those of gg_grouped_gemm_bf16 with K in the place of its N
+ * (arrays of no rows, M_cap = 0, may be NULL here and below); K and N are
+ * multiples of 8, N <= GG_MAX_DGRAD_N and K <= GG_MAX_N (the sum runs over N
+ * here). Malformed offsets whose groups overlap compute nothing where their
+ * row tiles outnumber M_cap / h + E (h = bm, or 16 for bm = 0).
  * Accumulation is fp32 in the matrix cores, as accurate as the product's with
  * N in the place of K.
  */

@@ -46,6 +46,7 @@ inline bool apart(Span a, Span b, S... others) {
 
 // Groups, rows and tile height; upper bounds of the row tiles and of the tiles
 // of a product with `cols` output columns (narrowest tiles: `narrow` columns).
+// The limit is the forward products', 2^28 tiles of kTileN columns.
 inline gg_status_t check_groups(const int32_t *off, int E, int cols, int M_cap, int bm, int narrow,
                                 int *row_tiles, long long *tiles) {
   if (off == nullptr || E < 1 || cols < 1 || M_cap < 0 || !valid_bm(bm)) return GG_ERR_INVALID_VALUE;
@@ -53,11 +54,12 @@ inline gg_status_t check_groups(const int32_t *off, int E, int cols, int M_cap, 
   if (!is_aligned(off, 4)) return GG_ERR_MISALIGNED;
   const long long hmin = bm ? bm : 16;
   const long long m = (long long)M_cap / hmin + E;
-  const long long b = m * ((cols + (long long)narrow - 1) / narrow);
-  // tile ids and rows + tile height must stay inside int32
-  if (b > (1LL << 28) || (long long)M_cap + 256 > INT32_MAX) return GG_ERR_UNSUPPORTED;
+  // tile ids, also of the narrowest tiles (at most kTileN / narrow times as
+  // many), and rows + tile height must stay inside int32
+  if (m * ((cols + kTileN - 1LL) / kTileN) > (1LL << 28) || (long long)M_cap + 256 > INT32_MAX)
+    return GG_ERR_UNSUPPORTED;
   *row_tiles = (int)m;
-  *tiles = b;
+  *tiles = m * ((cols + (long long)narrow - 1) / narrow);
   return GG_OK;
 }
 

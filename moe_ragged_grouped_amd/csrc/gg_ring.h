@@ -208,8 +208,8 @@ __device__ __forceinline__ RingGrid build_ring_schedule(RingSched &s,
     }
     tallest = scalar(tallest);
     total = scalar(total > tile_cap ? 0 : total);
-    const int narrow = total * cdiv(N, kNarrowestN);
-    if (!again || tallest <= 32 || 2 * narrow > G) break;
+    const int narrow = total * cdiv(N, kNarrowestN);  // (at most 2^30, by the host's bound)
+    if (!again || tallest <= 32 || narrow > G / 2) break;
     // a height's half at most doubles the tiles
     for (int n = 2 * narrow; tallest > 32 && n <= G; n *= 2) tallest /= 2;
     __syncthreads();  // wave_tiles is written again
@@ -219,7 +219,6 @@ __device__ __forceinline__ RingGrid build_ring_schedule(RingSched &s,
 #pragma unroll
   for (int w = kTileN; w >= kNarrowestN; w /= 2) {
     if (w < 128 && tallest == 16) break;  // eight waves side by side, 16 columns each
-    // the host's bounds keep total * ceil(N / 64) within 2^28
     const uint32_t rounds = ((uint32_t)(total * cdiv(N, w)) + G - 1) / (uint32_t)G;
     const unsigned long long cost = (unsigned long long)rounds * (uint32_t)(tallest + w + 96);
     if (w == kTileN || cost < best_cost) { width = w; best_cost = cost; }

@@ -160,6 +160,19 @@ def test_host_checks(lib, entry):
         assert _status(lib, entry, M_cap=0, **rows) == 0, "arrays of no rows may be null"
 
 
+@pytest.mark.parametrize("entry", [e for e in ENTRIES if "wgrad" not in e])
+def test_the_forward_products_tile_bound_holds(lib, entry):
+    # (M_cap / 16 + E) * ceil(columns / 256) up to 2^28 passes (and meets the check of the
+    # other size, which comes after it), one more 256 columns does not
+    cols, other = ("K", "N") if "dgrad" in entry else ("N", "K")
+    size = dict(E=4, M_cap=2 ** 28)
+    # the forward product draws the same line
+    fwd = lambda n: lib.gg_grouped_gemm_bf16(0, 32, 64, 128, 4, 256, n, 2 ** 28, 0, None)  # noqa: E731
+    assert fwd(15 * 256) == INVALID and fwd(15 * 256 + 8) == UNSUPPORTED
+    assert _status(lib, entry, **size, **{cols: 15 * 256, other: 100}) == MISALIGNED
+    assert _status(lib, entry, **size, **{cols: 15 * 256 + 8, other: 100}) == UNSUPPORTED
+
+
 def test_mx4_row_host_checks(lib):
     q = lambda X=16, c=32, s=48, rows=3, K=64: lib.gg_mx4_quantize(X, c, s, rows, K, None)  # noqa: E731
     assert q(X=0) == q(c=0) == q(s=0) == q(rows=-1) == q(K=0) == INVALID
