@@ -364,10 +364,13 @@ gg_status_t gg_grouped_gemm_bf16_dgrad_swiglu(const void *dY, const void *B,
  *       kernel read or write outside its arrays (they are clamped as in
  *       gg_grouped_gemm_bf16).
  *   K and N are multiples of 8, at most GG_MAX_K; E in [1, GG_MAX_EXPERTS];
- *   M_cap in [0, 2^31 - 257]; E * (ceil(K/128) * ceil(N/256) + 7) < 2^24
- *   (GG_ERR_UNSUPPORTED beyond; a launch holds 2^32 threads).
- * The sum over an expert's rows is taken in fp32 in the matrix cores, in an
- * order that the sizes fix: no atomics, so equal inputs give equal bits.
+ *   M_cap in [0, 2^31 - 257]; E * 8 * ceil(ceil(K/128) * ceil(N/256) / 8) < 2^24
+ *   (GG_ERR_UNSUPPORTED beyond; a launch counts its threads in 32 bits).
+ * The sum over an expert's rows is taken in fp32 in the matrix cores, with no
+ * atomics, in an order that E, K, N, M_cap and the expert's row count fix: equal
+ * arguments give equal bits. M_cap takes part (its mean per expert chooses
+ * between two tiles), so the same groups in a longer buffer may differ in the
+ * last places.
  */
 gg_status_t gg_grouped_gemm_bf16_wgrad(const void *A, const void *dC,
                                        const int32_t *group_offsets, float *dB,
@@ -404,7 +407,8 @@ gg_status_t gg_grouped_gemm_bf16_wgrad_bf16out(const void *A, const void *dC,
  * block of zeros gets scale byte 0. A block that holds an infinity or a NaN
  * gets scale byte 255 and codes 0, and so stands for NaN throughout.
  * X, q and scales are 16-byte aligned; rows in [0, 2^31 - 1], K <= GG_MAX_K,
- * rows * K < 2^37 (GG_ERR_UNSUPPORTED beyond; a launch holds 2^32 threads).
+ * rows * K <= 2^37 - 2^13 (GG_ERR_UNSUPPORTED beyond; a launch counts its
+ * threads in 32 bits).
  */
 gg_status_t gg_mx4_quantize(const void *X, void *q, void *scales, int64_t rows, int32_t K,
                             void *stream);
@@ -424,7 +428,7 @@ gg_status_t gg_mx4_quantize_weights(const void *B, void *q, void *scales, int32_
  * [batch][ceil(K/256)][rows][8] (batch = E and rows = N for weights, batch = 1
  * for activations). Every such value is a bf16 value except 4 and 6 times
  * 2^127 (scale byte 254), which become infinite; scale byte 255 gives NaN.
- * batch in [0, 65535]; rows in [0, 2^31 - 1]; rows * K < 2^37.
+ * batch in [0, 65535]; rows in [0, 2^31 - 1]; rows * K <= 2^37 - 2^13.
  */
 gg_status_t gg_mx4_dequantize(const void *q, const void *scales, void *Y, int32_t batch,
                               int64_t rows, int32_t K, void *stream);

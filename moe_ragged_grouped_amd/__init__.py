@@ -567,7 +567,8 @@ def grouped_gemm_wgrad(A, dC, offsets, out=None, accumulate: bool = False, strea
     bf16 [E, K, N] (out_dtype, default fp32, when out is not given; bf16 is the
     fp32 sum rounded to nearest even). An expert with no rows gets zeros. With
     accumulate the sums are added to ``out``, which must then be given and fp32.
-    The sums take no atomics: equal inputs give equal bits.
+    The sums take no atomics: equal inputs give equal bits, M_cap being one (it
+    takes part in the choice of the tile, and so in the order of summation).
     """
     import torch
     what = "grouped_gemm_wgrad"

@@ -239,6 +239,22 @@ def test_launches_of_2_to_the_32_threads_are_refused(lib):
     assert lib.gg_mx4_quantize_weights(16, 32, 48, 512, 2 ** 22, 8, None) == UNSUPPORTED
 
 
+def test_documented_ends_of_the_launch_limits(lib):
+    # the last size that passes meets the check behind the limit (null or overlapping arrays)
+    q = lambda rows, K: lib.gg_mx4_quantize(0, 32, 48, rows, K, None)  # noqa: E731
+    d = lambda rows, K: lib.gg_mx4_dequantize(0, 32, 48, 1, rows, K, None)  # noqa: E731
+    for f in (q, d):
+        assert f(2 ** 31 - 128, 64) == INVALID and f(2 ** 31 - 127, 64) == UNSUPPORTED
+        assert f(2 ** 24 - 1, 8192) == INVALID and f(2 ** 24, 8192) == UNSUPPORTED
+    w = lambda E, K, N: lib.gg_mx4_quantize_weights(16, 32, 48, E, K, N, None)  # noqa: E731
+    assert w(1023, 2 ** 21, 256) == INVALID and w(1024, 2 ** 21, 256) == UNSUPPORTED
+    for entry in ("gg_grouped_gemm_bf16_wgrad", "gg_grouped_gemm_bf16_wgrad_bf16out"):
+        g = lambda E, K, N: _status(lib, entry, E=E, K=K, N=N, dB=32)  # noqa: E731
+        # 1 x 16383 tiles go out as 16384: 1023 experts pass, 1024 do not
+        assert g(1023, 128, 16383 * 256) == INVALID and g(1024, 128, 16383 * 256) == UNSUPPORTED
+        assert g(1024, 128, 16376 * 256) == INVALID
+
+
 # ------------------------------------------------------------ the binding
 
 def _bf(*shape):
