@@ -1,0 +1,128 @@
+"""Every tile of the data gradient and the 4-bit product, with sums long enough that its
+ring of LDS stages runs over (needs an MI355X).
+
+``tests/ring_schedule.py`` says which launch runs on which tile; its tests hold that all
+are reached. Inputs are small whole numbers (or 4-bit codes at scales of 1/2 to 2), so
+that every partial sum is exact in fp32 and results are compared for equality with
+binary64 products; the plain form decodes and multiplies expert by expert.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+import oracle.operators as ref
+from tests import operators as ops
+from tests import parity
+from tests import ring_schedule as rs
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+SPARE = 3  # rows past the last group
+
+
+@pytest.fixture(scope="module")
+def gg():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import moe_ragged_grouped_amd as m
+    m.load_library()
+    return m
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _ints(gen, *shape):
+    return torch.randint(-3, 4, shape, generator=gen, device=DEV, dtype=torch.int8).bfloat16()
+
+
+def _offsets(sizes):
+    return torch.tensor(ops.offsets_of(sizes), dtype=torch.int32, device=DEV)
+
+
+def _per_expert(rows, weights, sizes):
+    """Binary64 products of each expert's rows with the transpose of its weights."""
+    parts = rows[:sum(sizes)].double().split([int(m) for m in sizes])
+    return torch.cat([a @ w.double().t().contiguous() for a, w in zip(parts, weights)])
+
+
+def _check_exact(out, want, what):
+    m = want.shape[0]
+    assert torch.equal(out[:m], want.to(out.dtype)), what
+    assert torch.isnan(out[m:]).all(), "%s: rows past the last group were written" % what
+
+
+def _nan(rows, cols, dtype):
+    return torch.full((rows, cols), float("nan"), device=DEV, dtype=dtype)
+
+
+def _dgrad(gg, sizes, K, N, bm, seed):
+    gen = _gen(seed)
+    M = sum(sizes) + SPARE
+    dC, B = _ints(gen, M, N), _ints(gen, len(sizes), K, N)
+    want = _per_expert(dC, B, sizes)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = _nan(M, K, dtype)
+        gg.grouped_gemm_dgrad(dC, B, _offsets(sizes), out=out, bm=bm)
+        _check_exact(out, want, "dgrad K=%d N=%d bm=%d %s" % (K, N, bm, dtype))
+
+
+@pytest.mark.parametrize("height,width", rs.CONFIGS)
+def test_dgrad_tiles(gg, height, width):
+    sizes, K = rs.launch_for(height, width)
+    for i, N in enumerate(rs.lengths_for(height, width, False)):
+        _dgrad(gg, sizes, K, N, height, 10 * height + width + i)
+
+
+def _codes(gen, sizes, K, N):
+    E, M, sl = len(sizes), sum(sizes) + SPARE, -(-K // 256)
+    byte = lambda *shape: torch.randint(0, 256, shape, generator=gen, device=DEV, dtype=torch.uint8)  # noqa: E731
+    scale = lambda *shape: torch.randint(126, 129, shape, generator=gen, device=DEV, dtype=torch.uint8)  # noqa: E731
+    Aq, a_s, Bq, b_s = byte(M, K // 2), scale(sl, M, 8), byte(E, N, K // 2), scale(E, sl, N, 8)
+    past = (torch.arange(sl * 8, device=DEV).view(sl, 1, 8) >= K // 32)
+    return Aq, a_s.masked_fill(past, 255), Bq, b_s.masked_fill(past, 255)  # (ignored by every reader)
+
+
+def _values(q, scale):
+    grid = torch.tensor(np.concatenate([ref.E2M1, -ref.E2M1]), device=DEV)
+    v = torch.stack([grid[(q & 15).int()], grid[(q >> 4).int()]], dim=-1).flatten(-2).unflatten(-1, (-1, 32))
+    blocks = scale.transpose(-3, -2).flatten(-2)[..., :v.shape[-2]]
+    return (v * torch.exp2(blocks.double() - 127)[..., None]).flatten(-2)
+
+
+def _mx4_want(codes, sizes):
+    Aq, a_s, Bq, b_s = codes
+    return _per_expert(_values(Aq, a_s), [_values(q, s) for q, s in zip(Bq, b_s)], sizes)
+
+
+def _mx4(gg, sizes, K, N, bm, seed):
+    codes = _codes(_gen(seed), sizes, K, N)
+    want = _mx4_want(codes, sizes)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = _nan(codes[0].shape[0], N, dtype)
+        gg.grouped_gemm_mx4(*codes, _offsets(sizes), out=out, bm=bm)
+        _check_exact(out, want, "mx4 K=%d N=%d bm=%d %s" % (K, N, bm, dtype))
+    return codes, want
+
+
+@pytest.mark.parametrize("height,width", rs.CONFIGS)
+def test_mx4_tiles(gg, height, width):
+    sizes, N = rs.launch_for(height, width)
+    for i, K in enumerate(rs.lengths_for(height, width, True)):
+        _mx4(gg, sizes, K, N, height, 10 * height + width + i)
+
+
+HEIGHTS = [300, 20, 0, 700, 64, 130]
+
+
+@pytest.mark.parametrize("copies", [1, 3, 4, 6, 12])
+def test_long_sums_at_mixed_heights(gg, copies):
+    sizes = HEIGHTS * copies
+    width, heights, _ = rs.tiles(sizes, 1032)
+    assert width == {1: 64, 3: 128, 4: 256, 6: 128, 12: 256}[copies] and len(heights) == 4
+    _dgrad(gg, sizes, 1032, 680, 0, copies)
+    _mx4(gg, sizes, 2016, 1032, 0, copies)
