@@ -78,11 +78,11 @@ def test_dgrad_tiles(gg, height, width):
         _dgrad(gg, sizes, K, N, height, 10 * height + width + i)
 
 
-def _codes(gen, sizes, K, N):
+def _codes(gen, sizes, K, N, a_lo=126):
     E, M, sl = len(sizes), sum(sizes) + SPARE, -(-K // 256)
     byte = lambda *shape: torch.randint(0, 256, shape, generator=gen, device=DEV, dtype=torch.uint8)  # noqa: E731
-    scale = lambda *shape: torch.randint(126, 129, shape, generator=gen, device=DEV, dtype=torch.uint8)  # noqa: E731
-    Aq, a_s, Bq, b_s = byte(M, K // 2), scale(sl, M, 8), byte(E, N, K // 2), scale(E, sl, N, 8)
+    scale = lambda lo, *shape: torch.randint(lo, lo + 3, shape, generator=gen, device=DEV, dtype=torch.uint8)  # noqa: E731
+    Aq, a_s, Bq, b_s = byte(M, K // 2), scale(a_lo, sl, M, 8), byte(E, N, K // 2), scale(126, E, sl, N, 8)
     past = (torch.arange(sl * 8, device=DEV).view(sl, 1, 8) >= K // 32)
     return Aq, a_s.masked_fill(past, 255), Bq, b_s.masked_fill(past, 255)  # (ignored by every reader)
 
@@ -126,3 +126,48 @@ def test_long_sums_at_mixed_heights(gg, copies):
     assert width == {1: 64, 3: 128, 4: 256, 6: 128, 12: 256}[copies] and len(heights) == 4
     _dgrad(gg, sizes, 1032, 680, 0, copies)
     _mx4(gg, sizes, 2016, 1032, 0, copies)
+
+
+SMALL = 119  # row scales for gates of a few units, where the activation bends
+
+
+def _mx4_swiglu(gg, codes, want, sizes, K, N, bm, what):
+    # the product is exact; the reference's error allowance covers the activation alone
+    M = codes[0].shape[0]
+    guard = torch.full((M * (N // 2) + 64,), -7.0, dtype=torch.bfloat16, device=DEV)
+    out = guard[:M * (N // 2)].view(M, N // 2)
+    gg.grouped_gemm_mx4_swiglu(*codes, _offsets(sizes), out=out, bm=bm)
+    got, c = ops.host(out), want.cpu().numpy()
+    parity.check_swiglu_bf16(got[:len(c)], c, np.abs(c), what, err=np.zeros_like(c))
+    assert (got[len(c):] == -7).all() and (guard[M * (N // 2):] == -7).all()
+
+
+@pytest.mark.parametrize("height,width", rs.CONFIGS)
+def test_mx4_swiglu_tiles(gg, height, width):
+    sizes, N = rs.launch_for(height, width)
+    K = rs.lengths_for(height, width, True)[-2]
+    codes = _codes(_gen(height + width), sizes, K, N, SMALL)
+    _mx4_swiglu(gg, codes, _mx4_want(codes, sizes), sizes, K, N, height, "swiglu %d x %d" % (height, width))
+
+
+@pytest.mark.parametrize("N", range(1032, 1081, 8))
+def test_mx4_swiglu_last_columns_of_wide_tiles(gg, N):
+    # 8 columns past a block of 16 (and none) at every place of a wave's 64, on tiles whose
+    # waves hold four blocks side by side and store 16 bytes a lane
+    sizes = [300, 5] * 40
+    for bm in (0, 256):
+        width, heights, _ = rs.tiles(sizes, N, bm)
+        assert width == 256 and (128 if bm == 0 else 256) in heights
+        codes = _codes(_gen(N), sizes, 288, N, SMALL)
+        want = _mx4_want(codes, sizes)
+        _mx4_swiglu(gg, codes, want, sizes, 288, N, bm, "swiglu N=%d bm=%d" % (N, bm))
+        out = _nan(codes[0].shape[0], N, torch.bfloat16)
+        gg.grouped_gemm_mx4(*codes, _offsets(sizes), out=out, bm=bm)
+        _check_exact(out, want, "bf16 N=%d bm=%d" % (N, bm))
+
+
+@pytest.mark.parametrize("copies", [1, 3, 4, 6, 12])
+def test_mx4_swiglu_at_mixed_heights(gg, copies):
+    sizes = HEIGHTS * copies
+    codes = _codes(_gen(copies), sizes, 544, 1032, SMALL)
+    _mx4_swiglu(gg, codes, _mx4_want(codes, sizes), sizes, 544, 1032, 0, "copies %d" % copies)
