@@ -171,3 +171,40 @@ def test_mx4_swiglu_at_mixed_heights(gg, copies):
     sizes = HEIGHTS * copies
     codes = _codes(_gen(copies), sizes, 544, 1032, SMALL)
     _mx4_swiglu(gg, codes, _mx4_want(codes, sizes), sizes, 544, 1032, 0, "copies %d" % copies)
+
+
+def _dgrad_swiglu(gg, sizes, K, N, bm, seed):
+    gen = _gen(seed)
+    m, M = sum(sizes), sum(sizes) + SPARE
+    dY, B, off = _ints(gen, M, N), _ints(gen, len(sizes), K, N), _offsets(sizes)
+    C = (2 * torch.randn((M, 2 * K), generator=gen, device=DEV)).bfloat16()
+    dh = _per_expert(dY, B, sizes).cpu().numpy()  # exact in the kernel too
+    c64 = C[:m].double().cpu().numpy()
+    want, want_h = ref.swiglu_grad(dh, c64)
+    err, err_h = ref.swiglu_grad_error(dh, 0.0, c64)
+    what = "dgrad_swiglu K=%d N=%d bm=%d" % (K, N, bm)
+    d, H = _nan(M, 2 * K, torch.bfloat16), _nan(M, K, torch.bfloat16)
+    gg.grouped_gemm_dgrad_swiglu(dY, B, off, C, out=d, out_h=H, bm=bm)
+    ops.check_bf16(ops.host(d[:m]), want, err, what)
+    ops.check_bf16(ops.host(H[:m]), want_h, err_h, what + " H")
+    assert torch.isnan(d[m:]).all() and torch.isnan(H[m:]).all(), what
+    # without H, and in place: the same bits
+    alone = _nan(M, 2 * K, torch.bfloat16)
+    gg.grouped_gemm_dgrad_swiglu(dY, B, off, C, out=alone, bm=bm)
+    assert torch.equal(alone[:m], d[:m]) and torch.isnan(alone[m:]).all(), what
+    spare = C[m:].clone()
+    H.fill_(float("nan"))
+    gg.grouped_gemm_dgrad_swiglu(dY, B, off, C, out=C, out_h=H, bm=bm)
+    assert torch.equal(C[:m], d[:m]) and torch.equal(C[m:], spare), what
+    ops.check_bf16(ops.host(H[:m]), want_h, err_h, what + " H in place")
+
+
+@pytest.mark.parametrize("height,width", rs.CONFIGS)
+def test_dgrad_swiglu_tiles(gg, height, width):
+    sizes, K = rs.launch_for(height, width)
+    _dgrad_swiglu(gg, sizes, K, rs.lengths_for(height, width, False)[-2], height, height + width)
+
+
+@pytest.mark.parametrize("copies", [1, 3, 4, 6, 12])
+def test_dgrad_swiglu_at_mixed_heights(gg, copies):
+    _dgrad_swiglu(gg, HEIGHTS * copies, 1032, 328, 0, copies)
