@@ -208,3 +208,45 @@ def test_dgrad_swiglu_tiles(gg, height, width):
 @pytest.mark.parametrize("copies", [1, 3, 4, 6, 12])
 def test_dgrad_swiglu_at_mixed_heights(gg, copies):
     _dgrad_swiglu(gg, HEIGHTS * copies, 1032, 328, 0, copies)
+
+
+def _many(E, seed, tall_at):
+    # small groups with empty ones among them; tall ones where tall_at says
+    sizes = np.random.default_rng(seed).integers(0, 24, size=E) * np.random.default_rng(seed + 1).integers(0, 2, size=E)
+    for e, m in tall_at.items():
+        sizes[e] = m
+    return sizes.tolist()
+
+
+# the schedule gives two experts to a thread: 128 to a wave
+MANY = {
+    # two waves and a bit, several rounds, tall experts in the last waves
+    "129": (_many(129, 1, {128: 700, 3: 300}), 1032),
+    "300": (_many(300, 2, {131: 300, 140: 700, 298: 130, 299: 517}), 1032),
+    "1024": (_many(1024, 3, {0: 130, 511: 300, 640: 700, 1022: 20, 1023: 517}), 520),
+    # one round, its only rows behind the first wave: heights cut for idle CUs
+    "sparse": ([0] * 200 + [700] + [0] * 300 + [20] + [0] * 521 + [5], 72),
+    "last": ([0] * 1023 + [1], 136),
+    "equal": ([16] * 1024, 136),
+}
+
+
+@pytest.mark.parametrize("bm", [0, 16, 128])
+@pytest.mark.parametrize("case", MANY)
+def test_more_experts_than_one_wave_holds(gg, case, bm):
+    sizes, cols = MANY[case]
+    if bm == 0:
+        width, heights, G = rs.tiles(sizes, cols)
+        rounds = sum(heights.values()) * -(-cols // width) / G
+        assert (rounds > 1 and len(heights) > 2) == (case in ("129", "300", "1024"))
+    _dgrad(gg, sizes, cols, 200, bm, 1)
+    codes, want = _mx4(gg, sizes, 544, cols, bm, 2)
+    out = _nan(codes[0].shape[0], cols // 2, torch.bfloat16)
+    gg.grouped_gemm_mx4_swiglu(*codes, _offsets(sizes), out=out, bm=bm)
+    m = sum(sizes)
+    gate, up = want[:, 0::2], want[:, 1::2]
+    # (fp32 activation of exact columns: |gate| + 4 units of 2^-22, then one rounding to bf16)
+    h = gate * torch.sigmoid(gate) * up
+    bound = (2.0 ** -8 + (gate.abs() + 4) * 2.0 ** -22) * h.abs() + 2.0 ** -100 * up.abs()
+    assert ((out[:m].double() - h).abs() <= bound).all() and torch.isnan(out[m:]).all()
+    _dgrad_swiglu(gg, sizes, cols, 136, bm, 3)
