@@ -56,7 +56,7 @@ inline gg_status_t check_groups(const int32_t *off, int E, int cols, int M_cap, 
   const long long m = (long long)M_cap / hmin + E;
   // tile ids, also of the narrowest tiles (at most kTileN / narrow times as
   // many), and rows + tile height must stay inside int32
-  if (m * ((cols + kTileN - 1LL) / kTileN) > (1LL << 28) || (long long)M_cap + 256 > INT32_MAX)
+  if (m * (((long long)cols + kTileN - 1) / kTileN) > (1LL << 28) || (long long)M_cap + 256 > INT32_MAX)
     return GG_ERR_UNSUPPORTED;
   *row_tiles = (int)m;
   *tiles = m * ((cols + (long long)narrow - 1) / narrow);
