@@ -121,7 +121,9 @@ def _check(status: int, what: str):
 
 def _int32(what, sizes):
     """Refuses what the C entry points, which count in int32, would see cut off.
-    sizes: all of them OR-ed together, which is one test for the lot."""
+    sizes: all of them OR-ed together, which is one test for the lot. (The
+    gradients and 4-bit operators call it only where sizes >> 31 is not 0: on the
+    smallest calls the host takes as long as the kernel.)"""
     if sizes >> 31 not in (0, -1):
         _check(3, what)  # GG_ERR_UNSUPPORTED
 
@@ -442,20 +444,25 @@ def grouped_gemm_fp8_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
 def _device_args(what, *tensors):
     """Checks that every (name, tensor, dtype, rank) is a contiguous device
     tensor of its dtype and rank, all on one device; returns that device."""
+    first = tensors[0][1]
+    index = first.get_device()
+    ok = first.is_cuda
+    for _, t, dtype, dims in tensors:
+        ok = (ok and t.dtype is dtype and t.dim() == dims and t.is_contiguous()
+              and t.get_device() == index)
+    if ok:
+        return first.device
     for name, t, dtype, dims in tensors:
         if t.dtype is not dtype:
             raise TypeError("%s: %s must be %s" % (what, name, dtype))
         if t.dim() != dims:
             raise ValueError("%s: %s must have %d dimensions, not %d" % (what, name, dims, t.dim()))
-    index = None
     for name, t, _, _ in tensors:
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("%s: %s must be a contiguous device tensor" % (what, name))
-        if index is None:
-            index = t.get_device()
-        elif t.get_device() != index:
+    for name, t, _, _ in tensors:
+        if t.get_device() != index:
             raise ValueError("%s: %s is on device %d, others on %d" % (what, name, t.get_device(), index))
-    return tensors[0][1].device
 
 
 def _match(what, ok, *tensors):
@@ -469,7 +476,10 @@ def _out(what, out, shape, dtypes, dtype, like, stream):
     if dtype is not None and dtype not in dtypes:
         raise TypeError("%s: out_dtype must be %s" % (what, " or ".join(str(d) for d in dtypes)))
     if out is None:
-        return _new(shape, dtypes[0] if dtype is None else dtype, like, stream)
+        dtype = dtypes[0] if dtype is None else dtype
+        if stream is None:
+            return like.new_empty(shape, dtype=dtype)
+        return _new(shape, dtype, like, stream)
     if (out.dtype not in dtypes or (dtype is not None and out.dtype is not dtype)
             or out.shape != shape or not out.is_contiguous() or out.device != like.device):
         raise ValueError("%s: out must be a contiguous %s %s tensor on %s" % (
@@ -487,14 +497,15 @@ def _call(name, dev, stream, tensors, *args):
         handle = stream.cuda_stream
     else:  # torch's current stream as a number: the Stream object costs 2 us
         handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
             st = fn(*args, handle)
     if st != 0:
         _check(st, name)
-    _keep(stream, *tensors)
+    if stream is not None:
+        _keep(stream, *tensors)
 
 
 def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_dtype=None):
@@ -517,7 +528,9 @@ def grouped_gemm_dgrad(dC, B, offsets, out=None, bm: int = 0, stream=None, out_d
     E, K, N = B.shape
     M_cap = dC.shape[0]
     _match(what, dC.shape[1] == N and offsets.shape[0] == E + 1, dC, B, offsets)
-    _int32(what, E | K | N | M_cap | int(bm))
+    sizes = E | K | N | M_cap | int(bm)
+    if sizes >> 31:
+        _int32(what, sizes)
     out = _out(what, out, (M_cap, K), (torch.float32, torch.bfloat16), out_dtype, dC, stream)
     name = "gg_grouped_gemm_bf16_dgrad" + ("" if out.dtype == torch.float32 else "_bf16out")
     _call(name, dev, stream, (dC, B, offsets, out), dC.data_ptr(), B.data_ptr(), offsets.data_ptr(),
@@ -546,7 +559,9 @@ def grouped_gemm_dgrad_swiglu(dY, B, offsets, C, out=None, out_h=None, with_h: b
     M_cap = dY.shape[0]
     _match(what, dY.shape[1] == N and offsets.shape[0] == E + 1
            and C.shape == (M_cap, 2 * K), dY, B, offsets, C)
-    _int32(what, E | K | N | M_cap | int(bm))
+    sizes = E | K | N | M_cap | int(bm)
+    if sizes >> 31:
+        _int32(what, sizes)
     out = _out(what, out, (M_cap, 2 * K), (bf,), None, dY, stream)
     h = None
     if with_h or out_h is not None:
@@ -578,7 +593,9 @@ def grouped_gemm_wgrad(A, dC, offsets, out=None, accumulate: bool = False, strea
     N = dC.shape[1]
     E = offsets.shape[0] - 1
     _match(what, dC.shape[0] == M_cap and E >= 1, A, dC, offsets)
-    _int32(what, E | K | N | M_cap)
+    sizes = E | K | N | M_cap
+    if sizes >> 31:
+        _int32(what, sizes)
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("%s: accumulate needs an fp32 out to add to" % what)
     out = _out(what, out, (E, K, N), (torch.float32, torch.bfloat16), out_dtype, A, stream)
@@ -608,7 +625,8 @@ def mx4_quantize(X, out=None, out_scale=None, stream=None):
     what = "mx4_quantize"
     dev = _device_args(what, ("X", X, torch.bfloat16, 2))
     M, K = X.shape
-    _int32(what, K)
+    if K >> 31:
+        _int32(what, K)
     u8 = (torch.uint8,)
     q = _out(what, out, (M, K // 2), u8, None, X, stream)
     s = _out(what, out_scale, (_mx4_slices(K), M, 8), u8, None, X, stream)
@@ -626,7 +644,9 @@ def mx4_quantize_weights(B, out=None, out_scale=None, stream=None):
     what = "mx4_quantize_weights"
     dev = _device_args(what, ("B", B, torch.bfloat16, 3))
     E, K, N = B.shape
-    _int32(what, E | K | N)
+    sizes = E | K | N
+    if sizes >> 31:
+        _int32(what, sizes)
     u8 = (torch.uint8,)
     q = _out(what, out, (E, N, K // 2), u8, None, B, stream)
     s = _out(what, out_scale, (E, _mx4_slices(K), N, 8), u8, None, B, stream)
@@ -648,7 +668,9 @@ def mx4_dequantize(q, scales, out=None, stream=None):
     dev = _device_args(what, ("q", q, torch.uint8, q.dim()), ("scales", scales, torch.uint8, q.dim() + 1))
     batch = q.shape[0] if q.dim() == 3 else 1
     rows, K = q.shape[-2], 2 * q.shape[-1]
-    _int32(what, batch | K)
+    sizes = batch | K
+    if sizes >> 31:
+        _int32(what, sizes)
     lead = (batch,) if q.dim() == 3 else ()
     _match(what, scales.shape == lead + (_mx4_slices(K), rows, 8), q, scales)
     y = _out(what, out, lead + (rows, K), (torch.bfloat16,), None, q, stream)
@@ -667,7 +689,9 @@ def _mx4_args(what, Aq, a_scale, Bq, b_scale, offsets, bm):
     _match(what, Aq.shape[1] == half and offsets.shape[0] == E + 1
            and a_scale.shape == (_mx4_slices(K), M_cap, 8)
            and b_scale.shape == (E, _mx4_slices(K), N, 8), Aq, a_scale, Bq, b_scale, offsets)
-    _int32(what, E | K | N | M_cap | bm)
+    sizes = E | K | N | M_cap | bm
+    if sizes >> 31:
+        _int32(what, sizes)
     return dev, E, K, N, M_cap
 
 
