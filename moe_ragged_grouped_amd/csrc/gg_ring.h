@@ -85,7 +85,9 @@ __device__ __forceinline__ void wg_barrier() {
 //
 // Height: where even the narrowest tiles leave more than half of the G
 // workgroups idle, no tile is taller than the tallest halved (to 32 at the
-// least) as often as twice as many tiles still fit. A tile's slices come one
+// least) as often as twice as many tiles still fit. (An estimate: one tall
+// expert among low ones is counted as if all tiles doubled, and may keep its
+// height although lowering it alone would fit.) A tile's slices come one
 // after the other, and the fewer bytes each has the sooner it is done.
 // Measured (us, without / with): data gradient, one expert of 618 rows, K = 1200,
 // N = 216 with SwiGLU, 11.8 / 9.4; of 1000 rows, K = 512, N = 2048, 23.7 / 16.0;
@@ -102,9 +104,11 @@ __device__ __forceinline__ void wg_barrier() {
 // Order: where a workgroup gets several tiles of different heights, experts
 // with tall tiles come first (by index among equals), so that the tiles of a
 // round cost about the same and the last round holds the small ones. Measured
-// on 16,384 rows routed by rank^-1.2 to 64 experts: data gradient K = 1344, N =
-// 1024 90.0 -> 82.7 us in bf16, 134 -> 113 with the SwiGLU gradient; launches of
-// one height keep the order of the experts, which costs 1.5 us less.
+// on 16,384 rows routed by rank^-1.2 to 64 experts, K = 1344, N = 1024, replayed
+// in a graph on one set of inputs (which stays in the caches in part): data
+// gradient 90.0 -> 82.7 us in bf16, 134 -> 113 with the SwiGLU gradient, which
+// takes 118 - 122 on inputs that change. Launches of one height keep the order
+// of the experts, which costs 1.5 us less.
 struct RingSched {
   int start[kMaxExperts];  // first row tile of an expert; INT_MAX if it has none
   int wave_tiles[kNumHeights][kThreads / kWave];

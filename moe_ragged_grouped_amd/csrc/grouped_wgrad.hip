@@ -25,7 +25,9 @@
 // overlap. A CU's vector memory path takes loads and stores in one order
 // (L1 is stalled on pending loads for 75% of the launch), and neither staggered
 // starts, nor stores spread over the next slices, nor more workgroups a CU
-// changed that; what helped is fewer and cheaper accesses: whole-line streamed
+// changed that (skewed routing is bounded by its longest group instead: 4,800 of
+// 16,384 rows are 150 slices for one workgroup, and bf16 takes 164 us where
+// uniform routing takes 139); what helped is fewer and cheaper accesses: whole-line streamed
 // stores (store_block) and rows kept in L2.
 
 #include "gg_common.h"
@@ -390,7 +392,9 @@ static gg_status_t wgrad(const void *A, const void *dC, const int32_t *off, void
   // CU, eight waves share long groups, of 3000 rows and more (W64 / W64R: one of
   // 16384, 1024 x 1024: 100 / 64; one of 8000, 2048 x 512: 50.7 / 48.5; two of
   // 3200, 2776 x 104: 28.8 / 23.9; shorter ones, eight of 1000, 256 x 512: 10.3 /
-  // 10.8; more tiles, four of 2000, 1024 x 512: 27.2 / 29.2).
+  // 10.8; more tiles, four of 2000, 1024 x 512: 27.2 / 29.2). All of groups of
+  // one size: the host knows M_cap only, so that spare rows count and the
+  // longest group of a skewed batch does not.
   if (big >= 256) return launch_wgrad<W128, O>(p, s);
   if (mid <= 64) return launch_wgrad<W32, O>(p, s);
   if (mid <= 256 && M_cap / E >= 3000) return launch_wgrad<W64R, O>(p, s);
