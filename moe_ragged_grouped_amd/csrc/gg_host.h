@@ -22,6 +22,23 @@ inline bool launch_fits(long long workgroups, int threads) {
   return workgroups <= UINT32_MAX / (uint32_t)threads;
 }
 
+// Enqueues a kernel. The status is this launch's own: the runtime's last error
+// may be an earlier call's, anyone's, and is left to whom it belongs.
+template <class T>
+struct as_declared {
+  typedef T type;
+};
+template <class... P>
+inline gg_status_t launch(void (*kernel)(P...), dim3 grid, int threads, int lds, void *stream,
+                          typename as_declared<P>::type... args) {
+  void *a[] = {(void *)&args...};
+  if (hipLaunchKernel((const void *)kernel, grid, dim3((unsigned)threads), a, (size_t)lds,
+                      static_cast<hipStream_t>(stream)) == hipSuccess)
+    return GG_OK;
+  (void)hipGetLastError();  // reported here, not by the next call of someone else
+  return GG_ERR_LAUNCH;
+}
+
 inline bool valid_bm(int bm) {
   return bm == 0 || bm == 16 || bm == 32 || bm == 64 || bm == 128 || bm == 256;
 }

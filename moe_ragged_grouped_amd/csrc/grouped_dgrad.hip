@@ -199,9 +199,7 @@ static gg_status_t dgrad(DgradParams p, void *stream) {
   if (!current_device(&dev)) return GG_ERR_LAUNCH;
   const RingLaunch li = ring_launch<dgrad_kernel<O>>(dev, kDgradLds);
   if (li.err != hipSuccess) return GG_ERR_LAUNCH;
-  hipLaunchKernelGGL((dgrad_kernel<O>), dim3((unsigned)li.workgroups(tiles)), dim3(kThreads),
-                     kDgradLds, static_cast<hipStream_t>(stream), p);
-  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+  return launch(dgrad_kernel<O>, dim3((unsigned)li.workgroups(tiles)), kThreads, kDgradLds, stream, p);
 }
 
 static DgradParams dgrad_params(const void *dC, const void *B, const int32_t *off, void *out,

@@ -387,9 +387,7 @@ static gg_status_t mx4_product(const void *Aq, const void *a_scale, const void *
   if (!current_device(&dev)) return GG_ERR_LAUNCH;
   const RingLaunch li = ring_launch<mx4_product_kernel<O>>(dev, kMx4Lds);
   if (li.err != hipSuccess) return GG_ERR_LAUNCH;
-  hipLaunchKernelGGL((mx4_product_kernel<O>), dim3((unsigned)li.workgroups(tiles)), dim3(kThreads),
-                     kMx4Lds, static_cast<hipStream_t>(stream), p);
-  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+  return launch(mx4_product_kernel<O>, dim3((unsigned)li.workgroups(tiles)), kThreads, kMx4Lds, stream, p);
 }
 
 // Full-width values, codes and scales of `rows` rows, none overlapping another.
@@ -423,10 +421,9 @@ extern "C" gg_status_t gg_mx4_quantize(const void *X, void *q, void *scales, int
   if (X == nullptr || q == nullptr || scales == nullptr) return GG_ERR_INVALID_VALUE;
   if (!is_aligned(X, 16) || !is_aligned(q, 16) || !is_aligned(scales, 16)) return GG_ERR_MISALIGNED;
   if (!rows_apart(X, q, scales, rows, K)) return GG_ERR_INVALID_VALUE;
-  hipLaunchKernelGGL(mx4_rows_kernel, dim3((unsigned)blocks), dim3(kQThreads), 0,
-                     static_cast<hipStream_t>(stream), static_cast<const u32x4 *>(X),
-                     static_cast<u32x4 *>(q), static_cast<uint8_t *>(scales), (long long)rows, K);
-  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+  return launch(mx4_rows_kernel, dim3((unsigned)blocks), kQThreads, 0, stream,
+                static_cast<const u32x4 *>(X), static_cast<u32x4 *>(q),
+                static_cast<uint8_t *>(scales), (long long)rows, K);
 }
 
 extern "C" gg_status_t gg_mx4_quantize_weights(const void *B, void *q, void *scales, int32_t E,
@@ -441,11 +438,9 @@ extern "C" gg_status_t gg_mx4_quantize_weights(const void *B, void *q, void *sca
       !launch_fits(slices * cols * E, kWqThreads))
     return GG_ERR_UNSUPPORTED;
   if (!rows_apart(B, q, scales, (long long)E * N, K)) return GG_ERR_INVALID_VALUE;
-  hipLaunchKernelGGL(mx4_weights_kernel, dim3((unsigned)(slices * cols * E)), dim3(kWqThreads), 0,
-                     static_cast<hipStream_t>(stream), static_cast<const uint16_t *>(B),
-                     static_cast<uint8_t *>(q), static_cast<uint8_t *>(scales), K, N, (int)slices,
-                     (int)cols);
-  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+  return launch(mx4_weights_kernel, dim3((unsigned)(slices * cols * E)), kWqThreads, 0, stream,
+                static_cast<const uint16_t *>(B), static_cast<uint8_t *>(q),
+                static_cast<uint8_t *>(scales), K, N, (int)slices, (int)cols);
 }
 
 extern "C" gg_status_t gg_mx4_dequantize(const void *q, const void *scales, void *Y, int32_t batch,
@@ -459,11 +454,9 @@ extern "C" gg_status_t gg_mx4_dequantize(const void *q, const void *scales, void
   if (q == nullptr || scales == nullptr || Y == nullptr) return GG_ERR_INVALID_VALUE;
   if (!is_aligned(q, 16) || !is_aligned(scales, 16) || !is_aligned(Y, 16)) return GG_ERR_MISALIGNED;
   if (!rows_apart(Y, q, scales, batch * rows, K)) return GG_ERR_INVALID_VALUE;
-  hipLaunchKernelGGL(mx4_values_kernel, dim3((unsigned)blocks, (unsigned)batch), dim3(kQThreads), 0,
-                     static_cast<hipStream_t>(stream), static_cast<const uint32_t *>(q),
-                     static_cast<const uint8_t *>(scales), static_cast<u32x4 *>(Y),
-                     (long long)rows, K, (K + kSliceK - 1) / kSliceK);
-  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+  return launch(mx4_values_kernel, dim3((unsigned)blocks, (unsigned)batch), kQThreads, 0, stream,
+                static_cast<const uint32_t *>(q), static_cast<const uint8_t *>(scales),
+                static_cast<u32x4 *>(Y), (long long)rows, K, (K + kSliceK - 1) / kSliceK);
 }
 
 extern "C" gg_status_t gg_grouped_gemm_mx4(const void *Aq, const void *a_scale, const void *Bq,

@@ -364,8 +364,7 @@ static gg_status_t launch_wgrad(WgradParams p, hipStream_t stream) {
   if (ring_launch<wgrad_kernel<C, O>>(dev, lds).err != hipSuccess) return GG_ERR_LAUNCH;
   p.tiles = (int)tiles;
   p.per_xcd = (int)per;
-  hipLaunchKernelGGL((wgrad_kernel<C, O>), dim3((unsigned)grid), dim3(C::THREADS), lds, stream, p);
-  return hipGetLastError() == hipSuccess ? GG_OK : GG_ERR_LAUNCH;
+  return launch(wgrad_kernel<C, O>, dim3((unsigned)grid), C::THREADS, lds, stream, p);
 }
 
 template <WOut O>

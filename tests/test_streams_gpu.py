@@ -102,6 +102,33 @@ def test_results_are_made_in_the_named_streams_order(gg, name):
     ops.beside(attempt)
 
 
+def test_an_earlier_error_of_the_runtime_is_not_the_calls(gg):
+    # another caller's refused call leaves its error in the runtime: these launches went through
+    X, off = _ones(M, K), _off()
+    W, C = _ones(E, K, N), torch.zeros((M, 2 * K), dtype=torch.bfloat16, device="cuda:0")
+    q, w = gg.mx4_quantize(X), gg.mx4_quantize_weights(W)
+    u8 = lambda t: torch.zeros_like(t)  # noqa: E731
+    calls = [
+        (lambda out: gg.grouped_gemm_dgrad(X, W, off, out=out), _ones(M, K, dtype=F32), float(N)),
+        (lambda out: gg.grouped_gemm_dgrad_swiglu(X, W, off, C, out=out), _ones(M, 2 * K), 0.0),
+        (lambda out: gg.grouped_gemm_wgrad(X, X, off, out=out), _ones(E, K, K, dtype=F32), M / 2.0),
+        (lambda out: gg.mx4_quantize(X, out=out, out_scale=u8_scale[0]), u8(q[0]), 0x66),
+        (lambda out: gg.mx4_quantize_weights(W, out=out, out_scale=u8_scale[1]), u8(w[0]), 0x66),
+        (lambda out: gg.mx4_dequantize(*q, out=out), _ones(M, K).mul_(3), 1.0),
+        (lambda out: gg.grouped_gemm_mx4(*q, *w, off, out=out), _ones(M, N, dtype=F32), float(K))]
+    u8_scale = (u8(q[1]), u8(w[1]))
+    lib = gg.load_library()
+    for call, out, want in calls:
+        call(out)
+        out.zero_().add_(5)
+        torch.cuda.synchronize()
+        assert lib.hipSetDevice(12345) != 0  # refused: there is no such device
+        call(out)
+        lib.hipGetLastError()
+        torch.cuda.synchronize()
+        assert (out == want).all()
+
+
 def test_tile_schedule_on_a_busy_stream(gg):
     off = _off()
     want, n = gg.tile_schedule(off, N, M)
