@@ -47,7 +47,7 @@ extern "C" {
 
 typedef enum {
   GG_OK = 0,
-  GG_ERR_INVALID_VALUE = 1, /* null pointer, non-positive size, bad bm        */
+  GG_ERR_INVALID_VALUE = 1, /* null pointer, non-positive size, bad bm, overlapping output */
   GG_ERR_MISALIGNED = 2,    /* pointer not 16-byte aligned, K or N not 8k     */
   GG_ERR_UNSUPPORTED = 3,   /* E, K or N above its limit, or index range beyond int32 */
   GG_ERR_LAUNCH = 4         /* the HIP runtime refused the launch             */

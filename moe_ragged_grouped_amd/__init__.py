@@ -502,6 +502,9 @@ def _call(name, dev, stream, tensors, *args):
     else:
         with torch.cuda.device(dev):
             st = fn(*args, handle)
+    if st == 1:  # (null pointers do not come from here)
+        raise GroupedGemmError("%s: status 1 (invalid size or tile height, or an output that shares "
+                               "memory with another array)" % name)
     if st != 0:
         _check(st, name)
     if stream is not None:

@@ -250,3 +250,44 @@ def test_more_experts_than_one_wave_holds(gg, case, bm):
     bound = (2.0 ** -8 + (gate.abs() + 4) * 2.0 ** -22) * h.abs() + 2.0 ** -100 * up.abs()
     assert ((out[:m].double() - h).abs() <= bound).all() and torch.isnan(out[m:]).all()
     _dgrad_swiglu(gg, sizes, cols, 136, bm, 3)
+
+
+def test_weights_beyond_4_gigabytes(gg):
+    # the last expert's weights, its gradient and its codes lie past 2^32 bytes
+    E, K, N, rows = 34, 8192, 8448, 37
+    sizes = [0] * (E - 2) + [5, rows]
+    gen, off, m = _gen(1), _offsets(sizes), 5 + rows
+    B = torch.randint(-3, 4, (E, K, N), generator=gen, device=DEV, dtype=torch.int8).bfloat16()
+    assert B[-1].data_ptr() - B.data_ptr() > 2 ** 32
+    dC, A = _ints(gen, m, N), _ints(gen, m, K)
+    want = torch.cat([dC[:5].double() @ B[-2].double().t().contiguous(), dC[5:].double() @ B[-1].double().t().contiguous()])
+    assert torch.equal(gg.grouped_gemm_dgrad(dC, B, off).double(), want)
+    # the quantisers: each expert as it is alone
+    q, s = gg.mx4_quantize_weights(B)
+    for e in (0, E - 1):
+        q1, s1 = gg.mx4_quantize_weights(B[e:e + 1])
+        assert torch.equal(q[e], q1[0]) and torch.equal(s[e], s1[0])
+    del B
+    back = gg.mx4_dequantize(q, s)
+    assert torch.equal(back[-1], _values(q[-1], s[-1]).bfloat16()) and torch.equal(back[1], _values(q[1], s[1]).bfloat16())
+    del back, q, s
+    dB = gg.grouped_gemm_wgrad(A, dC, off)
+    assert dB[-1].data_ptr() - dB.data_ptr() > 2 ** 32
+    for e, lo, hi in ((E - 2, 0, 5), (E - 1, 5, m)):
+        assert torch.equal(dB[e].double(), A[lo:hi].double().t().contiguous() @ dC[lo:hi].double())
+    assert not dB[:E - 2].any()
+    del dB
+    torch.cuda.empty_cache()
+    # 4-bit codes: four times as many weights
+    E, K, N = 33, 16384, 16896
+    sizes = [0] * (E - 1) + [rows]
+    Aq, a_s, _, _ = _codes(gen, sizes, K, 8)
+    Bq = torch.randint(0, 256, (E, N, K // 2), generator=gen, device=DEV, dtype=torch.uint8)
+    b_s = torch.full((E, K // 256, N, 8), 126, dtype=torch.uint8, device=DEV)
+    assert Bq[-1].data_ptr() - Bq.data_ptr() > 2 ** 32
+    a_s.fill_(127)  # products of up to 18 in steps of 1/8: sums of fewer than 2^22 steps
+    got = gg.grouped_gemm_mx4(Aq, a_s, Bq, b_s, _offsets(sizes))[:rows]
+    want = _values(Aq[:rows], a_s[:, :rows]) @ _values(Bq[-1], b_s[-1]).t().contiguous()
+    assert torch.equal(got.double(), want)
+    del Bq, b_s, want
+    torch.cuda.empty_cache()
