@@ -47,7 +47,7 @@ extern "C" {
 
 typedef enum {
   GG_OK = 0,
-  GG_ERR_INVALID_VALUE = 1, /* null pointer, non-positive size, bad bm, overlapping output */
+  GG_ERR_INVALID_VALUE = 1, /* null pointer, non-positive size, bad bm, output over an array */
   GG_ERR_MISALIGNED = 2,    /* pointer not 16-byte aligned, K or N not 8k     */
   GG_ERR_UNSUPPORTED = 3,   /* E, K or N above its limit, or index range beyond int32 */
   GG_ERR_LAUNCH = 4         /* the HIP runtime refused the launch             */
@@ -128,8 +128,8 @@ gg_status_t gg_grouped_gemm_bf16_bf16out(const void *A, const void *B,
  *       x * rcp(1 + 2^(-x log2 e)) with the hardware exp2 and reciprocal,
  *       within (|gate| + 3.5) * 2^-23 of the exact value relative to first
  *       order (-0 for gate below about -87.3, where the reciprocal would be
- *       subnormal: less than 1.1e-36 * |up| is lost), and rounded once to the nearest bf16 (ties to even). Rows at or past
- *       off[E] are not written.
+ *       subnormal: less than 1.1e-36 * |up| is lost), and rounded once to the
+ *       nearest bf16 (ties to even). Rows at or past off[E] are not written.
  * A, group_offsets, E, K, N, M_cap, bm, the stream, the status codes and
  * the conditions for them are those of gg_grouped_gemm_bf16 (N a multiple
  * of 8, so I is a multiple of 4).
@@ -335,13 +335,14 @@ gg_status_t gg_grouped_gemm_bf16_dgrad_bf16out(const void *dC, const void *B,
  *       gg_grouped_gemm_bf16_bf16out gives them;
  *   dC  bf16 [M_cap][2K], and H bf16 [M_cap][K] or NULL: the operand of the down
  *       projection's weight gradient, which a forward pass that kept only C has
- *       not stored. dC may be C itself, from its start. Rows at or beyond off[E] of C are not
- *       read, of dC and H not written. All are 16-byte aligned.
+ *       not stored. dC may be C itself, from its start. Rows at or beyond off[E]
+ *       of C are not read, of dC and H not written. All are 16-byte aligned.
  * Everything is evaluated in fp32 (hardware exp2 and reciprocal, each within one
  * ulp) and rounded once to bf16 on its way out. s is 0 where it would be subnormal
  * (gate below about -87.3); dC and H then are 0, off by less than 1.1e-36 *
- * |dH * up|, 1.1e-36 * |dH| and 1.1e-36 * |up|. An infinite gate gives NaN. Sizes, offsets, bm, the
- * stream and the status codes are those of gg_grouped_gemm_bf16_dgrad.
+ * |dH * up|, 1.1e-36 * |dH| and 1.1e-36 * |up|. An infinite gate gives NaN.
+ * Sizes, offsets, bm, the stream and the status codes are those of
+ * gg_grouped_gemm_bf16_dgrad.
  */
 gg_status_t gg_grouped_gemm_bf16_dgrad_swiglu(const void *dY, const void *B,
                                               const int32_t *group_offsets, const void *C, void *dC,

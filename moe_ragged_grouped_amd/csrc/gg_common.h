@@ -122,8 +122,8 @@ __device__ __forceinline__ void st_g8_bf16(uint16_t *p, f32x4 v) {
 // one ulp). Rounding -x log2 e moves the exponent by up to |x| log2(e) 2^-23,
 // so the result is within about (|x| + 3.5) 2^-23 of silu(x) * u relative; for x
 // below about -87.3 the reciprocal would be subnormal and is 0, giving -0
-// where the exact value is below 1.1e-36. Each result is rounded once to bf16 (ties to even)
-// and the pair stored as one 4-byte global store.
+// where the exact value is below 1.1e-36. Each result is rounded once to bf16
+// (ties to even) and the pair stored as one 4-byte global store.
 typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((address_space(1))) bf16x2 gbl_bf16x2;
 __device__ __forceinline__ float silu(float x) {
