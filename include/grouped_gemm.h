@@ -30,9 +30,9 @@
  *    overlap; if the tiles of all groups then outnumber what M_cap rows can
  *    produce with nondecreasing offsets, ((M_cap / h) + E) * ceil(N / 256)
  *    for the smallest height h in use, the call computes nothing at all.
- *  - An output may not share memory with another array of the call (the
- *    gradients and the 4-bit entry points return GG_ERR_INVALID_VALUE; the one
- *    exception is named there).
+ *  - An output may not share memory with another array of the call (all
+ *    but the forward products return GG_ERR_INVALID_VALUE; the two exceptions are
+ *    named there).
  *  - Calls on different streams may run concurrently; the library holds no
  *    mutable state besides a per-device cache of launch limits.
  */
@@ -473,6 +473,187 @@ gg_status_t gg_grouped_gemm_mx4_swiglu(const void *Aq, const void *a_scale, cons
                                        const void *b_scale, const int32_t *group_offsets, void *H,
                                        int32_t E, int32_t K, int32_t N, int32_t M_cap, int32_t bm,
                                        void *stream);
+
+/*
+ * 8-bit operands with a scale for each block of 128 ("fp8_block"). A value is an
+ * OCP E4M3 code (1 sign, 4 exponent and 3 mantissa bits, 448 at most) times its
+ * block's fp32 scale.
+ *   rows     codes uint8 [rows][K], scales fp32 [ceil(K/128)][rows]: one scale for
+ *            128 values along K, those of a slice of 128 k side by side.
+ *   weights  codes uint8 [E][N][K] (output columns as rows), scales fp32
+ *            [E][ceil(N/128)][ceil(K/128)]: one scale for 128 x 128 values.
+ *
+ * gg_fp8_quantize -- X bf16 [rows][K] to codes and scales. With top the largest
+ * magnitude of a block, counted as 2^-100 at least, and m = 448 / top cut to 16
+ * significant bits, a value's code is the one nearest to x * m (which is exact in
+ * fp32), ties to even, and the block's scale is 1 / m. A block that holds an
+ * infinity or a NaN gets scale NaN and codes 0, and so stands for NaN throughout.
+ * K is a multiple of 16, at most GG_MAX_K; rows in [0, 2^31 - 1]; ceil(rows/32) *
+ * ceil(K/512) < 2^24 (GG_ERR_UNSUPPORTED beyond; a launch counts its threads in 32
+ * bits). X, q and scales are 16-byte aligned.
+ */
+gg_status_t gg_fp8_quantize(const void *X, void *q, float *scales, int64_t rows, int32_t K,
+                            void *stream);
+
+/*
+ * gg_fp8_quantize_weights -- B bf16 [E][K][N] (the layout of the bf16 product) to
+ * codes and scales by the rule of gg_fp8_quantize, a block being 128 x 128 values.
+ *   for_grad == 0: codes [E][N][K], scales [E][ceil(N/128)][ceil(K/128)], what
+ *     gg_grouped_gemm_fp8_block takes; K a multiple of 16, N of 8.
+ *   for_grad != 0: codes [E][K][N], scales [E][ceil(K/128)][ceil(N/128)], the same
+ *     values with K and N exchanged: what the same entry point takes for the data
+ *     gradient dA = dC B^T (its K is then this N); N a multiple of 16, K of 8.
+ * The summed dimension is at most GG_MAX_K, the other at most GG_MAX_N, and
+ * E * ceil(K/128) * ceil(N/128) < 2^24.
+ */
+gg_status_t gg_fp8_quantize_weights(const void *B, void *q, float *scales, int32_t for_grad,
+                                    int32_t E, int32_t K, int32_t N, void *stream);
+
+/*
+ * gg_grouped_gemm_fp8_block -- the grouped product of 8-bit rows and weights with
+ * a scale for each block of 128:
+ *
+ *   C[r][n] = sum_b a_scale[b][r] * b_scale[e][n / 128][b] *
+ *             sum_{k in block b} dec(Aq[r][k]) * dec(Bq[e][n][k])
+ *
+ *   Aq, a_scale  codes uint8 [M_cap][K] and scales fp32 [ceil(K/128)][M_cap].
+ *                Rows at or beyond off[E] are never used.
+ *   Bq, b_scale  codes uint8 [E][N][K] and scales fp32 [E][ceil(N/128)][ceil(K/128)].
+ *                The scales are any fp32 numbers, not only what the quantiser makes.
+ *   C            fp32 [M_cap][N]. Rows at or beyond off[E] are not touched.
+ * K is a multiple of 16 and at most GG_MAX_K, N a multiple of 8 and at most
+ * GG_MAX_N; all pointers but group_offsets (4) are 16-byte aligned. Offsets, E,
+ * M_cap, bm, the stream and the status codes are those of gg_grouped_gemm_bf16.
+ * A block's products are summed on the fp8 matrix cores, which align 8 neighbouring
+ * products to the largest of them and drop what is 2^-14 of it or smaller; blocks
+ * are scaled and added in fp32. A NaN scale makes the row's or the columns'
+ * results NaN.
+ */
+gg_status_t gg_grouped_gemm_fp8_block(const void *Aq, const float *a_scale, const void *Bq,
+                                      const float *b_scale, const int32_t *group_offsets, float *C,
+                                      int32_t E, int32_t K, int32_t N, int32_t M_cap, int32_t bm,
+                                      void *stream);
+
+/*
+ * gg_grouped_gemm_fp8_block_bf16out -- the same with C bf16 [M_cap][N], each
+ * element the fp32 result rounded once to the nearest bf16 (ties to even).
+ */
+gg_status_t gg_grouped_gemm_fp8_block_bf16out(const void *Aq, const float *a_scale, const void *Bq,
+                                              const float *b_scale, const int32_t *group_offsets,
+                                              void *C, int32_t E, int32_t K, int32_t N,
+                                              int32_t M_cap, int32_t bm, void *stream);
+
+/*
+ * gg_grouped_gemm_fp8_block_swiglu -- gg_grouped_gemm_fp8_block for the gate and
+ * up projections, N = 2 I interleaved columns, with the SwiGLU of
+ * gg_grouped_gemm_bf16_swiglu in the epilogue: H bf16 [M_cap][N/2].
+ */
+gg_status_t gg_grouped_gemm_fp8_block_swiglu(const void *Aq, const float *a_scale, const void *Bq,
+                                             const float *b_scale, const int32_t *group_offsets,
+                                             void *H, int32_t E, int32_t K, int32_t N,
+                                             int32_t M_cap, int32_t bm, void *stream);
+
+/*
+ * gg_expert_sort -- the choices of a router, T tokens of k experts each, grouped by
+ * expert: the row lists that the grouped products take.
+ *
+ *   experts  int32 [T][k], or int64 where `wide` is not 0: the chosen experts. A
+ *            choice outside [0, E) is of no expert here (of another rank, or none)
+ *            and gets no row.
+ *   weights  fp32 [T][k], or NULL (then row_weights is NULL too).
+ *   offsets  int32 [E+1]: expert e has rows offsets[e] .. offsets[e+1]-1, in the
+ *            order of its choices (by token, then by place).
+ *   rows     int32 [T*k]: each row's token. -1 past offsets[E].
+ *   pos      int32 [T][k]: each choice's row, -1 where it has none.
+ *   row_weights  fp32 [T*k]: each row's weight. 0 past offsets[E].
+ *   workspace  gg_expert_sort_workspace(T * k, E) bytes of device memory, 16-byte
+ *            aligned (0 bytes: may be NULL). Its contents are used during the call only.
+ * T * k <= 2^31 - 1; k >= 1; E in [1, GG_MAX_EXPERTS]. Pointers are aligned to their
+ * elements. (src_rows and, for a combine, dst_rows of gg_grouped_gemm_bf16_gather
+ * and _gather_combine are both `rows`, row_weights theirs.)
+ */
+int64_t gg_expert_sort_workspace(int64_t choices, int32_t E);
+gg_status_t gg_expert_sort(const void *experts, int32_t wide, const float *weights, int32_t *offsets,
+                           int32_t *rows, int32_t *pos, float *row_weights, void *workspace, int64_t T,
+                           int32_t k, int32_t E, void *stream);
+
+/*
+ * gg_expert_spread -- each token's row to the rows of its choices:
+ * out[pos[t][j]] = X[t] for every pos[t][j] in [0, M_cap); other choices are
+ * skipped, and rows that no choice names are not touched. Two choices that name the
+ * same row race.
+ *   X, out   [T] and [M_cap] rows of row_bytes bytes, a multiple of 16; 16-byte
+ *            aligned. Any type: bytes are moved.
+ *   scales, out_scales  block scales that go with the rows, [slices][T] and
+ *            [slices][M_cap] elements of scale_bytes: 4 (fp8_block), 8 (mx4), or 0
+ *            with slices 0 and both pointers unused. 16-byte aligned.
+ * Its gradient is gg_expert_combine without weights.
+ */
+gg_status_t gg_expert_spread(const void *X, const int32_t *pos, void *out, const void *scales,
+                             void *out_scales, int32_t scale_bytes, int64_t T, int32_t k,
+                             int64_t row_bytes, int32_t slices, int64_t M_cap, void *stream);
+
+/*
+ * gg_expert_combine -- each token's rows, weighted and summed:
+ *   out[t][n] = sum_j weights[t][j] * Y[pos[t][j]][n]   over the j with pos in [0, M_cap)
+ *   Y        [M_cap][N], fp32 where y_fp32 is not 0, else bf16; out [T][N], fp32 where
+ *            out_fp32 is not 0, else bf16; both 16-byte aligned. N a multiple of 8.
+ *   weights  fp32 [T][k], or NULL for weights of 1.
+ * A token with no rows gets zeros. The sum is taken in fp32 in the order of j, one
+ * fused multiply-add a term (no atomics: equal inputs give equal bits), and rounded
+ * once. N <= GG_MAX_N; T * ceil(N/512) < 2^26.
+ */
+gg_status_t gg_expert_combine(const void *Y, int32_t y_fp32, const int32_t *pos, const float *weights,
+                              void *out, int32_t out_fp32, int64_t T, int32_t k, int32_t N,
+                              int64_t M_cap, void *stream);
+
+/*
+ * gg_expert_combine_grad -- the gradient of gg_expert_combine: given dO [T][N],
+ *   dY[pos[t][j]][n] = weights[t][j] * dO[t][n]
+ *   dweights[t][j]   = sum_n dO[t][n] * Y[pos[t][j]][n]     (0 where pos is not in [0, M_cap))
+ * dO, Y and dY are all fp32 (fp32 != 0) or all bf16. Rows of dY that no choice names
+ * are not touched; two choices that name the same row race. Products and sums are
+ * in fp32, dY is rounded once, dweights is fp32 [T][k] summed in a fixed order.
+ */
+gg_status_t gg_expert_combine_grad(const void *dO, const void *Y, int32_t fp32, const int32_t *pos,
+                                   const float *weights, void *dY, float *dweights, int64_t T,
+                                   int32_t k, int32_t N, int64_t M_cap, void *stream);
+
+/*
+ * gg_rms_norm_fp8 -- root-mean-square norm of X + residual, in 8 bits:
+ *   z = bf16(X + residual)  (X where residual is NULL),
+ *   y = z / sqrt(mean z^2 + eps) * weight,
+ *   q, scales = y by the rule of gg_fp8_quantize, from its fp32 values.
+ *   X, residual  bf16 [T][K], residual or NULL; weight bf16 [K].
+ *   q, scales    uint8 [T][K], fp32 [ceil(K/128)][T].
+ *   sum          bf16 [T][K]: z, the next residual; or NULL. Needs a residual. May be
+ *                X or residual itself, from its start.
+ *   norm         bf16 [T][K]: y rounded once; or NULL.
+ * K is a multiple of 16, at most 16384; T in [0, 2^24 - 2]; eps >= 0; everything
+ * 16-byte aligned.
+ */
+gg_status_t gg_rms_norm_fp8(const void *X, const void *residual, const void *weight, void *q,
+                            float *scales, void *sum, void *norm, int64_t T, int32_t K, float eps,
+                            void *stream);
+
+/*
+ * gg_rms_norm_grad -- the gradient of y = z / sqrt(mean z^2 + eps) * weight (for
+ * y in 8 bits, that of the values before they were rounded): with r = 1 /
+ * sqrt(mean z^2 + eps) and u = weight * dY,
+ *   dZ = r * (u - z * r^2 * mean(u * z)) + d_residual,
+ *   dweight[c] = sum_t dY[t][c] * z[t][c] * r[t].
+ *   dY, Z, d_residual, dZ  bf16 [T][K]; d_residual, the gradient that reaches z
+ *            past the norm, or NULL. dZ is rounded once.
+ *   weight   bf16 [K];  dweight fp32 [K], overwritten, summed in an order that T and
+ *            K fix (no atomics).
+ *   workspace  gg_rms_norm_grad_workspace(T, K) bytes of device memory, used during
+ *            the call only.
+ * Sizes and alignment are those of gg_rms_norm_fp8.
+ */
+int64_t gg_rms_norm_grad_workspace(int64_t T, int32_t K);
+gg_status_t gg_rms_norm_grad(const void *dY, const void *Z, const void *weight, const void *d_residual,
+                             void *dZ, float *dweight, void *workspace, int64_t T, int32_t K, float eps,
+                             void *stream);
 
 /*
  * gg_tile_schedule -- the flat tile list the product kernel consumes,

@@ -18,7 +18,9 @@ __all__ = ["grouped_gemm", "grouped_gemm_swiglu", "grouped_gemm_gather",
            "grouped_gemm_gather_combine", "grouped_gemm_fp8w", "grouped_gemm_fp8",
            "grouped_gemm_fp8_swiglu", "grouped_gemm_dgrad", "grouped_gemm_dgrad_swiglu",
            "grouped_gemm_wgrad", "mx4_quantize", "mx4_quantize_weights", "mx4_dequantize",
-           "grouped_gemm_mx4", "grouped_gemm_mx4_swiglu", "tile_schedule", "library_path", "load_library",
+           "grouped_gemm_mx4", "grouped_gemm_mx4_swiglu", "fp8_quantize", "fp8_quantize_weights",
+           "grouped_gemm_fp8_block", "grouped_gemm_fp8_block_swiglu", "expert_sort", "expert_spread",
+           "expert_combine", "expert_combine_grad", "rms_norm_fp8", "rms_norm_grad", "tile_schedule", "library_path", "load_library",
            "traced_grouped_gemm", "trace_library_path", "load_trace_library",
            "GroupedGemmError", "BM_CHOICES", "TILE_N", "MAX_EXPERTS", "SYMBOLS",
            "TRACE_SYMBOLS", "TRACE_WORKGROUPS", "TRACE_RECORD"]
@@ -37,7 +39,11 @@ SYMBOLS = ("gg_grouped_gemm_bf16", "gg_grouped_gemm_bf16_bf16out", "gg_grouped_g
            "gg_grouped_gemm_bf16_dgrad_bf16out", "gg_grouped_gemm_bf16_dgrad_swiglu",
            "gg_grouped_gemm_bf16_wgrad", "gg_grouped_gemm_bf16_wgrad_bf16out", "gg_mx4_quantize",
            "gg_mx4_quantize_weights", "gg_mx4_dequantize", "gg_grouped_gemm_mx4",
-           "gg_grouped_gemm_mx4_bf16out", "gg_grouped_gemm_mx4_swiglu", "gg_tile_schedule",
+           "gg_grouped_gemm_mx4_bf16out", "gg_grouped_gemm_mx4_swiglu", "gg_fp8_quantize",
+           "gg_fp8_quantize_weights", "gg_grouped_gemm_fp8_block", "gg_grouped_gemm_fp8_block_bf16out",
+           "gg_grouped_gemm_fp8_block_swiglu", "gg_expert_sort", "gg_expert_sort_workspace",
+           "gg_expert_spread", "gg_expert_combine", "gg_expert_combine_grad", "gg_rms_norm_fp8",
+           "gg_rms_norm_grad", "gg_rms_norm_grad_workspace", "gg_tile_schedule",
            "gg_status_string")
 
 # the tracing build (include/grouped_gemm_trace.h): a diagnostic library
@@ -101,10 +107,24 @@ def load_library():
                 ("gg_mx4_dequantize", [vp] * 3 + [i32, i64, i32]),
                 ("gg_grouped_gemm_mx4", [vp] * 6 + [i32] * 5),
                 ("gg_grouped_gemm_mx4_bf16out", [vp] * 6 + [i32] * 5),
-                ("gg_grouped_gemm_mx4_swiglu", [vp] * 6 + [i32] * 5)):
+                ("gg_grouped_gemm_mx4_swiglu", [vp] * 6 + [i32] * 5),
+                ("gg_fp8_quantize", [vp] * 3 + [i64, i32]),
+                ("gg_fp8_quantize_weights", [vp] * 3 + [i32] * 4),
+                ("gg_grouped_gemm_fp8_block", [vp] * 6 + [i32] * 5),
+                ("gg_grouped_gemm_fp8_block_bf16out", [vp] * 6 + [i32] * 5),
+                ("gg_grouped_gemm_fp8_block_swiglu", [vp] * 6 + [i32] * 5),
+                ("gg_expert_sort", [vp, i32] + [vp] * 6 + [i64, i32, i32]),
+                ("gg_expert_spread", [vp] * 5 + [i32, i64, i32, i64, i32, i64]),
+                ("gg_expert_combine", [vp, i32, vp, vp, vp, i32, i64, i32, i32, i64]),
+                ("gg_expert_combine_grad", [vp, vp, i32] + [vp] * 4 + [i64, i32, i32, i64]),
+                ("gg_rms_norm_fp8", [vp] * 7 + [i64, i32, ctypes.c_float]),
+                ("gg_rms_norm_grad", [vp] * 7 + [i64, i32, ctypes.c_float])):
             fn = getattr(lib, name)
             fn.argtypes = args + [vp]
             fn.restype = ctypes.c_int
+        for name in ("gg_expert_sort_workspace", "gg_rms_norm_grad_workspace"):
+            getattr(lib, name).argtypes = [i64, i32]
+            getattr(lib, name).restype = i64
         lib.gg_tile_schedule.argtypes = [vp, i32, i32, i32, i32, vp, vp, i32, vp]
         lib.gg_tile_schedule.restype = ctypes.c_int
         lib.gg_status_string.argtypes = [ctypes.c_int]
@@ -732,6 +752,328 @@ def grouped_gemm_mx4_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
           Aq.data_ptr(), a_scale.data_ptr(), Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(),
           out.data_ptr(), E, K, N, M_cap, int(bm))
     return out
+
+
+# ---- around the experts' products: 8-bit blocks, rows to the experts and back, the norm
+
+_BLOCK = 128
+
+
+def _fp8(t):
+    """E4M3 codes, as uint8 or as torch's float8_e4m3fn (either is taken)."""
+    import torch
+    return torch.float8_e4m3fn if t.dtype is torch.float8_e4m3fn else torch.uint8
+
+
+def fp8_quantize(X, out=None, out_scale=None, stream=None):
+    """bf16 rows [M, K] -> 8 bits (codes float8_e4m3fn [M, K], scales fp32 [ceil(K/128), M]).
+
+    Blocks of 128 values along K share a scale. With top a block's largest
+    magnitude (2^-100 at least) and m = 448 / top cut to 16 significant bits, a
+    value goes to the code nearest to x * m, ties to even, and the scale is
+    1 / m. A block with an infinity or a NaN stands for NaN. K is a multiple of 16.
+    """
+    import torch
+    what = "fp8_quantize"
+    dev = _device_args(what, ("X", X, torch.bfloat16, 2))
+    M, K = X.shape
+    if K >> 31:
+        _int32(what, K)
+    q = _out(what, out, (M, K), (torch.float8_e4m3fn, torch.uint8), None, X, stream)
+    s = _out(what, out_scale, (-(-K // _BLOCK), M), (torch.float32,), None, X, stream)
+    _call("gg_fp8_quantize", dev, stream, (X, q, s), X.data_ptr(), q.data_ptr(), s.data_ptr(), M, K)
+    return q, s
+
+
+def fp8_quantize_weights(B, for_grad: bool = False, out=None, out_scale=None, stream=None):
+    """bf16 weights [E, K, N] -> (codes float8_e4m3fn [E, N, K], scales fp32 [E, ceil(N/128), ceil(K/128)]).
+
+    The rule of fp8_quantize with blocks of 128 x 128: what grouped_gemm_fp8_block
+    takes as weights, made once. With for_grad the same values as codes [E, K, N]
+    and scales [E, ceil(K/128), ceil(N/128)]: the weights of the data gradient,
+    dA = grouped_gemm_fp8_block(*fp8_quantize(dC), *those, offsets). K is a multiple
+    of 16 and N of 8 (for_grad: N of 16 and K of 8).
+    """
+    import torch
+    what = "fp8_quantize_weights"
+    dev = _device_args(what, ("B", B, torch.bfloat16, 3))
+    E, K, N = B.shape
+    sizes = E | K | N
+    if sizes >> 31:
+        _int32(what, sizes)
+    rows, cols = (K, N) if for_grad else (N, K)
+    q = _out(what, out, (E, rows, cols), (torch.float8_e4m3fn, torch.uint8), None, B, stream)
+    s = _out(what, out_scale, (E, -(-rows // _BLOCK), -(-cols // _BLOCK)), (torch.float32,), None, B, stream)
+    _call("gg_fp8_quantize_weights", dev, stream, (B, q, s), B.data_ptr(), q.data_ptr(), s.data_ptr(),
+          int(bool(for_grad)), E, K, N)
+    return q, s
+
+
+def _fp8_block_args(what, Aq, a_scale, Bq, b_scale, offsets, bm):
+    import torch
+    f32 = torch.float32
+    dev = _device_args(what, ("Aq", Aq, _fp8(Aq), 2), ("a_scale", a_scale, f32, 2),
+                       ("Bq", Bq, _fp8(Bq), 3), ("b_scale", b_scale, f32, 3),
+                       ("offsets", offsets, torch.int32, 1))
+    E, N, K = Bq.shape
+    M_cap = Aq.shape[0]
+    slices = -(-K // _BLOCK)
+    _match(what, Aq.shape[1] == K and offsets.shape[0] == E + 1 and a_scale.shape == (slices, M_cap)
+           and b_scale.shape == (E, -(-N // _BLOCK), slices), Aq, a_scale, Bq, b_scale, offsets)
+    sizes = E | K | N | M_cap | bm
+    if sizes >> 31:
+        _int32(what, sizes)
+    return dev, E, K, N, M_cap
+
+
+def grouped_gemm_fp8_block(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, stream=None,
+                           out_dtype=None):
+    """C = val(Aq, a_scale) @ val(Bq[e], b_scale[e]).T per expert, fp8 matrix cores, one launch.
+
+    Aq, a_scale: E4M3 codes [M_cap, K] (float8_e4m3fn or uint8) and fp32 scales
+    [ceil(K/128), M_cap], one for 128 values of a row (fp8_quantize); Bq, b_scale:
+    codes [E, N, K] and scales [E, ceil(N/128), ceil(K/128)], one for 128 x 128
+    values (fp8_quantize_weights; any fp32 numbers). offsets int32 [E+1]; out:
+    optional fp32 or bf16 [M_cap, N] (out_dtype when out is not given, default
+    fp32; bf16 is the fp32 result rounded to nearest even). K is a multiple of 16,
+    N of 8. Rows at or past offsets[E] are left as they were. bm and stream as in
+    grouped_gemm. Blocks are scaled and added in fp32; inside a block of 128 the
+    matrix cores drop what is 2^-14 of the largest of 8 neighbouring products.
+    """
+    import torch
+    what = "grouped_gemm_fp8_block"
+    dev, E, K, N, M_cap = _fp8_block_args(what, Aq, a_scale, Bq, b_scale, offsets, int(bm))
+    out = _out(what, out, (M_cap, N), (torch.float32, torch.bfloat16), out_dtype, Aq, stream)
+    name = "gg_grouped_gemm_fp8_block" + ("" if out.dtype == torch.float32 else "_bf16out")
+    _call(name, dev, stream, (Aq, a_scale, Bq, b_scale, offsets, out), Aq.data_ptr(), a_scale.data_ptr(),
+          Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), E, K, N, M_cap, int(bm))
+    return out
+
+
+def grouped_gemm_fp8_block_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int = 0, stream=None):
+    """H[r, j] = silu(C[r, 2j]) * C[r, 2j+1] for C = grouped_gemm_fp8_block (interleaved columns).
+
+    Arguments of grouped_gemm_fp8_block; out: optional bf16 [M_cap, N // 2]. The
+    activation runs in fp32 in the epilogue and is rounded once to bf16.
+    """
+    import torch
+    what = "grouped_gemm_fp8_block_swiglu"
+    dev, E, K, N, M_cap = _fp8_block_args(what, Aq, a_scale, Bq, b_scale, offsets, int(bm))
+    out = _out(what, out, (M_cap, N // 2), (torch.bfloat16,), None, Aq, stream)
+    _call("gg_grouped_gemm_fp8_block_swiglu", dev, stream, (Aq, a_scale, Bq, b_scale, offsets, out),
+          Aq.data_ptr(), a_scale.data_ptr(), Bq.data_ptr(), b_scale.data_ptr(), offsets.data_ptr(),
+          out.data_ptr(), E, K, N, M_cap, int(bm))
+    return out
+
+
+def expert_sort(experts, E: int, weights=None, out=None, stream=None):
+    """A router's choices grouped by expert: (offsets, rows, pos) or, with weights, (..., row_weights).
+
+    experts: int32 or int64 [T, k], the k experts of each token; a choice outside
+    [0, E) (another rank's, or none) gets no row. weights: optional fp32 [T, k].
+    offsets: int32 [E+1], expert e's rows are offsets[e]..offsets[e+1]-1, in the
+    order of their choices; rows: int32 [T*k], each row's token; pos: int32 [T, k],
+    each choice's row; row_weights: fp32 [T*k], each row's weight. Past offsets[E]
+    rows holds -1 and row_weights 0; pos is -1 where a choice has no row. offsets
+    is what the products take; rows is src_rows (and dst_rows) of
+    grouped_gemm_gather and grouped_gemm_gather_combine, row_weights the weights of
+    the latter; pos is what expert_spread and expert_combine take. out: optional
+    tuple of the tensors that are returned. The order is the same on every call.
+    """
+    import torch
+    what = "expert_sort"
+    wide = experts.dtype is torch.int64
+    args = [("experts", experts, torch.int64 if wide else torch.int32, 2)]
+    if weights is not None:
+        args.append(("weights", weights, torch.float32, 2))
+    dev = _device_args(what, *args)
+    T, k = experts.shape
+    E = int(E)
+    _match(what, weights is None or weights.shape == (T, k), experts, *([] if weights is None else [weights]))
+    sizes = E | k | T * k
+    if sizes >> 31:
+        _int32(what, sizes)
+    i32 = (torch.int32,)
+    shapes = [((max(E, 0) + 1,), i32), ((T * k,), i32), ((T, k), i32)]
+    if weights is not None:
+        shapes.append(((T * k,), (torch.float32,)))
+    if out is None:
+        out = (None,) * len(shapes)
+    if len(out) != len(shapes):
+        raise ValueError("%s: out must hold %d tensors" % (what, len(shapes)))
+    out = tuple(_out(what, o, shape, dtypes, None, experts, stream) for o, (shape, dtypes) in zip(out, shapes))
+    need = load_library().gg_expert_sort_workspace(T * k, E)
+    space = _out(what, None, (need,), (torch.uint8,), None, experts, stream) if need else None
+    _call("gg_expert_sort", dev, stream, (experts, weights, *out, space), experts.data_ptr(), int(wide),
+          None if weights is None else weights.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
+          out[2].data_ptr(), None if weights is None else out[3].data_ptr(),
+          None if space is None else space.data_ptr(), T, k, E)
+    return out
+
+
+def expert_spread(X, pos, scale=None, M_cap=None, out=None, out_scale=None, stream=None):
+    """out[pos[t, j]] = X[t]: each token's row to the rows of its choices, in one launch.
+
+    X: [T, K] of any type whose rows are a multiple of 16 bytes (bf16, fp32, fp8
+    or 4-bit codes); pos: int32 [T, k] (expert_sort), entries outside [0, M_cap) are
+    skipped; out: optional [M_cap, K] like X (default: M_cap = T*k rows, or M_cap
+    where it is given). Rows that no choice names are left as they were. scale: the
+    block scales of X, which go with their rows: fp32 [ceil(K/128), T]
+    (fp8_quantize, rms_norm_fp8) or uint8 [ceil(K/256), T, 8] (mx4_quantize); then
+    (out, out_scale) is returned, out_scale [.., M_cap(, 8)]. The gradient with
+    respect to X is expert_combine(d_out, pos).
+    """
+    import torch
+    what = "expert_spread"
+    args = [("X", X, X.dtype, 2), ("pos", pos, torch.int32, 2)]
+    sb = 0
+    if scale is not None:
+        sb = 8 if scale.dtype is torch.uint8 else 4
+        args.append(("scale", scale, torch.uint8 if sb == 8 else torch.float32, 3 if sb == 8 else 2))
+    dev = _device_args(what, *args)
+    T, k = pos.shape
+    K = X.shape[1]
+    _match(what, X.shape[0] == T and (scale is None or scale.shape[1:] == ((T, 8) if sb == 8 else (T,))),
+           X, pos, *([] if scale is None else [scale]))
+    if M_cap is None:
+        M_cap = T * k if out is None else out.shape[0]
+    slices = 0 if scale is None else scale.shape[0]
+    sizes = k | T * k | M_cap | slices
+    if sizes >> 31:
+        _int32(what, sizes)
+    o = _out(what, out, (M_cap, K), (X.dtype,), None, X, stream)
+    s = None
+    if scale is not None:
+        s = _out(what, out_scale, (slices, M_cap) + ((8,) if sb == 8 else ()), (scale.dtype,), None, X, stream)
+    _call("gg_expert_spread", dev, stream, (X, pos, o, scale, s), X.data_ptr(), pos.data_ptr(), o.data_ptr(),
+          None if s is None else scale.data_ptr(), None if s is None else s.data_ptr(), sb if slices else 0, T,
+          k, K * X.element_size(), slices, M_cap)
+    return o if s is None else (o, s)
+
+
+def expert_combine(Y, pos, weights=None, out=None, stream=None, out_dtype=None):
+    """out[t] = sum_j weights[t, j] * Y[pos[t, j]]: the experts' rows back to their tokens, in one launch.
+
+    Y: bf16 or fp32 [M_cap, N], the rows; pos: int32 [T, k] (expert_sort), entries
+    outside [0, M_cap) are skipped; weights: optional fp32 [T, k] (default 1); out:
+    optional bf16 or fp32 [T, N] (out_dtype when out is not given, default Y's). A
+    token with no rows gets zeros. fp32 sums in the order of j, rounded once: equal
+    inputs give equal bits. N is a multiple of 8.
+    """
+    import torch
+    what = "expert_combine"
+    kinds = (torch.bfloat16, torch.float32)
+    args = [("Y", Y, Y.dtype if Y.dtype in kinds else kinds[0], 2), ("pos", pos, torch.int32, 2)]
+    if weights is not None:
+        args.append(("weights", weights, torch.float32, 2))
+    dev = _device_args(what, *args)
+    T, k = pos.shape
+    M_cap, N = Y.shape
+    _match(what, weights is None or weights.shape == (T, k), Y, pos, *([] if weights is None else [weights]))
+    sizes = k | T * k | M_cap | N
+    if sizes >> 31:
+        _int32(what, sizes)
+    if out is None and out_dtype is None:
+        out_dtype = Y.dtype
+    out = _out(what, out, (T, N), kinds, out_dtype, Y, stream)
+    _call("gg_expert_combine", dev, stream, (Y, pos, weights, out), Y.data_ptr(), int(Y.dtype is kinds[1]),
+          pos.data_ptr(), None if weights is None else weights.data_ptr(), out.data_ptr(),
+          int(out.dtype is kinds[1]), T, k, N, M_cap)
+    return out
+
+
+def expert_combine_grad(dO, Y, pos, weights, out=None, out_weights=None, stream=None):
+    """The gradient of expert_combine(Y, pos, weights): (dY, dweights), in one launch.
+
+    dO: [T, N] and Y: [M_cap, N], both bf16 or both fp32; pos: int32 [T, k];
+    weights: fp32 [T, k]. dY[pos[t, j]] = weights[t, j] * dO[t], like Y (``out``;
+    rows that no choice names are left as they were); dweights[t, j] = <dO[t],
+    Y[pos[t, j]]>, fp32 [T, k] (``out_weights``), 0 where a choice has no row.
+    Everything in fp32, dY rounded once, sums in a fixed order.
+    """
+    import torch
+    what = "expert_combine_grad"
+    kind = torch.float32 if Y.dtype is torch.float32 else torch.bfloat16
+    dev = _device_args(what, ("dO", dO, kind, 2), ("Y", Y, kind, 2), ("pos", pos, torch.int32, 2),
+                       ("weights", weights, torch.float32, 2))
+    T, k = pos.shape
+    M_cap, N = Y.shape
+    _match(what, dO.shape == (T, N) and weights.shape == (T, k), dO, Y, pos, weights)
+    sizes = k | T * k | M_cap | N
+    if sizes >> 31:
+        _int32(what, sizes)
+    dY = _out(what, out, (M_cap, N), (kind,), None, Y, stream)
+    dw = _out(what, out_weights, (T, k), (torch.float32,), None, Y, stream)
+    _call("gg_expert_combine_grad", dev, stream, (dO, Y, pos, weights, dY, dw), dO.data_ptr(), Y.data_ptr(),
+          int(kind is torch.float32), pos.data_ptr(), weights.data_ptr(), dY.data_ptr(), dw.data_ptr(), T, k,
+          N, M_cap)
+    return dY, dw
+
+
+def rms_norm_fp8(X, weight, residual=None, eps: float = 1e-6, with_norm: bool = False, out=None,
+                 out_scale=None, out_sum=None, out_norm=None, stream=None):
+    """Root-mean-square norm of X + residual in 8 bits: (q, scales[, sum][, norm]), in one launch.
+
+    X, residual: bf16 [T, K]; weight: bf16 [K]. With z = X + residual rounded to
+    bf16 (X without a residual) and y = z / sqrt(mean z^2 + eps) * weight in fp32:
+    q float8_e4m3fn [T, K] and scales fp32 [ceil(K/128), T] hold y by the rule of
+    fp8_quantize; sum is z, bf16 [T, K], returned where a residual is given
+    (out_sum may be X or residual itself); norm, with with_norm or out_norm, is y
+    rounded once to bf16 (a router's input). K is a multiple of 16, at most 16384.
+    """
+    import torch
+    what = "rms_norm_fp8"
+    bf = torch.bfloat16
+    args = [("X", X, bf, 2), ("weight", weight, bf, 1)]
+    if residual is not None:
+        args.append(("residual", residual, bf, 2))
+    dev = _device_args(what, *args)
+    T, K = X.shape
+    _match(what, weight.shape[0] == K and (residual is None or residual.shape == (T, K)), X, weight,
+           *([] if residual is None else [residual]))
+    if out_sum is not None and residual is None:
+        raise ValueError("%s: out_sum needs a residual" % what)
+    if K >> 31:
+        _int32(what, K)
+    q = _out(what, out, (T, K), (torch.float8_e4m3fn, torch.uint8), None, X, stream)
+    s = _out(what, out_scale, (-(-K // _BLOCK), T), (torch.float32,), None, X, stream)
+    z = None if residual is None else _out(what, out_sum, (T, K), (bf,), None, X, stream)
+    y = _out(what, out_norm, (T, K), (bf,), None, X, stream) if with_norm or out_norm is not None else None
+    _call("gg_rms_norm_fp8", dev, stream, (X, weight, residual, q, s, z, y), X.data_ptr(),
+          None if residual is None else residual.data_ptr(), weight.data_ptr(), q.data_ptr(), s.data_ptr(),
+          None if z is None else z.data_ptr(), None if y is None else y.data_ptr(), T, K, float(eps))
+    return (q, s) + (() if z is None else (z,)) + (() if y is None else (y,))
+
+
+def rms_norm_grad(dY, Z, weight, d_residual=None, eps: float = 1e-6, out=None, out_weight=None, stream=None):
+    """The gradient of y = z / sqrt(mean z^2 + eps) * weight: (dZ, dweight).
+
+    dY: bf16 [T, K], the gradient of y (of an y in 8 bits: of its values before
+    they were rounded); Z: bf16 [T, K], the sum that was normalised; weight: bf16
+    [K]; d_residual: optional bf16 [T, K], the gradient that reaches z past the
+    norm, added. dZ: bf16 [T, K], rounded once: the gradient of X and of residual
+    alike. dweight: fp32 [K], summed without atomics in an order that T and K fix.
+    """
+    import torch
+    what = "rms_norm_grad"
+    bf = torch.bfloat16
+    args = [("dY", dY, bf, 2), ("Z", Z, bf, 2), ("weight", weight, bf, 1)]
+    if d_residual is not None:
+        args.append(("d_residual", d_residual, bf, 2))
+    dev = _device_args(what, *args)
+    T, K = Z.shape
+    _match(what, dY.shape == (T, K) and weight.shape[0] == K
+           and (d_residual is None or d_residual.shape == (T, K)), dY, Z, weight,
+           *([] if d_residual is None else [d_residual]))
+    if K >> 31:
+        _int32(what, K)
+    dZ = _out(what, out, (T, K), (bf,), None, Z, stream)
+    dg = _out(what, out_weight, (K,), (torch.float32,), None, Z, stream)
+    space = _out(what, None, (load_library().gg_rms_norm_grad_workspace(T, K),), (torch.uint8,), None, Z, stream)
+    _call("gg_rms_norm_grad", dev, stream, (dY, Z, weight, d_residual, dZ, dg, space), dY.data_ptr(),
+          Z.data_ptr(), weight.data_ptr(), None if d_residual is None else d_residual.data_ptr(),
+          dZ.data_ptr(), dg.data_ptr(), space.data_ptr(), T, K, float(eps))
+    return dZ, dg
 
 
 def tile_schedule(offsets, N: int, M_cap: int, bm: int = 0, max_tiles: int = None, stream=None):

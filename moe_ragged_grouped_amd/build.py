@@ -26,6 +26,9 @@ SOURCES = [os.path.join(CSRC, "grouped_gemm.hip")]
 # the gradients and the 4-bit operators
 OPERATOR_SOURCES = [os.path.join(CSRC, f) for f in
                     ("grouped_dgrad.hip", "grouped_wgrad.hip", "grouped_mx4.hip")]
+# around the experts' products: rows to the experts and back, the norm, 8-bit blocks
+LAYER_SOURCES = [os.path.join(CSRC, f) for f in
+                 ("expert_rows.hip", "rms_norm.hip", "grouped_fp8_block.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -55,7 +58,7 @@ def _run(cmd, verbose: bool):
 
 def build(verbose: bool = False, extra=(), out: str = LIB, sources=None) -> str:
     """Compile every source (side by side) and link them into one library."""
-    sources = SOURCES + OPERATOR_SOURCES if sources is None else sources
+    sources = SOURCES + OPERATOR_SOURCES + LAYER_SOURCES if sources is None else sources
     flags = [f for f in FLAGS if f != "-shared"]
     with tempfile.TemporaryDirectory() as d:
         objs = [os.path.join(d, os.path.basename(s) + ".o") for s in sources]

@@ -5,10 +5,10 @@
 //   C[m][n] = sum_l A[m][l] * W[n][l]
 //
 // The data gradient (A = dC, W = B[e] with its K rows, l = the product's
-// columns) and the 4-bit product (both operands packed along K) have this
-// form. Both operands then look alike in bytes: a row of a slice is 128
-// bytes, 64 bf16 or 256 4-bit values, and one 16-byte piece of a row is what
-// a lane feeds to one matrix instruction.
+// columns) and the 4-bit and block-scaled 8-bit products (both operands packed
+// along K) have this form. Both operands then look alike in bytes: a row of a
+// slice is 128 bytes, 64 bf16, 128 8-bit or 256 4-bit values, and one 16-byte
+// piece of a row is what a lane feeds to one matrix instruction (two in 8 bits).
 //
 // MI355X mapping:
 //  * buffer_load_dwordx4 ... lds moves 16 bytes a lane from global memory into
@@ -47,10 +47,21 @@ typedef __attribute__((address_space(1))) u32x2 gbl_u32x2;
 
 __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// What a slice holds beside its 128-byte rows (the values of the products are
+// template arguments below; false and true name the first two).
+constexpr int kRowsBf16 = 0;  // nothing
+constexpr int kRowsMx4 = 1;   // 8 scale bytes a row, one for 32 values
+constexpr int kRowsFp8 = 2;   // one fp32 scale a row of A (that of 128 columns is a scalar)
+
 // 16 bytes a lane, global -> LDS at dst + 16 * lane (dst is wave-uniform).
 template <int POLICY = kCacheDefault>
 __device__ __forceinline__ void dma16(buf_rsrc r, lds_u8 *dst, uint32_t voff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 16, voff, 0, 0, POLICY);
+}
+
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void dma4(buf_rsrc r, lds_u8 *dst, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 4, voff, 0, 0, kCacheDefault);
 }
 
 // This wave's loads have landed up to the N youngest ones, and its LDS reads
@@ -280,6 +291,7 @@ __device__ __forceinline__ RingGrid build_ring_schedule(RingSched &s,
 // A device offset through the scalar cache: its wait does not count against
 // the loads and stores in flight.
 typedef __attribute__((address_space(4))) const int32_t cst_i32;
+typedef __attribute__((address_space(4))) const float cst_f32;
 __device__ __forceinline__ int clamp_off_s(const int32_t *off_g, int e, int M_cap) {
   const int v = ((cst_i32 *)off_g)[e];
   return min(max(v, 0), M_cap);
@@ -330,29 +342,33 @@ __device__ __forceinline__ Tile decode_ring_tile(const RingSched &s, const int32
 constexpr int kRowBytes = 128;  // bytes of a row in one slice
 constexpr int kRingBytes = 155 * 1024;  // LDS for the stages (the schedule takes 4.2 KB more)
 
-// Bytes of a stage: A's rows, B's rows, then (MX: 4-bit operands with a scale
-// byte per 32 values) 8 scale bytes per row of A and of B.
-__host__ __device__ constexpr int ring_stage(int BM, int BN, bool MX) {
-  return (BM + BN) * (kRowBytes + (MX ? 8 : 0));
+// Bytes of a stage: A's rows, B's rows, then the scales: in 4 bits 8 bytes per
+// row of A and of B; in 8 bits 4 bytes per row of A, up to a whole row, as stages
+// start on one.
+__host__ __device__ constexpr int ring_stage(int BM, int BN, int F) {
+  return (BM + BN) * (kRowBytes + (F == kRowsMx4 ? 8 : 0)) +
+         (F == kRowsFp8 ? (BM * 4 + kRowBytes - 1) / kRowBytes * kRowBytes : 0);
 }
 // As many stages as fit, up to 6 (96 KB and more in flight).
-__host__ __device__ constexpr int ring_stages(int BM, int BN, bool MX) {
-  const int s = kRingBytes / ring_stage(BM, BN, MX);
+__host__ __device__ constexpr int ring_stages(int BM, int BN, int F) {
+  const int s = kRingBytes / ring_stage(BM, BN, F);
   return s < 6 ? s : 6;
 }
 
-template <int BM_, int BN_, int WM_, int WN_, bool MX_>
+template <int BM_, int BN_, int WM_, int WN_, int F_>
 struct RingCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
-  static constexpr bool MX = MX_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, F = F_;
+  static constexpr bool MX = F == kRowsMx4, FP8 = F == kRowsFp8;
   static_assert(WM * WN == kThreads / kWave, "one wave per wave tile");
   static constexpr int WTM = BM / WM, WTN = BN / WN;
   static_assert(WTM % 16 == 0 && WTN % 16 == 0, "16x16 blocks");
   static constexpr int MI = WTM / 16, NI = WTN / 16;
   static constexpr int A_BYTES = BM * kRowBytes, B_BYTES = BN * kRowBytes;
-  static constexpr int STAGE = ring_stage(BM, BN, MX), S = ring_stages(BM, BN, MX);
-  // loads a wave issues per slice: of A, and of the weights and the scales
-  static constexpr int NA = BM >= 64 ? BM / 64 : 1, NB = BN / 64 + (MX ? 1 : 0), LPS = NA + NB;
+  static constexpr int STAGE = ring_stage(BM, BN, F), S = ring_stages(BM, BN, F);
+  // loads a wave issues per slice: of A (8 bits: and its scales), and of the
+  // weights (4 bits: and all scales)
+  static constexpr int NA = (BM >= 64 ? BM / 64 : 1) + (FP8 ? 1 : 0), NB = BN / 64 + (MX ? 1 : 0),
+                       LPS = NA + NB;
   // Two stages are all that the tallest tile leaves room for, and one slice
   // ahead is too little for weights that come from HBM (measured: 2.3 us a
   // slice against 1.5 for its products alone). But a wave takes all column
@@ -368,8 +384,10 @@ struct RingCfg {
 struct RingTile {
   const char *A;          // row 0 of the tile
   const char *B;          // weight row (output column) 0 of the tile
-  const char *As, *Bs;    // MX: scale bytes of the first slice, row 0 / column 0
-  uint64_t as_step, bs_step;  // MX: bytes from a slice's scales to the next one's
+  const char *As, *Bs;    // scales of the first slice, row 0 / column 0
+  // bytes from a slice's scales to the next one's (8 bits: from a column block's to
+  // the next one's)
+  uint64_t as_step, bs_step;
   uint32_t pitch;         // bytes of a row of A and of B
   int rows, ncols;        // valid rows and columns
 };
@@ -399,6 +417,14 @@ __device__ __forceinline__ void ring_scale_rows(buf_rsrc rs, int BM, int BN, lds
   const int at = 16 * (wave % 4) * n;
   lds_u8 *const dst = stage + (BM + BN) * kRowBytes + (is_b ? BM * 8 : 0) + at;
   if (lane < n) dma16(rs, dst, (uint32_t)(at + 16 * lane));
+}
+
+// fp32 scales of A, a row to a lane, BM / 8 rows a wave.
+__device__ __forceinline__ void ring_row_scales(const RingTile &t, int BM, int BN, lds_u8 *stage, int k,
+                                                int wave, int lane) {
+  const buf_rsrc rs = make_buf(t.As + (uint64_t)k * t.as_step, 4u * (uint32_t)t.rows);
+  const int n = BM / 8, at = wave * n;
+  if (lane < n) dma4(rs, stage + (BM + BN) * kRowBytes + 4 * at, 4u * (uint32_t)(at + lane));
 }
 
 // This wave's loads of slice k of a BM x BN tile into one stage, a group of 8
@@ -432,20 +458,22 @@ __device__ __forceinline__ void ring_load_b(const RingTile &t, buf_rsrc rb, int 
   if (t.pitch % kRowBytes == 0) dma16<kCacheStream>(rb, dst, ring_row_off(t, r, k, lane));
   else dma16(rb, dst, ring_row_off(t, r, k, lane));
 }
-__device__ __forceinline__ void ring_issue_a(const RingTile &t, int BM, lds_u8 *stage, int k, int wave,
-                                             int lane) {
+template <int F>
+__device__ __forceinline__ void ring_issue_a(const RingTile &t, int BM, int BN, lds_u8 *stage, int k,
+                                             int wave, int lane) {
   const buf_rsrc ra = ring_rows(t.A, t.rows, t, k);
   const int n = BM >= 64 ? BM / 64 : 1;
 #pragma unroll 1
   for (int i = 0; i < n; ++i) ring_load_a(t, ra, BM, stage, i, k, wave, lane);
+  if constexpr (F == kRowsFp8) ring_row_scales(t, BM, BN, stage, k, wave, lane);
 }
-template <bool MX>
+template <int F>
 __device__ __forceinline__ void ring_issue_b(const RingTile &t, int BM, int BN, lds_u8 *stage, int k,
                                              int wave, int lane) {
   const buf_rsrc rb = ring_rows(t.B, t.ncols, t, k);
 #pragma unroll 1
   for (int i = 0; i < BN / 64; ++i) ring_load_b(t, rb, BM, stage, i, k, wave, lane);
-  if constexpr (MX) ring_scale_rows(ring_scales(t, k, wave), BM, BN, stage, wave, lane);
+  if constexpr (F == kRowsMx4) ring_scale_rows(ring_scales(t, k, wave), BM, BN, stage, wave, lane);
 }
 
 // The same loads as pieces, to be issued between matrix instructions: a CU's
@@ -468,7 +496,9 @@ struct RingPieces {
   }
   template <int J>
   __device__ __forceinline__ void issue() const {
-    if constexpr (J < C::NA) {
+    if constexpr (C::FP8 && J == C::NA - 1) {
+      if (ka < KT) ring_row_scales(t, C::BM, C::BN, sa, ka, wave, lane);
+    } else if constexpr (J < C::NA) {
       if (ka < KT) ring_load_a(t, ra, C::BM, sa, J, ka, wave, lane);
     } else if constexpr (J < C::NA + C::BN / 64) {
       if (kb < KT) ring_load_b(t, rb, C::BM, sb, J - C::NA, kb, wave, lane);
@@ -483,17 +513,17 @@ __device__ __forceinline__ int ring_slices(const RingTile &t) {
 }
 
 // The first slices of a tile, as many as the ring takes ahead of the products.
-template <bool MX>
+template <int F>
 __device__ __forceinline__ void ring_prologue(const RingTile &t, int BM, int BN, lds_u8 *lds,
                                               int wave, int lane) {
-  const int n = min(ring_stages(BM, BN, MX) - 1, ring_slices(t)), bytes = ring_stage(BM, BN, MX);
+  const int n = min(ring_stages(BM, BN, F) - 1, ring_slices(t)), bytes = ring_stage(BM, BN, F);
 #pragma unroll 1
   for (int k = 0; k < n; ++k) {
-    ring_issue_a(t, BM, lds + k * bytes, k, wave, lane);
-    ring_issue_b<MX>(t, BM, BN, lds + k * bytes, k, wave, lane);
+    ring_issue_a<F>(t, BM, BN, lds + k * bytes, k, wave, lane);
+    ring_issue_b<F>(t, BM, BN, lds + k * bytes, k, wave, lane);
   }
-  if (ring_stages(BM, BN, MX) == 2 && ring_slices(t) > 1)  // EARLY_B
-    ring_issue_b<MX>(t, BM, BN, lds + bytes, 1, wave, lane);
+  if (ring_stages(BM, BN, F) == 2 && ring_slices(t) > 1)  // EARLY_B
+    ring_issue_b<F>(t, BM, BN, lds + bytes, 1, wave, lane);
 }
 
 // The products of one slice. Two matrix steps; lane group g takes 16-byte
@@ -571,6 +601,66 @@ __device__ __forceinline__ void ring_mma(f32x4 (&acc)[C::NI][C::MI], const lds_u
   });
 }
 
+// The same for 8-bit operands: one matrix step a slice, which is one block of
+// the scales, so each 16 x 16 product is taken by itself and added times its
+// scales (4 fused multiply-adds a lane to a matrix instruction, which the other
+// wave of the SIMD covers). Lane group g takes chunks g and 4 + g of a row. A
+// product is added while the next two are made.
+template <class C, class Mid, class Blk>
+__device__ __forceinline__ void ring_mma_fp8(f32x4 (&acc)[C::NI][C::MI], const lds_u8 *a_stage,
+                                             const lds_u8 *b_stage, int wm0, int wn0, int lane,
+                                             float column, Mid &&mid, Blk &&blk) {
+  const int g = lane / 16, s = lane % 16;
+  const lds_u8 *const ar = a_stage + (wm0 + s) * kRowBytes;
+  const lds_u8 *const br = b_stage + C::A_BYTES + (wn0 + s) * kRowBytes;
+  const lds_u8 *const sc = a_stage + C::A_BYTES + C::B_BYTES + 4 * (wm0 + s);
+  const int c0 = 16 * (g ^ (s & 7)), c1 = 16 * ((4 + g) ^ (s & 7));
+  // row fragments are read one block ahead, two where registers allow
+  constexpr int Y = C::MI > 4 ? 2 : 3;
+  ring_i32x8 x[C::NI], y[Y];
+  float scale[Y];
+  f32x4 d[3];  // the products of three matrix instructions
+  auto read = [&](const lds_u8 *row) {
+    const u32x4 lo = *(const lds_u32x4 *)(row + c0), hi = *(const lds_u32x4 *)(row + c1);
+    return __builtin_bit_cast(ring_i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto read_y = [&](auto bc) {
+    constexpr int b = decltype(bc)::value;
+    if constexpr (b < C::MI) {
+      y[b % Y] = read(ar + b * 16 * kRowBytes);
+      scale[b % Y] = *(const lds_f32 *)(sc + b * 64);
+    }
+  };
+#pragma unroll
+  for (int ni = 0; ni < C::NI; ++ni) x[ni] = read(br + ni * 16 * kRowBytes);
+  read_y(std::integral_constant<int, 0>{});
+  if constexpr (Y > 2) read_y(std::integral_constant<int, 1>{});
+  constexpr int P = C::NI * C::MI;
+  float both[2];  // the row's scale times the columns'
+  auto add = [&](auto ic) {  // the product of block i % NI of row block i / NI
+    constexpr int i = decltype(ic)::value, ni = i % C::NI, b = i / C::NI;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[ni][b][j] = __builtin_fmaf(d[i % 3][j], both[b % 2], acc[ni][b][j]);
+    // (the compiler would sink the sums past the loads' branches, and keep every
+    // product in registers until then)
+    asm volatile("" : "+v"(acc[ni][b]));
+    if constexpr (ni == C::NI - 1) blk(b);
+  };
+  static_for<P>([&](auto ic) {
+    constexpr int i = decltype(ic)::value, ni = i % C::NI, b = i / C::NI;
+    if constexpr (ni == 0) read_y(std::integral_constant<int, b + Y - 1>{});
+    // formats 0, 0 = E4M3; constant scales of 0 select the form without scales
+    d[i % 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        x[ni], y[b % Y], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+    if constexpr (ni == 0) both[b % 2] = scale[b % Y] * column;
+    if constexpr (i >= 2) add(std::integral_constant<int, i - 2>{});
+    if constexpr (ni == C::NI - 1) mid(std::integral_constant<int, b>{});
+    __builtin_amdgcn_sched_barrier(0);
+  });
+  if constexpr (P > 1) add(std::integral_constant<int, P - 2>{});
+  add(std::integral_constant<int, P - 1>{});
+}
+
 // One step: multiply slice k out of its stage (a_cur and b_cur, both its
 // start) and meanwhile refill the stage that slice k - 1 left: a_nxt is that
 // stage, b_nxt too, or with EARLY_B the present one, whose weights are read
@@ -584,7 +674,7 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[C::NI][C::MI], const Ring
                                           const lds_u8 *__restrict__ b_cur,
                                           lds_u8 *__restrict__ a_nxt, lds_u8 *__restrict__ b_nxt,
                                           int ka, int kb, int KT, int wave, int lane, int wm0, int wn0,
-                                          int blocks_left) {
+                                          int blocks_left, float column) {
   const RingPieces<C> loads(t, a_nxt, ka, b_nxt, kb, KT, wave, lane);
   auto mid = [&](auto mc) {
     constexpr int mi = decltype(mc)::value, j0 = mi * C::LPS / C::MI, j1 = (mi + 1) * C::LPS / C::MI;
@@ -599,7 +689,8 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[C::NI][C::MI], const Ring
     });
   };
   __builtin_amdgcn_s_setprio(1);
-  ring_mma<C>(acc, a_cur, b_cur, wm0, wn0, lane, blocks_left, mid, [](int) {});
+  if constexpr (C::FP8) ring_mma_fp8<C>(acc, a_cur, b_cur, wm0, wn0, lane, column, mid, [](int) {});
+  else ring_mma<C>(acc, a_cur, b_cur, wm0, wn0, lane, blocks_left, mid, [](int) {});
   __builtin_amdgcn_s_setprio(0);
 }
 
@@ -622,13 +713,24 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
     for (int mi = 0; mi < C::MI; ++mi) acc[ni][mi] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int KT = ring_slices(t);
   int cur = 0, nxt = C::S - 1;  // stages of slice k and of slice k + S - 1
+  // 8 bits: the scale of this wave's columns (they lie in one block of 128) in each
+  // slice, through the scalar cache
+  cst_f32 *columns = nullptr;
+  float column = 0.0f;
+  if constexpr (C::FP8) {
+    // (a wave past the last column takes the last block's)
+    const int band = C::BN > 128 ? min(wn0, t.ncols - 1) / 128 : 0;
+    columns = (cst_f32 *)(t.Bs + (uint64_t)band * t.bs_step);
+    column = columns[0];
+  }
   for (int k = 0; k < KT - 1; ++k) {
     if constexpr (C::EARLY_B) wait_loads<C::NB>();  // the weights of slice k + 1 stay in flight
     else wait_slices<C>(min(C::S - 2, KT - 1 - k));  // slices k + 1 .. min(k + S - 2, KT - 1) do
     wg_barrier();
     lds_u8 *const c = lds + cur * C::STAGE, *const n = lds + nxt * C::STAGE;
     ring_step<C>(acc, t, c, c, n, C::EARLY_B ? c : n, k + C::S - 1, k + C::S - (C::EARLY_B ? 0 : 1), KT,
-                 wave, lane, wm0, wn0, n_blocks - 8 * k);
+                 wave, lane, wm0, wn0, n_blocks - 8 * k, column);
+    if constexpr (C::FP8) column = columns[k + 1];
     cur = cur + 1 == C::S ? 0 : cur + 1;
     nxt = nxt + 1 == C::S ? 0 : nxt + 1;
   }
@@ -642,9 +744,10 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
     for (int ni = 0; ni < C::NI; ++ni) asm volatile("" : "+v"(acc[ni][mi]));
     if constexpr (C::MI <= 4) epi.block(acc, mi);
   };
-  ring_mma<C>(
-      acc, lds + cur * C::STAGE, lds + cur * C::STAGE, wm0, wn0, lane, n_blocks - 8 * (KT - 1),
-      [](auto) {}, final_block);
+  const lds_u8 *const last = lds + cur * C::STAGE;
+  auto none = [](auto) {};
+  if constexpr (C::FP8) ring_mma_fp8<C>(acc, last, last, wm0, wn0, lane, column, none, final_block);
+  else ring_mma<C>(acc, last, last, wm0, wn0, lane, n_blocks - 8 * (KT - 1), none, final_block);
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   wg_barrier();
   next();
@@ -662,7 +765,7 @@ static_assert(kThreads / kWave == 8, "eight waves share a slice's loads");
 // The tiles of one workgroup, one after the other. make(tile) gives a
 // RingTile, run(cfg, ring tile, tile, next) runs one with the configuration
 // cfg, a default-constructed RingCfg.
-template <bool MX, class Make, class Run>
+template <int F, class Make, class Run>
 __device__ __forceinline__ void run_ring_tiles(const RingSched &sched, const RingGrid &grid,
                                                const int32_t *off, int E, int M_cap, int N,
                                                int bm_fixed, lds_u8 *lds, Make &&make, Run &&run) {
@@ -674,7 +777,7 @@ __device__ __forceinline__ void run_ring_tiles(const RingSched &sched, const Rin
   RingTile rt = make(tl);
   {
     const int tid = threadIdx.x;
-    ring_prologue<MX>(rt, tl.bm, tl.bn, lds, scalar(tid / kWave), tid % kWave);
+    ring_prologue<F>(rt, tl.bm, tl.bn, lds, scalar(tid / kWave), tid % kWave);
   }
   for (;;) {
     const int t2 = t + G;
@@ -685,30 +788,30 @@ __device__ __forceinline__ void run_ring_tiles(const RingSched &sched, const Rin
     auto next = [&] {
       int tid = threadIdx.x;
       asm volatile("" : "+v"(tid));
-      if (more) ring_prologue<MX>(nrt, ntl.bm, ntl.bn, lds, scalar(tid / kWave), tid % kWave);
+      if (more) ring_prologue<F>(nrt, ntl.bm, ntl.bn, lds, scalar(tid / kWave), tid % kWave);
     };
     if (tl.bn == 256) {
       switch (tl.bm) {
-        case 16: run(RingCfg<16, 256, 1, 8, MX>{}, rt, tl, next); break;
-        case 32: run(RingCfg<32, 256, 1, 8, MX>{}, rt, tl, next); break;
-        case 64: run(RingCfg<64, 256, 1, 8, MX>{}, rt, tl, next); break;
-        case 128: run(RingCfg<128, 256, 2, 4, MX>{}, rt, tl, next); break;
-        default: run(RingCfg<256, 256, 2, 4, MX>{}, rt, tl, next); break;
+        case 16: run(RingCfg<16, 256, 1, 8, F>{}, rt, tl, next); break;
+        case 32: run(RingCfg<32, 256, 1, 8, F>{}, rt, tl, next); break;
+        case 64: run(RingCfg<64, 256, 1, 8, F>{}, rt, tl, next); break;
+        case 128: run(RingCfg<128, 256, 2, 4, F>{}, rt, tl, next); break;
+        default: run(RingCfg<256, 256, 2, 4, F>{}, rt, tl, next); break;
       }
     } else if (tl.bn == 128) {
       switch (tl.bm) {
-        case 16: run(RingCfg<16, 128, 1, 8, MX>{}, rt, tl, next); break;
-        case 32: run(RingCfg<32, 128, 1, 8, MX>{}, rt, tl, next); break;
-        case 64: run(RingCfg<64, 128, 2, 4, MX>{}, rt, tl, next); break;
-        case 128: run(RingCfg<128, 128, 2, 4, MX>{}, rt, tl, next); break;
-        default: run(RingCfg<256, 128, 4, 2, MX>{}, rt, tl, next); break;
+        case 16: run(RingCfg<16, 128, 1, 8, F>{}, rt, tl, next); break;
+        case 32: run(RingCfg<32, 128, 1, 8, F>{}, rt, tl, next); break;
+        case 64: run(RingCfg<64, 128, 2, 4, F>{}, rt, tl, next); break;
+        case 128: run(RingCfg<128, 128, 2, 4, F>{}, rt, tl, next); break;
+        default: run(RingCfg<256, 128, 4, 2, F>{}, rt, tl, next); break;
       }
     } else {
       switch (tl.bm) {
-        case 32: run(RingCfg<32, 64, 2, 4, MX>{}, rt, tl, next); break;
-        case 64: run(RingCfg<64, 64, 2, 4, MX>{}, rt, tl, next); break;
-        case 128: run(RingCfg<128, 64, 4, 2, MX>{}, rt, tl, next); break;
-        default: run(RingCfg<256, 64, 4, 2, MX>{}, rt, tl, next); break;
+        case 32: run(RingCfg<32, 64, 2, 4, F>{}, rt, tl, next); break;
+        case 64: run(RingCfg<64, 64, 2, 4, F>{}, rt, tl, next); break;
+        case 128: run(RingCfg<128, 64, 4, 2, F>{}, rt, tl, next); break;
+        default: run(RingCfg<256, 64, 4, 2, F>{}, rt, tl, next); break;
       }
     }
     if (!more) break;

@@ -1,0 +1,312 @@
+// Root-mean-square norm for gfx950: of a sum with the residual, quantised to
+// 8 bits with a scale for each block of 128 on its way out; and its gradient.
+//
+//   z = bf16(x + residual),  r = 1 / sqrt(mean z^2 + eps),  y = z * r * g
+//
+// z is rounded before it is normalised, as the layers behind the residual see
+// it. Everything else is held in fp32 and rounded once.
+
+#include "gg_common.h"
+#include "gg_fp8.h"
+#include "gg_host.h"
+#include "gg_ring.h"
+#include "grouped_gemm.h"
+
+namespace gg {
+
+// A row on kNormWaves waves, eight neighbouring values to a lane and V such
+// pieces of a row a lane; a workgroup takes kNormRows rows.
+constexpr int kNormWaves = 4, kNormRows = 2;
+constexpr int kNormThreads = kNormWaves * kNormRows * kWave;
+constexpr int kNormPiece = kNormWaves * kWave * 8;  // values of a row at one time
+
+__device__ __forceinline__ float sum_of_wave(float v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d, kWave);
+  return v;
+}
+
+struct NormParams {
+  const u32x4 *x, *res, *g;
+  u32x2 *q;
+  float *scales;
+  u32x4 *sum, *y;
+  int T, K;
+  float eps;
+};
+
+template <int V>
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(NormParams p) {
+  __shared__ float sums[kNormRows][kNormWaves];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = scalar(tid / kWave);
+  const int row = wave / kNormWaves, part = wave % kNormWaves;
+  const int t = blockIdx.x * kNormRows + row, pitch = p.K / 8;
+  const bool live = t < p.T;
+  const size_t base = (size_t)t * pitch;
+  u32x4 z[V];
+  float sq = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = (i * kNormWaves + part) * kWave + lane;
+    z[i] = live && c < pitch ? p.x[base + c] : u32x4{0, 0, 0, 0};
+  }
+  if (p.res != nullptr) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (i * kNormWaves + part) * kWave + lane;
+      if (!live || c >= pitch) continue;
+      const u32x4 r = p.res[base + c];
+      u32x4 s;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 two = {bf16_lo(z[i][j]) + bf16_lo(r[j]), bf16_hi(z[i][j]) + bf16_hi(r[j])};
+        s[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2));
+      }
+      z[i] = s;
+      if (p.sum != nullptr) p.sum[base + c] = s;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sq = __builtin_fmaf(bf16_lo(z[i][j]), bf16_lo(z[i][j]), sq);
+      sq = __builtin_fmaf(bf16_hi(z[i][j]), bf16_hi(z[i][j]), sq);
+    }
+  sq = sum_of_wave(sq);
+  if (lane == 0) sums[row][part] = sq;
+  __syncthreads();
+  sq = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kNormWaves; ++w) sq += sums[row][w];
+  const float r = 1.0f / sqrtf(sq / (float)p.K + p.eps);
+  if (!live) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = (i * kNormWaves + part) * kWave + lane;
+    const bool in = c < pitch;
+    const u32x4 g = in ? p.g[c] : u32x4{0, 0, 0, 0};
+    float v[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float zj = j % 2 ? bf16_hi(z[i][j / 2]) : bf16_lo(z[i][j / 2]);
+      const float gj = j % 2 ? bf16_hi(g[j / 2]) : bf16_lo(g[j / 2]);
+      v[j] = zj * gj * r;  // z g is exact: 16 bits
+      top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
+    }
+    const float m = fp8_multiplier(row16_max(top));
+    if (!in) continue;
+    if (p.y != nullptr) {
+      const u32x2 a = pack_bf16(f32x4{v[0], v[1], v[2], v[3]}),
+                  b = pack_bf16(f32x4{v[4], v[5], v[6], v[7]});
+      p.y[base + c] = u32x4{a.x, a.y, b.x, b.y};
+    }
+    u32x2 o = {fp8_quad(v[0] * m, v[1] * m, v[2] * m, v[3] * m),
+               fp8_quad(v[4] * m, v[5] * m, v[6] * m, v[7] * m)};
+    if (m == 0.0f) o = u32x2{0, 0};
+    p.q[base + c] = o;
+    if (lane % 16 == 0) p.scales[(size_t)(c / 16) * p.T + t] = fp8_scale(m);
+  }
+}
+
+// The gradient: with u = g dY and z the norm's input,
+//   dz = r (u - z r^2 mean(u z)) + the residual's gradient,  dg = sum over rows of dY z r.
+// A workgroup takes every so many rows and holds its share of dg in registers;
+// a second launch adds the shares in their order.
+constexpr int kGradGroups = 1024;  // workgroups at most
+
+struct NormGradParams {
+  const u32x4 *dy, *z, *g, *res;
+  u32x4 *dz;
+  float *shares;  // [workgroups][K]
+  int T, K;
+  float eps;
+};
+
+// THREADS a row, V pieces of 8 values a lane
+template <int V, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradParams p) {
+  constexpr int kGradThreads = THREADS, kGradWaves = THREADS / kWave;
+  __shared__ float sums[2][kGradWaves][2];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, pitch = p.K / 8;
+  float dg[V][8];
+  u32x4 g[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = i * kGradThreads + tid;
+    g[i] = c < pitch ? p.g[c] : u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
+  }
+  int turn = 0;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+    const size_t base = (size_t)t * pitch;
+    u32x4 z[V], d[V], res[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = i * kGradThreads + tid;
+      z[i] = d[i] = res[i] = u32x4{0, 0, 0, 0};
+      if (c < pitch) {
+        z[i] = p.z[base + c];
+        d[i] = p.dy[base + c];
+        if (p.res != nullptr) res[i] = p.res[base + c];
+      }
+    }
+    float sq = 0.0f, uz = 0.0f;
+    auto val = [](const u32x4 &v, int j) { return j % 2 ? bf16_hi(v[j / 2]) : bf16_lo(v[j / 2]); };
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float zj = val(z[i], j);
+        sq = __builtin_fmaf(zj, zj, sq);
+        uz = __builtin_fmaf(val(d[i], j) * val(g[i], j), zj, uz);
+      }
+    sq = sum_of_wave(sq);
+    uz = sum_of_wave(uz);
+    if (lane == 0) {
+      sums[turn][wave][0] = sq;
+      sums[turn][wave][1] = uz;
+    }
+    __syncthreads();
+    sq = uz = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kGradWaves; ++w) {
+      sq += sums[turn][w][0];
+      uz += sums[turn][w][1];
+    }
+    const float r = 1.0f / sqrtf(sq / (float)p.K + p.eps);
+    const float back = r * r * r * (uz / (float)p.K);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = i * kGradThreads + tid;
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float zj = val(z[i], j), dj = val(d[i], j);
+        dg[i][j] = __builtin_fmaf(dj, zj * r, dg[i][j]);
+        o[j] = __builtin_fmaf(-back, zj, r * (dj * val(g[i], j))) + val(res[i], j);
+      }
+      if (c < pitch) {
+        const u32x2 a = pack_bf16(f32x4{o[0], o[1], o[2], o[3]}),
+                    b = pack_bf16(f32x4{o[4], o[5], o[6], o[7]});
+        p.dz[base + c] = u32x4{a.x, a.y, b.x, b.y};
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = i * kGradThreads + tid;
+    if (c >= pitch) continue;
+    f32x4 *const s = (f32x4 *)(p.shares + (size_t)blockIdx.x * p.K + 8 * c);
+    s[0] = f32x4{dg[i][0], dg[i][1], dg[i][2], dg[i][3]};
+    s[1] = f32x4{dg[i][4], dg[i][5], dg[i][6], dg[i][7]};
+  }
+}
+
+// dg: a workgroup takes 64 columns, each wave every so many of the shares.
+constexpr int kShareThreads = 1024, kShareWaves = kShareThreads / kWave;
+
+__global__ __launch_bounds__(kShareThreads) void norm_shares_kernel(const float *__restrict__ shares,
+                                                                    float *__restrict__ dg, int groups,
+                                                                    int K) {
+  __shared__ float part[kShareWaves][kWave];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, c = blockIdx.x * kWave + lane;
+  float sum = 0.0f;
+  if (c < K) {
+#pragma unroll 8
+    for (int w = wave; w < groups; w += kShareWaves) sum += shares[(size_t)w * K + c];
+  }
+  part[wave][lane] = sum;
+  __syncthreads();
+  if (wave != 0 || c >= K) return;
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kShareWaves; ++w) sum += part[w][lane];
+  dg[c] = sum;
+}
+
+constexpr int kNormMost = 16384;  // columns
+static_assert(kNormMost == 8 * kNormPiece, "pieces of a lane");
+
+static int grad_groups(long long T) { return (int)(T < kGradGroups ? T : kGradGroups); }
+
+static gg_status_t check_norm(int64_t T, int K, float eps) {
+  if (T < 0 || K < 1 || !(eps >= 0.0f)) return GG_ERR_INVALID_VALUE;
+  if (K % 16 != 0) return GG_ERR_MISALIGNED;
+  if (K > kNormMost || T > INT32_MAX) return GG_ERR_UNSUPPORTED;
+  return GG_OK;
+}
+
+}  // namespace gg
+
+using namespace gg;
+
+extern "C" gg_status_t gg_rms_norm_fp8(const void *X, const void *residual, const void *weight, void *q,
+                                       float *scales, void *sum, void *norm, int64_t T, int32_t K,
+                                       float eps, void *stream) {
+  gg_status_t st = check_norm(T, K, eps);
+  if (st != GG_OK) return st;
+  const long long groups = (T + kNormRows - 1) / kNormRows;
+  if (!launch_fits(groups, kNormThreads)) return GG_ERR_UNSUPPORTED;
+  if (sum != nullptr && residual == nullptr) return GG_ERR_INVALID_VALUE;
+  if (T == 0) return GG_OK;
+  if (X == nullptr || weight == nullptr || q == nullptr || scales == nullptr) return GG_ERR_INVALID_VALUE;
+  for (const void *a : {X, residual, weight, (const void *)q, (const void *)scales, (const void *)sum, (const void *)norm})
+    if (!is_aligned(a, 16)) return GG_ERR_MISALIGNED;
+  const Span x = span(X, T, K, 2), res = span(residual, T, K, 2), g = span(weight, K, 2, 1),
+             c = span(q, T, K, 1), s = span(scales, (K + 127) / 128, T, 4), z = span(sum, T, K, 2),
+             y = span(norm, T, K, 2);
+  // (a lane reads what it adds before it stores the sum: in place is safe)
+  if (!apart(c, x, res, g, s, z, y) || !apart(s, x, res, g, z, y) || !apart(z, g, y) ||
+      !apart(y, x, res, g) || !(sum == X || apart(z, x)) || !(sum == residual || apart(z, res)))
+    return GG_ERR_INVALID_VALUE;
+  const NormParams p{static_cast<const u32x4 *>(X), static_cast<const u32x4 *>(residual),
+                     static_cast<const u32x4 *>(weight), static_cast<u32x2 *>(q), scales,
+                     static_cast<u32x4 *>(sum), static_cast<u32x4 *>(norm), (int)T, K, eps};
+  const int v = (K + kNormPiece - 1) / kNormPiece;
+  void (*const kernel)(NormParams) = v == 1   ? norm_kernel<1>
+                                     : v == 2 ? norm_kernel<2>
+                                     : v == 3 ? norm_kernel<3>
+                                     : v == 4 ? norm_kernel<4>
+                                              : norm_kernel<8>;
+  return launch(kernel, dim3((unsigned)groups), kNormThreads, 0, stream, p);
+}
+
+extern "C" int64_t gg_rms_norm_grad_workspace(int64_t T, int32_t K) {
+  return T < 1 || K < 1 || K > kNormMost ? 0 : (int64_t)grad_groups(T) * K * 4;
+}
+
+extern "C" gg_status_t gg_rms_norm_grad(const void *dY, const void *Z, const void *weight,
+                                        const void *d_residual, void *dZ, float *dweight,
+                                        void *workspace, int64_t T, int32_t K, float eps, void *stream) {
+  gg_status_t st = check_norm(T, K, eps);
+  if (st != GG_OK) return st;
+  if (weight == nullptr || dweight == nullptr) return GG_ERR_INVALID_VALUE;
+  if (T > 0 && (dY == nullptr || Z == nullptr || dZ == nullptr || workspace == nullptr))
+    return GG_ERR_INVALID_VALUE;
+  for (const void *a : {dY, Z, weight, d_residual, (const void *)dZ, (const void *)dweight, (const void *)workspace})
+    if (!is_aligned(a, 16)) return GG_ERR_MISALIGNED;
+  const Span dy = span(dY, T, K, 2), z = span(Z, T, K, 2), g = span(weight, K, 2, 1),
+             res = span(d_residual, T, K, 2), dz = span(dZ, T, K, 2), dg = span(dweight, K, 4, 1),
+             ws = span(workspace, gg_rms_norm_grad_workspace(T, K), 1, 1);
+  if (!apart(dz, dy, z, g, res, dg, ws) || !apart(dg, dy, z, g, res, ws) || !apart(ws, dy, z, g, res))
+    return GG_ERR_INVALID_VALUE;
+  const int groups = grad_groups(T);
+  if (T > 0) {
+    const NormGradParams p{static_cast<const u32x4 *>(dY), static_cast<const u32x4 *>(Z),
+                           static_cast<const u32x4 *>(weight), static_cast<const u32x4 *>(d_residual),
+                           static_cast<u32x4 *>(dZ), static_cast<float *>(workspace), (int)T, K, eps};
+    const int v = (K + 2047) / 2048;
+    void (*const kernel)(NormGradParams) = v == 1   ? norm_grad_kernel<1, 256>
+                                           : v == 2 ? norm_grad_kernel<2, 256>
+                                           : v == 3 ? norm_grad_kernel<3, 256>
+                                           : v == 4 ? norm_grad_kernel<4, 256>
+                                                    : norm_grad_kernel<2, 1024>;
+    st = launch(kernel, dim3((unsigned)groups), v <= 4 ? 256 : 1024, 0, stream, p);
+    if (st != GG_OK) return st;
+  }
+  return launch(norm_shares_kernel, dim3((unsigned)((K + kWave - 1) / kWave)), kShareThreads, 0, stream,
+                static_cast<const float *>(workspace), dweight, groups, K);
+}
