@@ -757,6 +757,7 @@ def grouped_gemm_mx4_swiglu(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int
 # ---- around the experts' products: 8-bit blocks, rows to the experts and back, the norm
 
 _BLOCK = 128
+_SORT_RECOUNT = 8192  # choices that gg_expert_sort takes without a workspace, whatever E
 
 
 def _fp8(t):
@@ -882,31 +883,41 @@ def expert_sort(experts, E: int, weights=None, out=None, stream=None):
     """
     import torch
     what = "expert_sort"
-    wide = experts.dtype is torch.int64
-    args = [("experts", experts, torch.int64 if wide else torch.int32, 2)]
-    if weights is not None:
-        args.append(("weights", weights, torch.float32, 2))
-    dev = _device_args(what, *args)
+    kind = experts.dtype
+    if kind is not torch.int64:
+        kind = torch.int32
+    if weights is None:
+        dev = _device_args(what, ("experts", experts, kind, 2))
+    else:
+        dev = _device_args(what, ("experts", experts, kind, 2), ("weights", weights, torch.float32, 2))
+        _match(what, weights.shape == experts.shape, experts, weights)
     T, k = experts.shape
-    E = int(E)
-    _match(what, weights is None or weights.shape == (T, k), experts, *([] if weights is None else [weights]))
-    sizes = E | k | T * k
+    E, n = int(E), T * k
+    sizes = E | k | n
     if sizes >> 31:
         _int32(what, sizes)
-    i32 = (torch.int32,)
-    shapes = [((max(E, 0) + 1,), i32), ((T * k,), i32), ((T, k), i32)]
-    if weights is not None:
-        shapes.append(((T * k,), (torch.float32,)))
-    if out is None:
-        out = (None,) * len(shapes)
-    if len(out) != len(shapes):
-        raise ValueError("%s: out must hold %d tensors" % (what, len(shapes)))
-    out = tuple(_out(what, o, shape, dtypes, None, experts, stream) for o, (shape, dtypes) in zip(out, shapes))
-    need = load_library().gg_expert_sort_workspace(T * k, E)
-    space = _out(what, None, (need,), (torch.uint8,), None, experts, stream) if need else None
-    _call("gg_expert_sort", dev, stream, (experts, weights, *out, space), experts.data_ptr(), int(wide),
-          None if weights is None else weights.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
-          out[2].data_ptr(), None if weights is None else out[3].data_ptr(),
+    i32 = torch.int32
+    if out is None and stream is None:
+        new = experts.new_empty
+        out = (new((max(E, 0) + 1,), dtype=i32), new((n,), dtype=i32), new((T, k), dtype=i32))
+        if weights is not None:
+            out += (new((n,), dtype=torch.float32),)
+    else:
+        wanted = [((max(E, 0) + 1,), i32), ((n,), i32), ((T, k), i32)]
+        if weights is not None:
+            wanted.append(((n,), torch.float32))
+        if out is None:
+            out = (None,) * len(wanted)
+        if len(out) != len(wanted):
+            raise ValueError("%s: out must hold %d tensors" % (what, len(wanted)))
+        out = tuple(_out(what, o, shape, (dt,), None, experts, stream) for o, (shape, dt) in zip(out, wanted))
+    space = None
+    if n > _SORT_RECOUNT:
+        space = _out(what, None, (load_library().gg_expert_sort_workspace(n, E),), (torch.uint8,), None, experts,
+                     stream)
+    _call("gg_expert_sort", dev, stream, (experts, weights, *out, space), experts.data_ptr(),
+          int(kind is torch.int64), None if weights is None else weights.data_ptr(), out[0].data_ptr(),
+          out[1].data_ptr(), out[2].data_ptr(), None if weights is None else out[3].data_ptr(),
           None if space is None else space.data_ptr(), T, k, E)
     return out
 

@@ -19,11 +19,14 @@ namespace gg {
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
-// Choices one workgroup sorts alone: its rows and weights then wait in LDS, so
-// that they leave in whole lines.
-constexpr int kSortAlone = 8192, kSortPerWave = kSortAlone / kSortWaves;
-// More are split: one launch counts, the next places.
+// The choices are split over workgroups, 1024 each while there are no more than
+// 256 workgroups. Every workgroup needs the counts of all choices and of those
+// before its own. Few choices it counts by itself, in the same launch; of more
+// than 8192 one launch counts each part and the next places. Measured (us, 8
+// choices a token by rank^-1.2 of 64 experts, launches in a graph; one launch /
+// two): 2048 choices 5.2 / 6.8, 8192 7.7 / 7.3, 16384 10.2 / 7.5, 65536 25.7 /
+// 7.9. A launch costs the host 3 us besides, which is why 8192 still takes one.
+constexpr int kSortRecount = 8192;
 constexpr int kSplitThreads = 512, kSplitWaves = kSplitThreads / kWave;
 constexpr int kSplitChunk = 1024, kSplitMost = 256;  // choices a workgroup at least; workgroups at most
 
@@ -92,59 +95,6 @@ struct SortParams {
   int k, E, bits, chunk;
 };
 
-template <class I>
-__global__ __launch_bounds__(kSortThreads) void sort_alone_kernel(SortParams p) {
-  extern __shared__ __attribute__((aligned(16))) int sort_lds[];
-  int *const sums = sort_lds, *const rows = sums + kSortWaves, *const seen = rows + kSortAlone;
-  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, E = p.E, n = (int)p.n;
-  for (int i = tid; i < kSortWaves * E; i += kSortThreads) seen[i] = 0;
-  for (int i = tid; i < n; i += kSortThreads) rows[i] = -1;
-  __syncthreads();
-  constexpr int kSteps = kSortPerWave / kWave;
-  // a wave takes neighbouring choices, as many as it needs
-  const int per = (n + kSortThreads - 1) / kSortThreads * kWave, i0 = wave * per;
-  int e[kSteps], place[kSteps];
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int i = i0 + s * kWave + lane;
-    e[s] = s * kWave < per ? choice((const I *)p.experts, i, n, E) : E;
-  }
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-    if (s * kWave < per) place[s] = wave_place(e[s], E, p.bits, seen + wave * E);
-  __syncthreads();
-  // each expert's choices over the waves, then over the experts
-  int mine = 0;
-  if (tid < E)
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int c = seen[w * E + tid];
-      seen[w * E + tid] = mine;
-      mine += c;
-    }
-  int total;
-  const int start = group_starts<kSortWaves>(mine, sums, total);
-  if (tid < E) {
-    p.offsets[tid] = start;
-    for (int w = 0; w < kSortWaves; ++w) seen[w * E + tid] += start;
-  }
-  if (tid == 0) p.offsets[E] = total;
-  __syncthreads();
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int i = i0 + s * kWave + lane;
-    if (s * kWave >= per || i >= n) continue;
-    const int at = e[s] < E ? seen[wave * E + e[s]] + place[s] : -1;
-    p.pos[i] = at;
-    if (at >= 0) rows[at] = i;
-  }
-  __syncthreads();
-  for (int r = tid; r < n; r += kSortThreads) {
-    const int i = rows[r];
-    p.rows[r] = i < 0 ? -1 : i / p.k;
-    if (p.w != nullptr) p.row_w[r] = i < 0 ? 0.0f : p.w[i];
-  }
-}
-
 // Choices of each expert in this workgroup's part.
 template <class I>
 __global__ __launch_bounds__(kSplitThreads) void sort_count_kernel(SortParams p) {
@@ -162,7 +112,7 @@ __global__ __launch_bounds__(kSplitThreads) void sort_count_kernel(SortParams p)
     p.counts[(size_t)blockIdx.x * pitch + e] = e < p.E ? sort_lds[e] : 0;
 }
 
-template <class I>
+template <class I, bool COUNTED>
 __global__ __launch_bounds__(kSplitThreads) void sort_place_kernel(SortParams p) {
   extern __shared__ __attribute__((aligned(16))) int sort_lds[];
   const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, E = p.E;
@@ -171,32 +121,61 @@ __global__ __launch_bounds__(kSplitThreads) void sort_place_kernel(SortParams p)
   int *const all = sums + kSplitWaves;  // [E] choices of an expert
   int *const base = all + E;           // [E] its first row, then the next one of this workgroup
   int *const seen = base + E;          // [waves][E]
-  for (int e = tid; e < 2 * E; e += kSplitThreads) all[e] = 0;
-  __syncthreads();
-  // the workgroups' counts: a thread takes four experts of every so many
-  // workgroups, with eight loads in flight
-  const int quads = (E + 3) / 4, beside = kSplitThreads / quads, g0 = tid / quads, q = tid - g0 * quads;
-  if (g0 < beside) {
-    i32x4 sum = {0, 0, 0, 0}, before = {0, 0, 0, 0};
-    for (int g = g0; g < G; g += 8 * beside) {
-      i32x4 c[8];
+  const I *const experts = (const I *)p.experts;
+  const long long i0 = (long long)b * p.chunk, i1 = min(i0 + p.chunk, p.n);
+  constexpr int kSteps = kSplitChunk / kSplitThreads;
+  // this workgroup's first choices and weights, on their way during the counting
+  int e[kSteps];
+  float w[kSteps];
+  auto fetch = [&](long long r0) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        c[u] = i32x4{0, 0, 0, 0};
-        if (g + u * beside < G) c[u] = ((const i32x4 *)p.counts)[(size_t)(g + u * beside) * quads + q];
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        sum += c[u];
-        if (g + u * beside < b) before += c[u];
-      }
+    for (int s = 0; s < kSteps; ++s) {
+      const long long i = r0 + (wave * kSteps + s) * kWave + lane;
+      e[s] = choice(experts, i, i1, E);
+      w[s] = p.w != nullptr && i < i1 ? p.w[i] : 0.0f;
     }
+  };
+  fetch(i0);
+  for (int x = tid; x < 2 * E; x += kSplitThreads) all[x] = 0;
+  __syncthreads();
+  if constexpr (COUNTED) {
+    // the workgroups' counts: a thread takes four experts of every so many
+    // workgroups, with eight loads in flight
+    const int quads = (E + 3) / 4, beside = kSplitThreads / quads, g0 = tid / quads, q = tid - g0 * quads;
+    if (g0 < beside) {
+      i32x4 sum = {0, 0, 0, 0}, before = {0, 0, 0, 0};
+      for (int g = g0; g < G; g += 8 * beside) {
+        i32x4 c[8];
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (4 * q + x < E) {
-        if (sum[x] != 0) atomicAdd(&all[4 * q + x], sum[x]);
-        if (before[x] != 0) atomicAdd(&base[4 * q + x], before[x]);
+        for (int u = 0; u < 8; ++u) {
+          c[u] = i32x4{0, 0, 0, 0};
+          if (g + u * beside < G) c[u] = ((const i32x4 *)p.counts)[(size_t)(g + u * beside) * quads + q];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          sum += c[u];
+          if (g + u * beside < b) before += c[u];
+        }
       }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (4 * q + x < E) {
+          if (sum[x] != 0) atomicAdd(&all[4 * q + x], sum[x]);
+          if (before[x] != 0) atomicAdd(&base[4 * q + x], before[x]);
+        }
+    }
+  } else {
+    // all choices, those before this workgroup's apart, with eight loads in flight
+    for (long long r0 = tid; r0 < p.n; r0 += 8 * kSplitThreads) {
+      int c[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) c[u] = choice(experts, r0 + u * kSplitThreads, p.n, E);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (c[u] < E) atomicAdd((r0 + u * kSplitThreads < i0 ? base : all) + c[u], 1);
+    }
+    __syncthreads();
+    for (int x = tid; x < E; x += kSplitThreads) all[x] += base[x];
   }
   __syncthreads();
   // two experts a thread (E <= 1024)
@@ -210,23 +189,19 @@ __global__ __launch_bounds__(kSplitThreads) void sort_place_kernel(SortParams p)
     if (e0 + 1 < E) p.offsets[e0 + 1] = start + c0;
     if (tid == 0) p.offsets[E] = total;
   }
-  const long long i0 = (long long)b * p.chunk, i1 = min(i0 + p.chunk, p.n);
-  constexpr int kSteps = kSplitChunk / kSplitThreads;
   for (long long r0 = i0; r0 < i1; r0 += kSplitChunk) {
+    if (r0 != i0) fetch(r0);
     for (int i = tid; i < kSplitWaves * E; i += kSplitThreads) seen[i] = 0;
     __syncthreads();
-    int e[kSteps], place[kSteps];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      e[s] = choice((const I *)p.experts, r0 + (wave * kSteps + s) * kWave + lane, i1, E);
+    int place[kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) place[s] = wave_place(e[s], E, p.bits, seen + wave * E);
     __syncthreads();
     for (int x = tid; x < E; x += kSplitThreads) {
       int at = base[x];
-      for (int w = 0; w < kSplitWaves; ++w) {
-        const int c = seen[w * E + x];
-        seen[w * E + x] = at;
+      for (int v = 0; v < kSplitWaves; ++v) {
+        const int c = seen[v * E + x];
+        seen[v * E + x] = at;
         at += c;
       }
       base[x] = at;
@@ -239,8 +214,8 @@ __global__ __launch_bounds__(kSplitThreads) void sort_place_kernel(SortParams p)
       const int at = e[s] < E ? seen[wave * E + e[s]] + place[s] : -1;
       p.pos[i] = at;
       if (at >= 0) {
-        p.rows[at] = (int)(i / p.k);
-        if (p.w != nullptr) p.row_w[at] = p.w[i];
+        p.rows[at] = (int)i / p.k;
+        if (p.w != nullptr) p.row_w[at] = w[s];
       }
     }
     __syncthreads();  // seen is cleared again
@@ -254,10 +229,11 @@ __global__ __launch_bounds__(kSplitThreads) void sort_place_kernel(SortParams p)
 
 // ------------------------------------------------------------------ spread
 //
-// A wave reads 4 KB of a token's row and writes them to each of its rows.
+// A wave reads V KB of a token's row and writes them to each of its rows; the
+// places of eight rows are read together.
 
 constexpr int kRowThreads = 256, kRowWaves = kRowThreads / kWave;
-constexpr int kSpreadVecs = 4, kSpreadBytes = kSpreadVecs * kWave * 16;
+constexpr int kJ = 8;  // rows in flight
 
 struct SpreadParams {
   const u32x4 *X;
@@ -269,29 +245,56 @@ struct SpreadParams {
   int T, k, pitch, segments, M, scale_bytes, slices;  // pitch in 16 bytes
 };
 
+// The places of choices j0 .. j0 + 7 of a token; -1 where there is no row.
+__device__ __forceinline__ void places(int (&at)[kJ], const int32_t *pos, int k, int M, int t, int j0) {
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    at[j] = j0 + j < k ? scalar(pos[(size_t)t * k + j0 + j]) : -1;
+    if (at[j] >= M) at[j] = -1;
+  }
+}
+
+template <int V>
 __global__ __launch_bounds__(kRowThreads) void spread_kernel(SpreadParams p) {
   const int lane = threadIdx.x % kWave, wave = scalar(threadIdx.x / kWave);
   const long long u = (long long)blockIdx.x * kRowWaves + wave;
   if (u >= p.units) return;
   const int t = (int)(u / p.segments), seg = (int)(u - (long long)t * p.segments);
-  const int c0 = seg * kSpreadVecs * kWave + lane;
-  u32x4 v[kSpreadVecs];
+  const int c0 = seg * V * kWave + lane;
+  u32x4 v[V];
 #pragma unroll
-  for (int i = 0; i < kSpreadVecs; ++i)
+  for (int i = 0; i < V; ++i)
     if (c0 + i * kWave < p.pitch) v[i] = p.X[(size_t)t * p.pitch + c0 + i * kWave];
-  for (int j = 0; j < p.k; ++j) {
-    const int at = scalar(p.pos[(size_t)t * p.k + j]);
-    if (at < 0 || at >= p.M) continue;
+  for (int j0 = 0; j0 < p.k; j0 += kJ) {
+    int at[kJ];
+    places(at, p.pos, p.k, p.M, t, j0);
 #pragma unroll
-    for (int i = 0; i < kSpreadVecs; ++i)
-      if (c0 + i * kWave < p.pitch) p.out[(size_t)at * p.pitch + c0 + i * kWave] = v[i];
-    if (seg == 0 && p.scale_bytes == 4)
-      for (int s = lane; s < p.slices; s += kWave)
-        ((uint32_t *)p.out_scales)[(size_t)s * p.M + at] = ((const uint32_t *)p.scales)[(size_t)s * p.T + t];
-    if (seg == 0 && p.scale_bytes == 8)
-      for (int s = lane; s < p.slices; s += kWave)
-        ((u32x2 *)p.out_scales)[(size_t)s * p.M + at] = ((const u32x2 *)p.scales)[(size_t)s * p.T + t];
+    for (int j = 0; j < kJ; ++j) {
+      if (at[j] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c0 + i * kWave < p.pitch) p.out[(size_t)at[j] * p.pitch + c0 + i * kWave] = v[i];
+    }
+    // the scales: a slice to a lane, the waves of a token in turn
+    auto move = [&](auto one) {
+      typedef decltype(one) S;
+      for (int s = seg * kWave + lane; s < p.slices; s += p.segments * kWave) {
+        const S x = ((const S *)p.scales)[(size_t)s * p.T + t];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+          if (at[j] >= 0) ((S *)p.out_scales)[(size_t)s * p.M + at[j]] = x;
+      }
+    };
+    if (p.scale_bytes == 4) move(uint32_t{});
+    else if (p.scale_bytes == 8) move(u32x2{});
   }
+}
+
+// Pieces a lane takes: as many as leave every CU eight waves, up to four.
+static int spread_pieces(long long T, long long row_bytes) {
+  int v = 4;
+  while (v > 1 && T * ((row_bytes + v * 1024 - 1) / (v * 1024)) < 256 * 8) v /= 2;
+  return v;
 }
 
 // ----------------------------------------------------------------- combine
@@ -299,8 +302,6 @@ __global__ __launch_bounds__(kRowThreads) void spread_kernel(SpreadParams p) {
 // A lane takes eight columns of one token: its k rows are loaded together and
 // summed in fp32 in the order of the choices, the weighted one by one fused
 // multiply-add a term. Rounded once.
-
-constexpr int kJ = 8;  // rows in flight
 
 template <class Y>
 struct Eight;  // eight values of a row in fp32
@@ -447,37 +448,30 @@ static int split_sort(long long n, int *chunk) {
   c = (c + kSplitChunk - 1) / kSplitChunk * kSplitChunk;
   if (c < kSplitChunk) c = kSplitChunk;
   *chunk = (int)c;
-  return (int)((n + c - 1) / c);
+  return n > c ? (int)((n + c - 1) / c) : 1;  // (no choices: the offsets remain to be written)
 }
 
 template <class I>
 static gg_status_t expert_sort(SortParams p, void *stream) {
-  if (p.n <= kSortAlone) {
-    const int lds = (kSortWaves + kSortAlone + kSortWaves * p.E) * 4;
-    int dev = 0;
-    if (!current_device(&dev)) return GG_ERR_LAUNCH;
-    const RingLaunch li =
-        ring_launch<sort_alone_kernel<I>>(dev, (kSortWaves + kSortAlone + kSortWaves * kMaxExperts) * 4);
-    if (li.err != hipSuccess) return GG_ERR_LAUNCH;
-    return launch(sort_alone_kernel<I>, dim3(1), kSortThreads, lds, stream, p);
-  }
   const int G = split_sort(p.n, &p.chunk);
+  if (p.n <= kSortRecount)
+    return launch(sort_place_kernel<I, false>, dim3((unsigned)G), kSplitThreads,
+                  (kSplitWaves + 2 * p.E + kSplitWaves * p.E) * 4, stream, p);
   gg_status_t st = launch(sort_count_kernel<I>, dim3((unsigned)G), kSplitThreads, p.E * 4, stream, p);
   if (st != GG_OK) return st;
-  return launch(sort_place_kernel<I>, dim3((unsigned)G), kSplitThreads,
+  return launch(sort_place_kernel<I, true>, dim3((unsigned)G), kSplitThreads,
                 (kSplitWaves + 2 * p.E + kSplitWaves * p.E) * 4, stream, p);
 }
 
-static_assert((kSortWaves + kSortAlone + kSortWaves * kMaxExperts) * 4 <= 160 * 1024, "LDS");
 static_assert((kSplitWaves + 2 * kMaxExperts + kSplitWaves * kMaxExperts) * 4 <= 64 * 1024, "LDS");
-static_assert(2 * kSplitThreads >= kMaxExperts && kSortThreads >= kMaxExperts, "experts of a thread");
+static_assert(2 * kSplitThreads >= kMaxExperts, "experts of a thread");
 
 }  // namespace gg
 
 using namespace gg;
 
 extern "C" int64_t gg_expert_sort_workspace(int64_t choices, int32_t E) {
-  if (choices <= kSortAlone || choices > INT32_MAX || E < 1) return 0;
+  if (choices <= kSortRecount || choices > INT32_MAX || E < 1) return 0;
   int chunk;
   return (int64_t)split_sort(choices, &chunk) * ((E + 3LL) / 4) * 16;
 }
@@ -518,7 +512,8 @@ extern "C" gg_status_t gg_expert_spread(const void *X, const int32_t *pos, void 
       (scale_bytes == 0) != (slices == 0))
     return GG_ERR_INVALID_VALUE;
   if (row_bytes % 16 != 0) return GG_ERR_MISALIGNED;
-  const long long segments = (row_bytes + kSpreadBytes - 1) / kSpreadBytes, units = T * segments;
+  const int V = spread_pieces(T, row_bytes);
+  const long long segments = (row_bytes + V * 1024 - 1) / (V * 1024), units = T * segments;
   if (row_bytes > (1LL << 31) || !launch_fits((units + kRowWaves - 1) / kRowWaves, kRowThreads))
     return GG_ERR_UNSUPPORTED;
   if (T > 0 && (X == nullptr || (M_cap > 0 && out == nullptr))) return GG_ERR_INVALID_VALUE;
@@ -533,7 +528,7 @@ extern "C" gg_status_t gg_expert_spread(const void *X, const int32_t *pos, void 
   const SpreadParams p{static_cast<const u32x4 *>(X), static_cast<u32x4 *>(out),
                        static_cast<const char *>(scales), static_cast<char *>(out_scales), pos, units,
                        (int)T, k, (int)(row_bytes / 16), (int)segments, (int)M_cap, scale_bytes, slices};
-  return launch(spread_kernel, dim3((unsigned)((units + kRowWaves - 1) / kRowWaves)), kRowThreads, 0,
+  return launch(V == 4 ? spread_kernel<4> : V == 2 ? spread_kernel<2> : spread_kernel<1>, dim3((unsigned)((units + kRowWaves - 1) / kRowWaves)), kRowThreads, 0,
                 stream, p);
 }
 
