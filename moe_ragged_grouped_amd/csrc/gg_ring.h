@@ -605,7 +605,8 @@ __device__ __forceinline__ void ring_mma(f32x4 (&acc)[C::NI][C::MI], const lds_u
 // the scales, so each 16 x 16 product is taken by itself and added times its
 // scales (4 fused multiply-adds a lane to a matrix instruction, which the other
 // wave of the SIMD covers). Lane group g takes chunks g and 4 + g of a row. A
-// product is added while the next two are made.
+// product is added while the next four are made (two: 1.5% slower at 64 x 256
+// rows, K = 1024, N = 2688; the additions take 10% of that launch's time).
 template <class C, class Mid, class Blk>
 __device__ __forceinline__ void ring_mma_fp8(f32x4 (&acc)[C::NI][C::MI], const lds_u8 *a_stage,
                                              const lds_u8 *b_stage, int wm0, int wn0, int lane,
@@ -619,7 +620,8 @@ __device__ __forceinline__ void ring_mma_fp8(f32x4 (&acc)[C::NI][C::MI], const l
   constexpr int Y = C::MI > 4 ? 2 : 3;
   ring_i32x8 x[C::NI], y[Y];
   float scale[Y];
-  f32x4 d[3];  // the products of three matrix instructions
+  constexpr int D = 4;  // matrix instructions between a product and its addition
+  f32x4 d[D + 1];
   auto read = [&](const lds_u8 *row) {
     const u32x4 lo = *(const lds_u32x4 *)(row + c0), hi = *(const lds_u32x4 *)(row + c1);
     return __builtin_bit_cast(ring_i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -636,11 +638,13 @@ __device__ __forceinline__ void ring_mma_fp8(f32x4 (&acc)[C::NI][C::MI], const l
   read_y(std::integral_constant<int, 0>{});
   if constexpr (Y > 2) read_y(std::integral_constant<int, 1>{});
   constexpr int P = C::NI * C::MI;
-  float both[2];  // the row's scale times the columns'
+  // the row's scale times the columns', of every row block that is not added yet
+  constexpr int R = D / C::NI + 2;
+  float both[R];
   auto add = [&](auto ic) {  // the product of block i % NI of row block i / NI
     constexpr int i = decltype(ic)::value, ni = i % C::NI, b = i / C::NI;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[ni][b][j] = __builtin_fmaf(d[i % 3][j], both[b % 2], acc[ni][b][j]);
+    for (int j = 0; j < 4; ++j) acc[ni][b][j] = __builtin_fmaf(d[i % (D + 1)][j], both[b % R], acc[ni][b][j]);
     // (the compiler would sink the sums past the loads' branches, and keep every
     // product in registers until then)
     asm volatile("" : "+v"(acc[ni][b]));
@@ -650,15 +654,15 @@ __device__ __forceinline__ void ring_mma_fp8(f32x4 (&acc)[C::NI][C::MI], const l
     constexpr int i = decltype(ic)::value, ni = i % C::NI, b = i / C::NI;
     if constexpr (ni == 0) read_y(std::integral_constant<int, b + Y - 1>{});
     // formats 0, 0 = E4M3; constant scales of 0 select the form without scales
-    d[i % 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+    d[i % (D + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
         x[ni], y[b % Y], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-    if constexpr (ni == 0) both[b % 2] = scale[b % Y] * column;
-    if constexpr (i >= 2) add(std::integral_constant<int, i - 2>{});
+    if constexpr (ni == 0) both[b % R] = scale[b % Y] * column;
+    if constexpr (i >= D) add(std::integral_constant<int, i - D>{});
     if constexpr (ni == C::NI - 1) mid(std::integral_constant<int, b>{});
     __builtin_amdgcn_sched_barrier(0);
   });
-  if constexpr (P > 1) add(std::integral_constant<int, P - 2>{});
-  add(std::integral_constant<int, P - 1>{});
+  constexpr int L = P < D ? P : D;
+  static_for<L>([&](auto jc) { add(std::integral_constant<int, P - L + decltype(jc)::value>{}); });
 }
 
 // One step: multiply slice k out of its stage (a_cur and b_cur, both its
@@ -700,9 +704,16 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[C::NI][C::MI], const Ring
 // read of the tile and its stores (or, for tiles of at most 4 row blocks a
 // wave, which store during the last slice, after them): it issues the next
 // tile's prologue.
-template <class C, class Epi, class Next>
+//
+// Loads and stores return in order, so a wait for the first slice would also wait
+// for the stores that the tile before issued after it. Where `after` says that it
+// was one that stores behind the prologue, STORES times at least a wave, that many
+// may stay in flight at the first slice (64 x 256 rows, K = 1024, N = 2688 with
+// SwiGLU 70.1 -> 68.7 us).
+template <class C, int STORES = 0, class Epi, class Next>
 __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, int tid,
-                                              int n_blocks, Epi &&epi, Next &&next) {
+                                              int n_blocks, Epi &&epi, Next &&next,
+                                              bool after = false) {
   const int wave = scalar(tid / kWave);
   const int lane = tid % kWave;
   const int wm0 = (wave / C::WN) * C::WTM, wn0 = (wave % C::WN) * C::WTN;
@@ -724,8 +735,12 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
     column = columns[0];
   }
   for (int k = 0; k < KT - 1; ++k) {
-    if constexpr (C::EARLY_B) wait_loads<C::NB>();  // the weights of slice k + 1 stay in flight
-    else wait_slices<C>(min(C::S - 2, KT - 1 - k));  // slices k + 1 .. min(k + S - 2, KT - 1) do
+    if constexpr (C::EARLY_B) {  // the weights of slice k + 1 stay in flight
+      if (STORES > 0 && k == 0 && after) wait_loads<C::NB + STORES>();
+      else wait_loads<C::NB>();
+    }
+    if constexpr (!C::EARLY_B)
+      wait_slices<C>(min(C::S - 2, KT - 1 - k));  // slices k + 1 .. min(k + S - 2, KT - 1) do
     wg_barrier();
     lds_u8 *const c = lds + cur * C::STAGE, *const n = lds + nxt * C::STAGE;
     ring_step<C>(acc, t, c, c, n, C::EARLY_B ? c : n, k + C::S - 1, k + C::S - (C::EARLY_B ? 0 : 1), KT,
@@ -751,6 +766,7 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   wg_barrier();
   next();
+  if constexpr (STORES > 0) asm volatile("" ::: "memory");  // the stores come behind the prologue
   if constexpr (C::MI > 4) {
 #pragma unroll
     for (int mi = 0; mi < C::MI; ++mi) {
@@ -764,14 +780,26 @@ static_assert(kThreads / kWave == 8, "eight waves share a slice's loads");
 
 // The tiles of one workgroup, one after the other. make(tile) gives a
 // RingTile, run(cfg, ring tile, tile, next) runs one with the configuration
-// cfg, a default-constructed RingCfg.
+// cfg, a default-constructed RingCfg. In 8 bits the tiles are dealt out with two
+// differences:
+//  * A launch of less than a round spreads its tiles over all XCDs, so that they
+//    come through eight L2s and not through the first few.
+//  * Every other round from the fourth on is dealt out backwards: where heights
+//    mix, tall tiles come first, and the workgroups that got more of them would
+//    get the taller ones of every later round too (skewed 16k 84.8 -> 83.8 us).
 template <int F, class Make, class Run>
 __device__ __forceinline__ void run_ring_tiles(const RingSched &sched, const RingGrid &grid,
                                                const int32_t *off, int E, int M_cap, int N,
                                                int bm_fixed, lds_u8 *lds, Make &&make, Run &&run) {
   const int G = gridDim.x, b = blockIdx.x;
   // contiguous tiles on one XCD (workgroup ids go round-robin to the XCDs)
+  constexpr bool FP8 = F == kRowsFp8;
   int t = (b % 8) * (G / 8) + b / 8;
+  [[maybe_unused]] int slot = t, round = 0;
+  if constexpr (FP8) {
+    const int per = grid.total < G ? cdiv(grid.total, 8) : G / 8;
+    t = slot = b / 8 < per ? (b % 8) * per + b / 8 : grid.total;
+  }
   if (t >= grid.total) return;
   Tile tl = decode_ring_tile(sched, off, t, E, M_cap, N, bm_fixed, grid);
   RingTile rt = make(tl);
@@ -780,7 +808,11 @@ __device__ __forceinline__ void run_ring_tiles(const RingSched &sched, const Rin
     ring_prologue<F>(rt, tl.bm, tl.bn, lds, scalar(tid / kWave), tid % kWave);
   }
   for (;;) {
-    const int t2 = t + G;
+    int t2 = t + G;
+    if constexpr (FP8) {
+      ++round;
+      t2 = round * G + (round >= 3 && round % 2 == 1 ? G - 1 - slot : slot);
+    }
     const bool more = t2 < grid.total;
     Tile ntl = tl;
     if (more) ntl = decode_ring_tile(sched, off, t2, E, M_cap, N, bm_fixed, grid);

@@ -174,6 +174,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_product_kernel(Fp8BlockParams
     t.ncols = min(tl.bn, N - tl.col0);
     return t;
   };
+  bool after = false;  // the tile before was one of 256 x 256, which stores behind the prologue
   auto run = [&](auto cfg, const RingTile &t, const Tile &tl, auto &next) {
     using C = decltype(cfg);
     int tid = threadIdx.x;
@@ -181,7 +182,9 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_product_kernel(Fp8BlockParams
     const int wave = scalar(tid / kWave);
     ProductEpi<C, O> epi{p.C, p.N, tl.row0, tl.col0, t.rows, t.ncols, (wave / C::WN) * C::WTM,
                          (wave % C::WN) * C::WTN, tid % kWave};
-    run_ring_tile<C>(t, lds, tid, 0, epi, next);
+    // its stores: 8 row blocks of one, two or four
+    run_ring_tile<C, 8 * (O == MOut::F32 ? 4 : O == MOut::BF16 ? 2 : 1)>(t, lds, tid, 0, epi, next, after);
+    after = C::BM == 256 && C::BN == 256;
   };
   run_ring_tiles<kRowsFp8>(sched, grid, p.off, p.E, p.M_cap, p.N, p.bm_fixed, lds, make, run);
 }
