@@ -321,13 +321,13 @@ struct Eight<float> {
   __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i] : b[i - 4]; }
 };
 
-__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8], bool stream) {
   const u32x2 a = pack_bf16(f32x4{v[0], v[1], v[2], v[3]}), b = pack_bf16(f32x4{v[4], v[5], v[6], v[7]});
-  *(u32x4 *)p = u32x4{a.x, a.y, b.x, b.y};
+  st_rows((u32x4 *)p, u32x4{a.x, a.y, b.x, b.y}, stream);
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-  *(f32x4 *)p = f32x4{v[0], v[1], v[2], v[3]};
-  *(f32x4 *)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+__device__ __forceinline__ void store8(float *p, const float (&v)[8], bool stream) {
+  st_rows((f32x4 *)p, f32x4{v[0], v[1], v[2], v[3]}, stream);
+  st_rows((f32x4 *)(p + 4), f32x4{v[4], v[5], v[6], v[7]}, stream);
 }
 
 struct CombineParams {
@@ -338,6 +338,7 @@ struct CombineParams {
   float *dw;
   long long units;
   int T, k, N, M, segments;
+  bool stream;
 };
 
 template <class Y, class O>
@@ -370,7 +371,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w[j], y[j].get(i), sum[i]);
   }
-  store8((O *)p.out + (size_t)t * p.N + n, sum);
+  store8((O *)p.out + (size_t)t * p.N + n, sum, p.stream);
 }
 
 // A workgroup a token: the gradient of its rows, and the scalar products with
@@ -414,7 +415,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(CombineParams
           dot[j] = __builtin_fmaf(d.get(i), y[j].get(i), dot[j]);
           o[i] = w[j] * d.get(i);
         }
-        store8((Y *)p.out + (size_t)at[j] * p.N + n, o);
+        store8((Y *)p.out + (size_t)at[j] * p.N + n, o, p.stream);
       }
     }
 #pragma unroll
@@ -549,7 +550,7 @@ extern "C" gg_status_t gg_expert_combine(const void *Y, int32_t y_fp32, const in
     return GG_ERR_INVALID_VALUE;
   if (T == 0) return GG_OK;
   const CombineParams p{Y, nullptr, pos, weights, out, nullptr, units, (int)T, k, N, (int)M_cap,
-                        (int)segments};
+                        (int)segments, streams(T * N * (out_fp32 ? 4 : 2))};
   const dim3 grid((unsigned)groups);
   if (y_fp32 && out_fp32) return launch(combine_kernel<float, float>, grid, kRowThreads, 0, stream, p);
   if (y_fp32) return launch(combine_kernel<float, uint16_t>, grid, kRowThreads, 0, stream, p);
@@ -576,7 +577,8 @@ extern "C" gg_status_t gg_expert_combine_grad(const void *dO, const void *Y, int
              w = span(weights, T, k, 4), dy = span(dY, M_cap, N, b), dw = span(dweights, T, k, 4);
   if (!apart(dy, o, y, at, w, dw) || !apart(dw, o, y, at, w)) return GG_ERR_INVALID_VALUE;
   if (T == 0) return GG_OK;
-  const CombineParams p{Y, dO, pos, weights, dY, dweights, T, (int)T, k, N, (int)M_cap, 1};
+  const CombineParams p{Y, dO, pos, weights, dY, dweights, T, (int)T, k, N, (int)M_cap, 1,
+                        streams(M_cap * N * b)};
   return launch(fp32 ? combine_grad_kernel<float> : combine_grad_kernel<uint16_t>, dim3((unsigned)T),
                 kRowThreads, 0, stream, p);
 }

@@ -98,6 +98,19 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
 }
 
+// A store of a lane's piece of a row, as streaming data (nt) or not. (The empty
+// asm keeps the compiler from making one plain store of the two.)
+template <class T>
+__device__ __forceinline__ void st_rows(T *p, T v, bool stream) {
+  if (stream) {
+    asm volatile("");
+    __builtin_nontemporal_store(v, p);
+    asm volatile("");
+  } else {
+    *p = v;
+  }
+}
+
 // One 16-byte global store (global_store_dwordx4).
 __device__ __forceinline__ void st_g16(float *p, f32x4 v) { *(gbl_f32x4 *)p = v; }
 

@@ -33,6 +33,7 @@ struct NormParams {
   u32x4 *sum, *y;
   int T, K;
   float eps;
+  bool stream;
 };
 
 template <int V>
@@ -63,7 +64,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormParams p) {
         s[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2));
       }
       z[i] = s;
-      if (p.sum != nullptr) p.sum[base + c] = s;
+      if (p.sum != nullptr) st_rows(p.sum + base + c, s, p.stream);
     }
   }
 #pragma unroll
@@ -100,21 +101,22 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormParams p) {
     if (p.y != nullptr) {
       const u32x2 a = pack_bf16(f32x4{v[0], v[1], v[2], v[3]}),
                   b = pack_bf16(f32x4{v[4], v[5], v[6], v[7]});
-      p.y[base + c] = u32x4{a.x, a.y, b.x, b.y};
+      st_rows(p.y + base + c, u32x4{a.x, a.y, b.x, b.y}, p.stream);
     }
     u32x2 o = {fp8_quad(v[0] * m, v[1] * m, v[2] * m, v[3] * m),
                fp8_quad(v[4] * m, v[5] * m, v[6] * m, v[7] * m)};
     if (m == 0.0f) o = u32x2{0, 0};
-    p.q[base + c] = o;
+    st_rows(p.q + base + c, o, p.stream);
     if (lane % 16 == 0) p.scales[(size_t)(c / 16) * p.T + t] = fp8_scale(m);
   }
 }
 
 // The gradient: with u = g dY and z the norm's input,
 //   dz = r (u - z r^2 mean(u z)) + the residual's gradient,  dg = sum over rows of dY z r.
-// A workgroup takes every so many rows and holds its share of dg in registers;
-// a second launch adds the shares in their order.
-constexpr int kGradGroups = 1024;  // workgroups at most
+// A workgroup takes every so many rows, as many lanes to a row as it has pieces of
+// eight values (two pieces a lane above 8192 values), and holds its share of dg in
+// registers; a second launch adds the shares in their order.
+constexpr int kGradMost = 1024;  // threads of a workgroup at most
 
 struct NormGradParams {
   const u32x4 *dy, *z, *g, *res;
@@ -122,30 +124,31 @@ struct NormGradParams {
   float *shares;  // [workgroups][K]
   int T, K;
   float eps;
+  bool stream;
 };
 
-// THREADS a row, V pieces of 8 values a lane
-template <int V, int THREADS>
-__global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradParams p) {
-  constexpr int kGradThreads = THREADS, kGradWaves = THREADS / kWave;
-  __shared__ float sums[2][kGradWaves][2];
+template <int V>
+__global__ __launch_bounds__(kGradMost) void norm_grad_kernel(NormGradParams p) {
+  __shared__ float sums[2][kGradMost / kWave][2];
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, pitch = p.K / 8;
+  const int threads = blockDim.x, waves = threads / kWave;
   float dg[V][8];
   u32x4 g[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = i * kGradThreads + tid;
+    const int c = i * threads + tid;
     g[i] = c < pitch ? p.g[c] : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
   }
+  auto val = [](const u32x4 &v, int j) { return j % 2 ? bf16_hi(v[j / 2]) : bf16_lo(v[j / 2]); };
   int turn = 0;
   for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
     const size_t base = (size_t)t * pitch;
     u32x4 z[V], d[V], res[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * kGradThreads + tid;
+      const int c = i * threads + tid;
       z[i] = d[i] = res[i] = u32x4{0, 0, 0, 0};
       if (c < pitch) {
         z[i] = p.z[base + c];
@@ -154,7 +157,6 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradParams p) {
       }
     }
     float sq = 0.0f, uz = 0.0f;
-    auto val = [](const u32x4 &v, int j) { return j % 2 ? bf16_hi(v[j / 2]) : bf16_lo(v[j / 2]); };
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -169,10 +171,9 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradParams p) {
       sums[turn][wave][0] = sq;
       sums[turn][wave][1] = uz;
     }
-    __syncthreads();
+    __syncthreads();  // (one a row: the next row's sums go to the other half)
     sq = uz = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kGradWaves; ++w) {
+    for (int w = 0; w < waves; ++w) {
       sq += sums[turn][w][0];
       uz += sums[turn][w][1];
     }
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradParams p) {
     const float back = r * r * r * (uz / (float)p.K);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * kGradThreads + tid;
+      const int c = i * threads + tid;
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -191,13 +192,13 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradParams p) {
       if (c < pitch) {
         const u32x2 a = pack_bf16(f32x4{o[0], o[1], o[2], o[3]}),
                     b = pack_bf16(f32x4{o[4], o[5], o[6], o[7]});
-        p.dz[base + c] = u32x4{a.x, a.y, b.x, b.y};
+        st_rows(p.dz + base + c, u32x4{a.x, a.y, b.x, b.y}, p.stream);
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = i * kGradThreads + tid;
+    const int c = i * threads + tid;
     if (c >= pitch) continue;
     f32x4 *const s = (f32x4 *)(p.shares + (size_t)blockIdx.x * p.K + 8 * c);
     s[0] = f32x4{dg[i][0], dg[i][1], dg[i][2], dg[i][3]};
@@ -205,32 +206,46 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradParams p) {
   }
 }
 
-// dg: a workgroup takes 64 columns, each wave every so many of the shares.
-constexpr int kShareThreads = 1024, kShareWaves = kShareThreads / kWave;
+// dg: a workgroup takes 32 columns, a half wave every 32nd of the shares, in four
+// sums side by side.
+constexpr int kShareThreads = 1024, kShareCols = 32, kShareRows = kShareThreads / kShareCols;
 
 __global__ __launch_bounds__(kShareThreads) void norm_shares_kernel(const float *__restrict__ shares,
                                                                     float *__restrict__ dg, int groups,
                                                                     int K) {
-  __shared__ float part[kShareWaves][kWave];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, c = blockIdx.x * kWave + lane;
-  float sum = 0.0f;
+  __shared__ float part[kShareRows][kShareCols];
+  const int col = threadIdx.x % kShareCols, row = threadIdx.x / kShareCols;
+  const int c = blockIdx.x * kShareCols + col;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < K) {
-#pragma unroll 8
-    for (int w = wave; w < groups; w += kShareWaves) sum += shares[(size_t)w * K + c];
-  }
-  part[wave][lane] = sum;
-  __syncthreads();
-  if (wave != 0 || c >= K) return;
-  sum = 0.0f;
+#pragma unroll 2
+    for (int w = row; w < groups; w += 4 * kShareRows)
 #pragma unroll
-  for (int w = 0; w < kShareWaves; ++w) sum += part[w][lane];
-  dg[c] = sum;
+      for (int u = 0; u < 4; ++u)
+        if (w + u * kShareRows < groups) sum[u] += shares[(size_t)(w + u * kShareRows) * K + c];
+  }
+  part[row][col] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  __syncthreads();
+  if (row != 0 || c >= K) return;
+  float all = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kShareRows; ++w) all += part[w][col];
+  dg[c] = all;
 }
 
 constexpr int kNormMost = 16384;  // columns
 static_assert(kNormMost == 8 * kNormPiece, "pieces of a lane");
 
-static int grad_groups(long long T) { return (int)(T < kGradGroups ? T : kGradGroups); }
+// Threads of a row of the gradient, and workgroups: what the card holds at one time.
+static int grad_threads(int K) {
+  const int pieces = (K / 8 + (K > 8192)) / (K > 8192 ? 2 : 1);
+  return (pieces + kWave - 1) / kWave * kWave;
+}
+static int grad_groups(long long T, int K) {
+  const int beside = 2048 / grad_threads(K);
+  const long long most = 256LL * (beside < 16 ? beside : 16);
+  return (int)(T < most ? T : most);
+}
 
 static gg_status_t check_norm(int64_t T, int K, float eps) {
   if (T < 0 || K < 1 || !(eps >= 0.0f)) return GG_ERR_INVALID_VALUE;
@@ -264,7 +279,8 @@ extern "C" gg_status_t gg_rms_norm_fp8(const void *X, const void *residual, cons
     return GG_ERR_INVALID_VALUE;
   const NormParams p{static_cast<const u32x4 *>(X), static_cast<const u32x4 *>(residual),
                      static_cast<const u32x4 *>(weight), static_cast<u32x2 *>(q), scales,
-                     static_cast<u32x4 *>(sum), static_cast<u32x4 *>(norm), (int)T, K, eps};
+                     static_cast<u32x4 *>(sum), static_cast<u32x4 *>(norm), (int)T, K, eps,
+                     streams(T * K * 2)};
   const int v = (K + kNormPiece - 1) / kNormPiece;
   void (*const kernel)(NormParams) = v == 1   ? norm_kernel<1>
                                      : v == 2 ? norm_kernel<2>
@@ -275,7 +291,7 @@ extern "C" gg_status_t gg_rms_norm_fp8(const void *X, const void *residual, cons
 }
 
 extern "C" int64_t gg_rms_norm_grad_workspace(int64_t T, int32_t K) {
-  return T < 1 || K < 1 || K > kNormMost ? 0 : (int64_t)grad_groups(T) * K * 4;
+  return T < 1 || K < 1 || K > kNormMost ? 0 : (int64_t)grad_groups(T, K) * K * 4;
 }
 
 extern "C" gg_status_t gg_rms_norm_grad(const void *dY, const void *Z, const void *weight,
@@ -293,20 +309,16 @@ extern "C" gg_status_t gg_rms_norm_grad(const void *dY, const void *Z, const voi
              ws = span(workspace, gg_rms_norm_grad_workspace(T, K), 1, 1);
   if (!apart(dz, dy, z, g, res, dg, ws) || !apart(dg, dy, z, g, res, ws) || !apart(ws, dy, z, g, res))
     return GG_ERR_INVALID_VALUE;
-  const int groups = grad_groups(T);
+  const int groups = grad_groups(T, K);
   if (T > 0) {
     const NormGradParams p{static_cast<const u32x4 *>(dY), static_cast<const u32x4 *>(Z),
                            static_cast<const u32x4 *>(weight), static_cast<const u32x4 *>(d_residual),
-                           static_cast<u32x4 *>(dZ), static_cast<float *>(workspace), (int)T, K, eps};
-    const int v = (K + 2047) / 2048;
-    void (*const kernel)(NormGradParams) = v == 1   ? norm_grad_kernel<1, 256>
-                                           : v == 2 ? norm_grad_kernel<2, 256>
-                                           : v == 3 ? norm_grad_kernel<3, 256>
-                                           : v == 4 ? norm_grad_kernel<4, 256>
-                                                    : norm_grad_kernel<2, 1024>;
-    st = launch(kernel, dim3((unsigned)groups), v <= 4 ? 256 : 1024, 0, stream, p);
+                           static_cast<u32x4 *>(dZ), static_cast<float *>(workspace), (int)T, K, eps,
+                           streams(T * K * 2)};
+    st = launch(K > 8192 ? norm_grad_kernel<2> : norm_grad_kernel<1>, dim3((unsigned)groups), grad_threads(K),
+                0, stream, p);
     if (st != GG_OK) return st;
   }
-  return launch(norm_shares_kernel, dim3((unsigned)((K + kWave - 1) / kWave)), kShareThreads, 0, stream,
+  return launch(norm_shares_kernel, dim3((unsigned)((K + kShareCols - 1) / kShareCols)), kShareThreads, 0, stream,
                 static_cast<const float *>(workspace), dweight, groups, K);
 }
