@@ -587,6 +587,8 @@ gg_status_t gg_expert_sort(const void *experts, int32_t wide, const float *weigh
  *   scales, out_scales  block scales that go with the rows, [slices][T] and
  *            [slices][M_cap] elements of scale_bytes: 4 (fp8_block), 8 (mx4), or 0
  *            with slices 0 and both pointers unused. 16-byte aligned.
+ * T * ceil(row_bytes / 4096) / 4, and with scales ceil(T / 256) * 8 * ceil(slices /
+ * 32) besides, stay below 2^24 (GG_ERR_UNSUPPORTED beyond).
  * Its gradient is gg_expert_combine without weights.
  */
 gg_status_t gg_expert_spread(const void *X, const int32_t *pos, void *out, const void *scales,

@@ -230,7 +230,11 @@ __global__ __launch_bounds__(kSplitThreads) void sort_place_kernel(SortParams p)
 // ------------------------------------------------------------------ spread
 //
 // A wave reads V KB of a token's row and writes them to each of its rows; the
-// places of eight rows are read together.
+// places of eight rows are read together. Block scales are moved by workgroups of
+// their own, behind those of the rows: 256 tokens, a token to a lane, and four
+// slices each, so that the rows of an expert, which lie in the order of their
+// tokens, come out of one L2 as runs (scattered by the waves that move the rows,
+// the 800,000 scales of 2048 x 8 rows of 6144 took 8 of 25 us).
 
 constexpr int kRowThreads = 256, kRowWaves = kRowThreads / kWave;
 constexpr int kJ = 8;  // rows in flight
@@ -242,7 +246,9 @@ struct SpreadParams {
   char *out_scales;
   const int32_t *pos;
   long long units;  // tokens x segments
-  int T, k, pitch, segments, M, scale_bytes, slices;  // pitch in 16 bytes
+  int T, k, pitch, segments, M;  // pitch in 16 bytes
+  int scale_bytes, slices;
+  unsigned row_groups, slice_groups;  // workgroups of the rows; of the scales of 256 tokens
 };
 
 // The places of choices j0 .. j0 + 7 of a token; -1 where there is no row.
@@ -254,8 +260,38 @@ __device__ __forceinline__ void places(int (&at)[kJ], const int32_t *pos, int k,
   }
 }
 
+constexpr int kScaleSlices = 4;
+
+template <class S>
+__device__ __forceinline__ void spread_scales(const SpreadParams &p, unsigned group) {
+  const int t = (int)(group / p.slice_groups) * kRowThreads + threadIdx.x;
+  const int s0 = (int)(group % p.slice_groups) * kScaleSlices;
+  if (t >= p.T || s0 >= p.slices) return;
+  S x[kScaleSlices];
+#pragma unroll
+  for (int i = 0; i < kScaleSlices; ++i)
+    if (s0 + i < p.slices) x[i] = ((const S *)p.scales)[(size_t)(s0 + i) * p.T + t];
+  for (int j0 = 0; j0 < p.k; j0 += kJ) {
+    int at[kJ];
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) at[j] = j0 + j < p.k ? p.pos[(size_t)t * p.k + j0 + j] : -1;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      if (at[j] < 0 || at[j] >= p.M) continue;
+#pragma unroll
+      for (int i = 0; i < kScaleSlices; ++i)
+        if (s0 + i < p.slices) ((S *)p.out_scales)[(size_t)(s0 + i) * p.M + at[j]] = x[i];
+    }
+  }
+}
+
 template <int V>
 __global__ __launch_bounds__(kRowThreads) void spread_kernel(SpreadParams p) {
+  if (blockIdx.x >= p.row_groups) {
+    if (p.scale_bytes == 4) spread_scales<uint32_t>(p, blockIdx.x - p.row_groups);
+    else spread_scales<u32x2>(p, blockIdx.x - p.row_groups);
+    return;
+  }
   const int lane = threadIdx.x % kWave, wave = scalar(threadIdx.x / kWave);
   const long long u = (long long)blockIdx.x * kRowWaves + wave;
   if (u >= p.units) return;
@@ -275,24 +311,12 @@ __global__ __launch_bounds__(kRowThreads) void spread_kernel(SpreadParams p) {
       for (int i = 0; i < V; ++i)
         if (c0 + i * kWave < p.pitch) p.out[(size_t)at[j] * p.pitch + c0 + i * kWave] = v[i];
     }
-    // the scales: a slice to a lane, the waves of a token in turn
-    auto move = [&](auto one) {
-      typedef decltype(one) S;
-      for (int s = seg * kWave + lane; s < p.slices; s += p.segments * kWave) {
-        const S x = ((const S *)p.scales)[(size_t)s * p.T + t];
-#pragma unroll
-        for (int j = 0; j < kJ; ++j)
-          if (at[j] >= 0) ((S *)p.out_scales)[(size_t)s * p.M + at[j]] = x;
-      }
-    };
-    if (p.scale_bytes == 4) move(uint32_t{});
-    else if (p.scale_bytes == 8) move(u32x2{});
   }
 }
 
 // Pieces a lane takes: as many as leave every CU eight waves, up to four.
 static int spread_pieces(long long T, long long row_bytes) {
-  int v = 4;
+  int v = row_bytes > 2048 ? 4 : row_bytes > 1024 ? 2 : 1;
   while (v > 1 && T * ((row_bytes + v * 1024 - 1) / (v * 1024)) < 256 * 8) v /= 2;
   return v;
 }
@@ -515,8 +539,11 @@ extern "C" gg_status_t gg_expert_spread(const void *X, const int32_t *pos, void 
   if (row_bytes % 16 != 0) return GG_ERR_MISALIGNED;
   const int V = spread_pieces(T, row_bytes);
   const long long segments = (row_bytes + V * 1024 - 1) / (V * 1024), units = T * segments;
-  if (row_bytes > (1LL << 31) || !launch_fits((units + kRowWaves - 1) / kRowWaves, kRowThreads))
-    return GG_ERR_UNSUPPORTED;
+  // (a multiple of the XCDs, so that the same slices stay on one)
+  const long long row_groups = (units + kRowWaves - 1) / kRowWaves,
+                  slice_groups = ((slices + kScaleSlices - 1LL) / kScaleSlices + 7) / 8 * 8;
+  const long long groups = row_groups + (T + kRowThreads - 1) / kRowThreads * slice_groups;
+  if (row_bytes > (1LL << 31) || !launch_fits(groups, kRowThreads)) return GG_ERR_UNSUPPORTED;
   if (T > 0 && (X == nullptr || (M_cap > 0 && out == nullptr))) return GG_ERR_INVALID_VALUE;
   if (T > 0 && slices > 0 && (scales == nullptr || (M_cap > 0 && out_scales == nullptr)))
     return GG_ERR_INVALID_VALUE;
@@ -528,8 +555,9 @@ extern "C" gg_status_t gg_expert_spread(const void *X, const int32_t *pos, void 
   if (T == 0 || M_cap == 0) return GG_OK;
   const SpreadParams p{static_cast<const u32x4 *>(X), static_cast<u32x4 *>(out),
                        static_cast<const char *>(scales), static_cast<char *>(out_scales), pos, units,
-                       (int)T, k, (int)(row_bytes / 16), (int)segments, (int)M_cap, scale_bytes, slices};
-  return launch(V == 4 ? spread_kernel<4> : V == 2 ? spread_kernel<2> : spread_kernel<1>, dim3((unsigned)((units + kRowWaves - 1) / kRowWaves)), kRowThreads, 0,
+                       (int)T, k, (int)(row_bytes / 16), (int)segments, (int)M_cap, scale_bytes,
+                       slices, (unsigned)row_groups, (unsigned)slice_groups};
+  return launch(V == 4 ? spread_kernel<4> : V == 2 ? spread_kernel<2> : spread_kernel<1>, dim3((unsigned)groups), kRowThreads, 0,
                 stream, p);
 }
 

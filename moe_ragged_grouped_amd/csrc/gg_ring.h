@@ -423,6 +423,9 @@ __device__ __forceinline__ void ring_scale_rows(buf_rsrc rs, int BM, int BN, lds
 __device__ __forceinline__ void ring_row_scales(const RingTile &t, int BM, int BN, lds_u8 *stage, int k,
                                                 int wave, int lane) {
   const buf_rsrc rs = make_buf(t.As + (uint64_t)k * t.as_step, 4u * (uint32_t)t.rows);
+  // (a wave's place is worked out where it is used: kept over the loop it would
+  // cost a scalar that the loop does not have)
+  asm volatile("" : "+s"(wave));
   const int n = BM / 8, at = wave * n;
   if (lane < n) dma4(rs, stage + (BM + BN) * kRowBytes + 4 * at, 4u * (uint32_t)(at + lane));
 }
@@ -795,10 +798,9 @@ __device__ __forceinline__ void run_ring_tiles(const RingSched &sched, const Rin
   // contiguous tiles on one XCD (workgroup ids go round-robin to the XCDs)
   constexpr bool FP8 = F == kRowsFp8;
   int t = (b % 8) * (G / 8) + b / 8;
-  [[maybe_unused]] int slot = t, round = 0;
   if constexpr (FP8) {
     const int per = grid.total < G ? cdiv(grid.total, 8) : G / 8;
-    t = slot = b / 8 < per ? (b % 8) * per + b / 8 : grid.total;
+    t = b / 8 < per ? (b % 8) * per + b / 8 : grid.total;
   }
   if (t >= grid.total) return;
   Tile tl = decode_ring_tile(sched, off, t, E, M_cap, N, bm_fixed, grid);
@@ -809,9 +811,9 @@ __device__ __forceinline__ void run_ring_tiles(const RingSched &sched, const Rin
   }
   for (;;) {
     int t2 = t + G;
-    if constexpr (FP8) {
-      ++round;
-      t2 = round * G + (round >= 3 && round % 2 == 1 ? G - 1 - slot : slot);
+    if constexpr (FP8) {  // (the place in this round follows from t: one scalar less to keep)
+      const int round = t / G, at = t - round * G;
+      t2 = (round + 1) * G + (round >= 2 ? G - 1 - at : at);
     }
     const bool more = t2 < grid.total;
     Tile ntl = tl;

@@ -200,7 +200,10 @@ def test_row_host_checks(lib):
     assert spread(T=-1) == spread(k=0) == spread(M=-1) == spread(rb=0) == INVALID
     assert spread(rb=40) == MISALIGNED
     assert spread(T=2 ** 31) == spread(M=2 ** 31) == spread(T=2 ** 30, k=2) == spread(rb=2 ** 31 + 16) == UNSUPPORTED
-    assert spread(T=2 ** 26, k=1) == UNSUPPORTED and spread(T=2 ** 26 - 4, k=1, X=0) == INVALID
+    bare = dict(sb=0, slices=0, k=1)
+    assert spread(T=2 ** 26, **bare) == UNSUPPORTED and spread(T=2 ** 26 - 4, X=0, **bare) == INVALID
+    # a quarter of the tokens, and eight workgroups for each 256 of them
+    assert spread(T=2 ** 26 - 4, k=1, X=0) == UNSUPPORTED and spread(T=2 ** 25, k=1, X=0) == INVALID
     assert spread(T=0, M=0) == spread(M=0) == spread(T=0, M=0, X=0, pos=0, out=0, s=0, os=0) == 0
 
     good_c = dict(Y=16, y32=0, pos=32, w=48, out=64, o32=0, T=5, k=2, N=64, M=10)
