@@ -489,7 +489,7 @@ gg_status_t gg_grouped_gemm_mx4_swiglu(const void *Aq, const void *a_scale, cons
  * fp32), ties to even, and the block's scale is 1 / m. A block that holds an
  * infinity or a NaN gets scale NaN and codes 0, and so stands for NaN throughout.
  * K is a multiple of 16, at most GG_MAX_K; rows in [0, 2^31 - 1]; ceil(rows/32) *
- * ceil(K/512) < 2^24 (GG_ERR_UNSUPPORTED beyond; a launch counts its threads in 32
+ * ceil(K/512) < 2^23 (GG_ERR_UNSUPPORTED beyond; a launch counts its threads in 32
  * bits). X, q and scales are 16-byte aligned.
  */
 gg_status_t gg_fp8_quantize(const void *X, void *q, float *scales, int64_t rows, int32_t K,

@@ -28,12 +28,13 @@ __device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t two) {
 __device__ __forceinline__ uint32_t wider(uint32_t two) { return max(two & 0xffffu, two >> 16) << 16; }
 
 // Rows: a wave takes kF8Rows rows x 4 blocks, a block on 16 lanes of 8 values;
-// a workgroup's four waves take rows below each other, so that its scales of one
-// block are 32 rows, a line of memory.
-constexpr int kF8Rows = 8, kF8Cols = 4;
-constexpr int kF8GroupRows = kF8Rows * kF8Threads / kWave;
+// a workgroup's eight waves take rows below each other, so that its scales of one
+// block are 32 rows, a line of memory. (16384 x 6144: 8 rows a wave and four waves
+// 54.6 us, 16 rows 124.)
+constexpr int kF8Rows = 4, kF8Cols = 4, kF8RowThreads = 512;
+constexpr int kF8GroupRows = kF8Rows * kF8RowThreads / kWave;
 
-__global__ __launch_bounds__(kF8Threads) void fp8_rows_kernel(const u32x4 *__restrict__ X,
+__global__ __launch_bounds__(kF8RowThreads) void fp8_rows_kernel(const u32x4 *__restrict__ X,
                                                               u32x2 *__restrict__ q,
                                                               float *__restrict__ scales,
                                                               long long rows, int K, int cols) {
@@ -88,7 +89,8 @@ __global__ __launch_bounds__(kF8Threads) void fp8_weights_kernel(const uint16_t 
   u32x4 v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    v[i] = in ? *(const u32x4 *)(src + (size_t)i * N) : u32x4{0, 0, 0, 0};
+    // (streamed: [64][1024][2688] 98.4 -> 82.4 us)
+    v[i] = in ? __builtin_nontemporal_load((const u32x4 *)(src + (size_t)i * N)) : u32x4{0, 0, 0, 0};
   uint32_t two = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -234,14 +236,14 @@ extern "C" gg_status_t gg_fp8_quantize(const void *X, void *q, float *scales, in
   const long long slices = (K + (long long)kFp8Block - 1) / kFp8Block,
                   cols = (slices + kF8Cols - 1) / kF8Cols;
   const long long groups = (rows + kF8GroupRows - 1) / kF8GroupRows;
-  if (K > GG_MAX_K || rows > INT32_MAX || !launch_fits(groups * cols, kF8Threads))
+  if (K > GG_MAX_K || rows > INT32_MAX || !launch_fits(groups * cols, kF8RowThreads))
     return GG_ERR_UNSUPPORTED;
   if (rows == 0) return GG_OK;
   if (X == nullptr || q == nullptr || scales == nullptr) return GG_ERR_INVALID_VALUE;
   if (!is_aligned(X, 16) || !is_aligned(q, 16) || !is_aligned(scales, 16)) return GG_ERR_MISALIGNED;
   const Span x = span(X, rows, K, 2), c = span(q, rows, K, 1), s = span(scales, slices, rows, 4);
   if (!apart(x, c, s) || !apart(c, s)) return GG_ERR_INVALID_VALUE;
-  return launch(fp8_rows_kernel, dim3((unsigned)(groups * cols)), kF8Threads, 0, stream,
+  return launch(fp8_rows_kernel, dim3((unsigned)(groups * cols)), kF8RowThreads, 0, stream,
                 static_cast<const u32x4 *>(X), static_cast<u32x2 *>(q), scales, (long long)rows, K,
                 (int)cols);
 }

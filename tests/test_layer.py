@@ -162,9 +162,9 @@ def test_quantiser_host_checks(lib):
     assert q(X=24) == q(c=40) == q(s=52) == q(K=40) == MISALIGNED
     assert q(rows=2 ** 31) == q(K=2 ** 22 + 16) == q(rows=2 ** 31 - 1, K=2 ** 22) == UNSUPPORTED
     assert q(rows=0) == q(rows=0, X=0, c=0, s=0) == 0
-    # 2^24 - 1 workgroups of 32 rows x 512 values pass, and meet the next check
-    assert q(rows=32 * (2 ** 24 - 1), K=512, X=0) == INVALID
-    assert q(rows=32 * (2 ** 24 - 1) + 1, K=512, X=0) == UNSUPPORTED
+    # 2^23 - 1 workgroups of 32 rows x 512 values pass, and meet the next check
+    assert q(rows=32 * (2 ** 23 - 1), K=512, X=0) == INVALID
+    assert q(rows=32 * (2 ** 23 - 1) + 1, K=512, X=0) == UNSUPPORTED
 
     def w(B=16, c=32, s=48, g=0, E=2, K=64, N=16):
         return lib.gg_fp8_quantize_weights(B, c, s, g, E, K, N, None)
