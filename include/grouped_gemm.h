@@ -616,6 +616,7 @@ gg_status_t gg_expert_combine(const void *Y, int32_t y_fp32, const int32_t *pos,
  * dO, Y and dY are all fp32 (fp32 != 0) or all bf16. Rows of dY that no choice names
  * are not touched; two choices that name the same row race. Products and sums are
  * in fp32, dY is rounded once, dweights is fp32 [T][k] summed in a fixed order.
+ * N is a multiple of 8, N <= GG_MAX_N, T < 2^24.
  */
 gg_status_t gg_expert_combine_grad(const void *dO, const void *Y, int32_t fp32, const int32_t *pos,
                                    const float *weights, void *dY, float *dweights, int64_t T,
@@ -632,7 +633,8 @@ gg_status_t gg_expert_combine_grad(const void *dO, const void *Y, int32_t fp32, 
  *                X or residual itself, from its start.
  *   norm         bf16 [T][K]: y rounded once; or NULL.
  * K is a multiple of 16, at most 16384; T in [0, 2^24 - 2]; eps >= 0; everything
- * 16-byte aligned.
+ * 16-byte aligned. A row that holds an infinity or a NaN, or zeros alone with eps =
+ * 0, has NaN in the blocks where y is not finite.
  */
 gg_status_t gg_rms_norm_fp8(const void *X, const void *residual, const void *weight, void *q,
                             float *scales, void *sum, void *norm, int64_t T, int32_t K, float eps,

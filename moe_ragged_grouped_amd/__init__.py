@@ -896,6 +896,8 @@ def expert_sort(experts, E: int, weights=None, out=None, stream=None):
     sizes = E | k | n
     if sizes >> 31:
         _int32(what, sizes)
+    if E > MAX_EXPERTS:  # before memory is taken for so many offsets
+        _check(3, what)
     i32 = torch.int32
     if out is None and stream is None:
         new = experts.new_empty
@@ -928,7 +930,8 @@ def expert_spread(X, pos, scale=None, M_cap=None, out=None, out_scale=None, stre
     X: [T, K] of any type whose rows are a multiple of 16 bytes (bf16, fp32, fp8
     or 4-bit codes); pos: int32 [T, k] (expert_sort), entries outside [0, M_cap) are
     skipped; out: optional [M_cap, K] like X (default: M_cap = T*k rows, or M_cap
-    where it is given). Rows that no choice names are left as they were. scale: the
+    where it is given). Rows that no choice names are left as they were; of two
+    choices that name one row either may land. scale: the
     block scales of X, which go with their rows: fp32 [ceil(K/128), T]
     (fp8_quantize, rms_norm_fp8) or uint8 [ceil(K/256), T, 8] (mx4_quantize); then
     (out, out_scale) is returned, out_scale [.., M_cap(, 8)]. The gradient with
@@ -946,6 +949,10 @@ def expert_spread(X, pos, scale=None, M_cap=None, out=None, out_scale=None, stre
     K = X.shape[1]
     _match(what, X.shape[0] == T and (scale is None or scale.shape[1:] == ((T, 8) if sb == 8 else (T,))),
            X, pos, *([] if scale is None else [scale]))
+    row_bytes = K * X.element_size()
+    if scale is not None and scale.shape[0] != -(-row_bytes // _BLOCK):
+        raise ValueError("%s: rows of %d bytes have %d slices of scales, not %d" % (
+            what, row_bytes, -(-row_bytes // _BLOCK), scale.shape[0]))
     if M_cap is None:
         M_cap = T * k if out is None else out.shape[0]
     slices = 0 if scale is None else scale.shape[0]
@@ -958,7 +965,7 @@ def expert_spread(X, pos, scale=None, M_cap=None, out=None, out_scale=None, stre
         s = _out(what, out_scale, (slices, M_cap) + ((8,) if sb == 8 else ()), (scale.dtype,), None, X, stream)
     _call("gg_expert_spread", dev, stream, (X, pos, o, scale, s), X.data_ptr(), pos.data_ptr(), o.data_ptr(),
           None if s is None else scale.data_ptr(), None if s is None else s.data_ptr(), sb if slices else 0, T,
-          k, K * X.element_size(), slices, M_cap)
+          k, row_bytes, slices, M_cap)
     return o if s is None else (o, s)
 
 
@@ -1031,6 +1038,7 @@ def rms_norm_fp8(X, weight, residual=None, eps: float = 1e-6, with_norm: bool = 
     fp8_quantize; sum is z, bf16 [T, K], returned where a residual is given
     (out_sum may be X or residual itself); norm, with with_norm or out_norm, is y
     rounded once to bf16 (a router's input). K is a multiple of 16, at most 16384.
+    What is not finite, and zeros with eps = 0, stands for NaN in its row.
     """
     import torch
     what = "rms_norm_fp8"

@@ -537,13 +537,14 @@ extern "C" gg_status_t gg_expert_spread(const void *X, const int32_t *pos, void 
       (scale_bytes == 0) != (slices == 0))
     return GG_ERR_INVALID_VALUE;
   if (row_bytes % 16 != 0) return GG_ERR_MISALIGNED;
+  if (row_bytes > (1LL << 31)) return GG_ERR_UNSUPPORTED;
   const int V = spread_pieces(T, row_bytes);
   const long long segments = (row_bytes + V * 1024 - 1) / (V * 1024), units = T * segments;
   // (a multiple of the XCDs, so that the same slices stay on one)
   const long long row_groups = (units + kRowWaves - 1) / kRowWaves,
-                  slice_groups = ((slices + kScaleSlices - 1LL) / kScaleSlices + 7) / 8 * 8;
+                  slice_groups = ((slices + (long long)kScaleSlices - 1) / kScaleSlices + 7) / 8 * 8;
   const long long groups = row_groups + (T + kRowThreads - 1) / kRowThreads * slice_groups;
-  if (row_bytes > (1LL << 31) || !launch_fits(groups, kRowThreads)) return GG_ERR_UNSUPPORTED;
+  if (!launch_fits(groups, kRowThreads)) return GG_ERR_UNSUPPORTED;
   if (T > 0 && (X == nullptr || (M_cap > 0 && out == nullptr))) return GG_ERR_INVALID_VALUE;
   if (T > 0 && slices > 0 && (scales == nullptr || (M_cap > 0 && out_scales == nullptr)))
     return GG_ERR_INVALID_VALUE;

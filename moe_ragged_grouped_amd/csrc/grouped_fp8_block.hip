@@ -233,11 +233,11 @@ extern "C" gg_status_t gg_fp8_quantize(const void *X, void *q, float *scales, in
                                        void *stream) {
   if (rows < 0 || K < 1) return GG_ERR_INVALID_VALUE;
   if (K % 16 != 0) return GG_ERR_MISALIGNED;
+  if (K > GG_MAX_K || rows > INT32_MAX) return GG_ERR_UNSUPPORTED;
   const long long slices = (K + (long long)kFp8Block - 1) / kFp8Block,
                   cols = (slices + kF8Cols - 1) / kF8Cols;
   const long long groups = (rows + kF8GroupRows - 1) / kF8GroupRows;
-  if (K > GG_MAX_K || rows > INT32_MAX || !launch_fits(groups * cols, kF8RowThreads))
-    return GG_ERR_UNSUPPORTED;
+  if (!launch_fits(groups * cols, kF8RowThreads)) return GG_ERR_UNSUPPORTED;
   if (rows == 0) return GG_OK;
   if (X == nullptr || q == nullptr || scales == nullptr) return GG_ERR_INVALID_VALUE;
   if (!is_aligned(X, 16) || !is_aligned(q, 16) || !is_aligned(scales, 16)) return GG_ERR_MISALIGNED;

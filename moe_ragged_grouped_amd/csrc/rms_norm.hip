@@ -250,7 +250,9 @@ static int grad_groups(long long T, int K) {
 static gg_status_t check_norm(int64_t T, int K, float eps) {
   if (T < 0 || K < 1 || !(eps >= 0.0f)) return GG_ERR_INVALID_VALUE;
   if (K % 16 != 0) return GG_ERR_MISALIGNED;
-  if (K > kNormMost || T > INT32_MAX) return GG_ERR_UNSUPPORTED;
+  // (a launch counts its threads, two rows to 512, in 32 bits)
+  if (K > kNormMost || T > INT32_MAX || !launch_fits((T + kNormRows - 1) / kNormRows, kNormThreads))
+    return GG_ERR_UNSUPPORTED;
   return GG_OK;
 }
 
@@ -264,7 +266,6 @@ extern "C" gg_status_t gg_rms_norm_fp8(const void *X, const void *residual, cons
   gg_status_t st = check_norm(T, K, eps);
   if (st != GG_OK) return st;
   const long long groups = (T + kNormRows - 1) / kNormRows;
-  if (!launch_fits(groups, kNormThreads)) return GG_ERR_UNSUPPORTED;
   if (sum != nullptr && residual == nullptr) return GG_ERR_INVALID_VALUE;
   if (T == 0) return GG_OK;
   if (X == nullptr || weight == nullptr || q == nullptr || scales == nullptr) return GG_ERR_INVALID_VALUE;

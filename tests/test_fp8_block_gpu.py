@@ -211,6 +211,31 @@ def test_many_tiles_a_workgroup(gg):
     assert (ops.host(gg.grouped_gemm_fp8_block(*_dev(args))) == ref.fp8_product(*args, bounds=False)[0]).all()
 
 
+@pytest.mark.parametrize("sizes", [[256] * 100 + [1], [700] * 24 + [100] * 60 + [30] * 50, [64] * 300])
+def test_rounds_of_tiles(gg, sizes):
+    # three and more rounds of tiles on every workgroup, in one height and mixed: a tile's first
+    # slice comes in behind the stores of the one before. One to eight slices, every output.
+    rng = np.random.default_rng(len(sizes))
+    N, M = 2056, sum(sizes)
+    for K in (112, 256, 384, 1024):
+        args = _dev(_exact_operands(rng, sizes, K, N))
+        block, band = torch.arange(K, device=DEV) // 128, torch.arange(N, device=DEV) // 128
+        a = args[0].view(F8).double() * args[1].t().double()[:, block]
+        C, at = torch.empty(M, N, dtype=torch.float64, device=DEV), 0
+        for e, m in enumerate(sizes):
+            b = args[2][e].view(F8).double() * args[3][e].double()[band][:, block]
+            C[at:at + m] = a[at:at + m] @ b.t()
+            at += m
+        for _ in range(3):
+            assert torch.equal(gg.grouped_gemm_fp8_block(*args).double(), C), K
+            assert torch.equal(gg.grouped_gemm_fp8_block(*args, out_dtype=torch.bfloat16), C.bfloat16()), K
+            # the activation in fp32 is off by at most (|gate| + 3.5) 2^-23, then rounded to bf16
+            gate, up = C[:, 0::2], C[:, 1::2]
+            want = gate * torch.sigmoid(gate) * up
+            off = (gg.grouped_gemm_fp8_block_swiglu(*args).double() - want).abs()
+            assert (off <= (2.0 ** -8 + (gate.abs() + 4) * 2.0 ** -22) * want.abs() + 2.0 ** -100 * up.abs()).all(), K
+
+
 def test_scales_are_any_numbers(gg):
     # 0, negative, subnormal-making and large ones; a NaN stays in its row or its 128 columns
     rng = np.random.default_rng(12)

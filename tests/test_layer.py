@@ -240,7 +240,8 @@ def test_norm_host_checks(lib):
     assert norm(res=0) == INVALID, "a sum of nothing"
     assert norm(T=-1) == norm(K=0) == norm(eps=-1.0) == norm(eps=float("nan")) == INVALID
     assert norm(K=40) == MISALIGNED
-    assert norm(K=16400) == norm(T=2 ** 31) == UNSUPPORTED
+    assert norm(K=16400) == norm(T=2 ** 31) == norm(T=2 ** 24 - 1) == UNSUPPORTED
+    assert norm(T=2 ** 24 - 2, X=0) == INVALID
     assert norm(T=0) == norm(T=0, X=0, res=0, q=0, s=0, sum=0, norm=0) == 0
     good_g = dict(dy=16, z=32, g=48, res=64, dz=80, dg=96, ws=112, T=5, K=64, eps=1e-6)
 
@@ -252,7 +253,7 @@ def test_norm_host_checks(lib):
         if n not in ("T", "K", "eps"):
             assert grad(**{n: good_g[n] + 8}) == MISALIGNED, n
     assert grad(T=-1) == grad(K=0) == grad(eps=-1.0) == INVALID
-    assert grad(K=40) == MISALIGNED and grad(K=16400) == grad(T=2 ** 31) == UNSUPPORTED
+    assert grad(K=40) == MISALIGNED and grad(K=16400) == grad(T=2 ** 31) == grad(T=2 ** 24 - 1) == UNSUPPORTED
     need = lib.gg_rms_norm_grad_workspace
     assert need(0, 64) == need(5, 16400) == 0 and need(3, 64) > 0 and need(10 ** 6, 64) % 16 == 0
 
@@ -339,6 +340,8 @@ def _dev(kind, *shape):
     lambda t: gg.expert_spread(t("bf", 5, 32), t("i", 4, 2)),
     lambda t: gg.expert_spread(t("f8", 4, 32), t("i", 4, 2), scale=t("f", 1, 5)),
     lambda t: gg.expert_spread(t("f8", 4, 32), t("i", 4, 2), scale=t("u8", 1, 4)),
+    lambda t: gg.expert_spread(t("f8", 4, 144), t("i", 4, 2), scale=t("f", 1, 4)),
+    lambda t: gg.expert_spread(t("f8", 4, 128), t("i", 4, 2), scale=t("f", 2, 4)),
     lambda t: gg.expert_spread(t("bf", 4, 32), t("i", 4, 2), out=t("f", 8, 32)),
     lambda t: gg.expert_combine(t("h", 8, 32), t("i", 4, 2)),
     lambda t: gg.expert_combine(t("bf", 8, 32), t("i", 4, 2), weights=t("f", 8)),
@@ -381,6 +384,7 @@ def test_host_tensors_and_strides_are_refused(lib):
                                                t("f", 2, -(-BIG // 128), 1), t("i", 3)),
     lambda t: gg.expert_sort(t("i", BIG // 2, 2), 3),
     lambda t: gg.expert_sort(t("i", 4, 2), 2 ** 32 + 4),
+    lambda t: gg.expert_sort(t("i", 4, 2), 2 ** 30),
     lambda t: gg.expert_spread(t("bf", BIG, 8), t("i", BIG, 1)),
     lambda t: gg.expert_spread(t("bf", 4, 8), t("i", 4, 1), M_cap=BIG),
     lambda t: gg.expert_combine(t("bf", BIG, 8), t("i", 4, 1)),
