@@ -20,10 +20,26 @@ constexpr int kNormWaves = 4, kNormRows = 2;
 constexpr int kNormThreads = kNormWaves * kNormRows * kWave;
 constexpr int kNormPiece = kNormWaves * kWave * 8;  // values of a row at one time
 
-__device__ __forceinline__ float sum_of_wave(float v) {
+template <class T>
+__device__ __forceinline__ T sum_of_wave(T v) {
 #pragma unroll
   for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d, kWave);
   return v;
+}
+
+// The multiplier of a block whose largest magnitude is t * r, t an fp32 number
+// (z g is exact: 16 bits) and r a 64-bit one. It is cut to 16 bits, so where 448 /
+// (t r) is next to such a number the last bits of r decide on a whole block: the
+// one found in fp32 is put right by comparing in 64 bits. (With r in fp32 a
+// quarter percent of the blocks came out one step off, which made nearly all of
+// the codes that differ from the formula's.)
+__device__ __forceinline__ float norm_multiplier(uint32_t t, float r, double rd) {
+  const float m = fp8_multiplier(__builtin_bit_cast(uint32_t, __builtin_bit_cast(float, t) * r));
+  if (m == 0.0f) return m;
+  const double top = fmax((double)__builtin_bit_cast(float, t) * rd, 0x1p-100);
+  const uint32_t bits = __builtin_bit_cast(uint32_t, m);
+  const float up = __builtin_bit_cast(float, bits + 0x100u), down = __builtin_bit_cast(float, bits - 0x100u);
+  return (double)m * top > (double)kFp8Max ? down : (double)up * top <= (double)kFp8Max ? up : m;
 }
 
 struct NormParams {
@@ -38,14 +54,13 @@ struct NormParams {
 
 template <int V>
 __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormParams p) {
-  __shared__ float sums[kNormRows][kNormWaves];
+  __shared__ double sums[kNormRows][kNormWaves];
   const int tid = threadIdx.x, lane = tid % kWave, wave = scalar(tid / kWave);
   const int row = wave / kNormWaves, part = wave % kNormWaves;
   const int t = blockIdx.x * kNormRows + row, pitch = p.K / 8;
   const bool live = t < p.T;
   const size_t base = (size_t)t * pitch;
   u32x4 z[V];
-  float sq = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (i * kNormWaves + part) * kWave + lane;
@@ -67,20 +82,26 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormParams p) {
       if (p.sum != nullptr) st_rows(p.sum + base + c, s, p.stream);
     }
   }
+  // eight squares in fp32, the rest in 64 bits
+  double sq = 0.0;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
+    float few = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      sq = __builtin_fmaf(bf16_lo(z[i][j]), bf16_lo(z[i][j]), sq);
-      sq = __builtin_fmaf(bf16_hi(z[i][j]), bf16_hi(z[i][j]), sq);
+      few = __builtin_fmaf(bf16_lo(z[i][j]), bf16_lo(z[i][j]), few);
+      few = __builtin_fmaf(bf16_hi(z[i][j]), bf16_hi(z[i][j]), few);
     }
+    sq += (double)few;
+  }
   sq = sum_of_wave(sq);
   if (lane == 0) sums[row][part] = sq;
   __syncthreads();
-  sq = 0.0f;
+  sq = 0.0;
 #pragma unroll
   for (int w = 0; w < kNormWaves; ++w) sq += sums[row][w];
-  const float r = 1.0f / sqrtf(sq / (float)p.K + p.eps);
+  const double rd = 1.0 / sqrt(sq / p.K + (double)p.eps);
+  const float r = (float)rd;
   if (!live) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -93,10 +114,12 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormParams p) {
     for (int j = 0; j < 8; ++j) {
       const float zj = j % 2 ? bf16_hi(z[i][j / 2]) : bf16_lo(z[i][j / 2]);
       const float gj = j % 2 ? bf16_hi(g[j / 2]) : bf16_lo(g[j / 2]);
-      v[j] = zj * gj * r;  // z g is exact: 16 bits
+      v[j] = zj * gj;
       top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
     }
-    const float m = fp8_multiplier(row16_max(top));
+    const float m = norm_multiplier(row16_max(top), r, rd);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= r;
     if (!in) continue;
     if (p.y != nullptr) {
       const u32x2 a = pack_bf16(f32x4{v[0], v[1], v[2], v[3]}),
