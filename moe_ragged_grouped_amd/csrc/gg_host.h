@@ -39,12 +39,13 @@ inline gg_status_t launch(void (*kernel)(P...), dim3 grid, int threads, int lds,
   return GG_ERR_LAUNCH;
 }
 
-// Outputs of this many bytes are stored as streaming data: the L2s (32 MB) hold
-// no such array until the next call reads it, and what they do hold stays there.
-// Measured (us, without / with): 2048 x 8 rows of 6144 combined 43.0 / 41.7, the
-// gradient 90.2 / 87.8; the norm of 16384 x 6144 128.1 / 123.2, its gradient (8191)
-// 89.2 / 86.8.
-inline bool streams(long long bytes) { return bytes >= (64LL << 20); }
+// Outputs of this many bytes are stored as streaming data: half of what the L2s
+// hold (32 MB), each of which keeps what its own XCD wrote and the next call may
+// read on another. Measured (us, without / with): 2048 x 8 rows of 6144 combined
+// (25 MB) 46.9 / 41.7, the gradient 90.2 / 87.8; the norm of 16384 x 6144 128.1 /
+// 123.2, its gradient (8191) 89.2 / 86.8; weights [64][1024][2688] to 8 bits 92.1 /
+// 84.6.
+inline bool streams(long long bytes) { return bytes >= (16LL << 20); }
 
 inline bool valid_bm(int bm) {
   return bm == 0 || bm == 16 || bm == 32 || bm == 64 || bm == 128 || bm == 256;

@@ -76,7 +76,8 @@ template <bool TURN>
 __global__ __launch_bounds__(kF8Threads) void fp8_weights_kernel(const uint16_t *__restrict__ B,
                                                                  uint8_t *__restrict__ q,
                                                                  float *__restrict__ scales, int K,
-                                                                 int N, int kblocks, int nblocks) {
+                                                                 int N, int kblocks, int nblocks,
+                                                                 bool stream) {
   __shared__ __attribute__((aligned(16))) uint8_t codes[TURN ? kF8Tile * kF8Tile : 16];
   __shared__ uint32_t tops[kF8Threads / kWave];
   const uint32_t at = blockIdx.x / (uint32_t)nblocks;
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(kF8Threads) void fp8_weights_kernel(const uint16_t 
                  fp8_quad(bf16_lo(v[i].z) * m, bf16_hi(v[i].z) * m, bf16_lo(v[i].w) * m,
                           bf16_hi(v[i].w) * m)};
       if (m == 0.0f) o = u32x2{0, 0};
-      *(u32x2 *)(q + ((size_t)e * K + k0 + i) * N + n) = o;
+      st_rows((u32x2 *)(q + ((size_t)e * K + k0 + i) * N + n), o, stream);
     }
   } else {
     // the eight codes of column 8 c + j at 8-byte chunk g ^ c of its row, so that
@@ -132,7 +133,8 @@ __global__ __launch_bounds__(kF8Threads) void fp8_weights_kernel(const uint16_t 
       const u32x4 w = *(const u32x4 *)(codes + col * kF8Tile + 16 * (piece ^ (x / 2)));
       const int nn = nb * kF8Tile + col, k = kb * kF8Tile + 16 * piece;
       if (nn < N && k < K)  // K is a multiple of 16
-        *(u32x4 *)(q + ((size_t)e * N + nn) * K + k) = x % 2 ? u32x4{w.z, w.w, w.x, w.y} : w;
+        st_rows((u32x4 *)(q + ((size_t)e * N + nn) * K + k), x % 2 ? u32x4{w.z, w.w, w.x, w.y} : w,
+                stream);
     }
   }
 }
@@ -266,7 +268,8 @@ extern "C" gg_status_t gg_fp8_quantize_weights(const void *B, void *q, float *sc
   if (!apart(b, c, s) || !apart(c, s)) return GG_ERR_INVALID_VALUE;
   return launch(for_grad ? fp8_weights_kernel<false> : fp8_weights_kernel<true>,
                 dim3((unsigned)(kb * nb * E)), kF8Threads, 0, stream, static_cast<const uint16_t *>(B),
-                static_cast<uint8_t *>(q), scales, K, N, (int)kb, (int)nb);
+                static_cast<uint8_t *>(q), scales, K, N, (int)kb, (int)nb,
+                streams((long long)E * K * N));
 }
 
 extern "C" gg_status_t gg_grouped_gemm_fp8_block(const void *Aq, const float *a_scale, const void *Bq,
