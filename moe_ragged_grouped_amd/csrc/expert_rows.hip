@@ -1,6 +1,11 @@
 // Tokens' rows to their experts and back, for gfx950: the stable sort of the
 // choices by expert, the rows moved to their groups, the weighted sum of a
 // token's rows, and its gradient.
+//
+// All of them move bytes. 2048 tokens of 8 choices, rows of 6144 bf16: spread 34 us
+// for 226 MB (6.6 TB/s), combine 42 for 227 (5.4), gradient 87 for 428 (4.9, half
+// of it writes). The sort moves little and waits: 64 x 8 choices 4 us, 16384 x 8 in
+// two launches 8, each launch's start and its round trips to memory.
 
 #include "gg_common.h"
 #include "gg_fp8.h"

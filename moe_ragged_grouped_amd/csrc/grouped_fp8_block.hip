@@ -5,6 +5,14 @@
 // Row scales lie slice by slice, scales[k / 128][row], so that those of a
 // tile's rows in one slice are one run of memory; weights are kept with their
 // output columns as rows, codes [E][N][K] and scales [E][N / 128][K / 128].
+//
+// What bounds them. The quantisers move bytes: rows 16384 x 6144 54 us (5.6 TB/s),
+// weights [64][1024][2688] 85 us (6.2). The product of 32 experts x 16 rows, K =
+// 6144, N = 4096: 125 us for 813 MB (6.5 TB/s), the weights' bytes. 64 experts,
+// 16384 skewed rows, K = 1024, N = 2688 with SwiGLU: 84 us for 237 MB and 90 GFLOP;
+// eight slices a tile at 2.0 us each (0.85 of it on the matrix cores), a tile's
+// start and its epilogue not covered by products. One row on each of 8 experts: 9.8
+// us, 6 of launch, schedule and first loads.
 
 #include "gg_common.h"
 #include "gg_fp8.h"
