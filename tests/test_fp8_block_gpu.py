@@ -181,13 +181,10 @@ def _exact_operands(rng, sizes, K, N, extra=0):
             ops.offsets_of(sizes))
 
 
-@pytest.mark.parametrize("width", [64, 128, 256])
-@pytest.mark.parametrize("bm", BMS[1:])
+@pytest.mark.parametrize("bm,width", [(b, w) for b in BMS[1:] for w in (64, 128, 256) if b > 16 or w > 64])
 def test_every_tile_exactly(gg, bm, width):
     # each height by its argument, each width by the number of tiles, K below, at and past the
-    # ring's stages, and several tiles a workgroup
-    if bm == 16 and width == 64:
-        pytest.skip("64 columns need 32 rows")
+    # ring's stages (64 columns need 32 rows)
     rng = np.random.default_rng(bm + width)
     for E, N in ((1, 264), (24, 264), (24, 1288), (28, 2056), (60, 264)):
         sizes = [int(m) for m in rng.integers(bm // 2 + 1, bm + 1, E)]
