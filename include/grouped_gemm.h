@@ -652,6 +652,9 @@ gg_status_t gg_rms_norm_fp8(const void *X, const void *residual, const void *wei
  *            K fix (no atomics).
  *   workspace  gg_rms_norm_grad_workspace(T, K) bytes of device memory, used during
  *            the call only.
+ * Rows, gradients and weights may lie anywhere in bf16's range: squares, products and
+ * powers of r that leave fp32 do no harm where the results do not (z * r is an fp32
+ * number).
  * Sizes and alignment are those of gg_rms_norm_fp8.
  */
 int64_t gg_rms_norm_grad_workspace(int64_t T, int32_t K);

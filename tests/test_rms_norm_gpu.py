@@ -149,3 +149,71 @@ def test_rows_past_2_to_the_32_bytes(gg):
     w, wg, err, mags = ref.norm_grad(oracle._bf16_to_f64(res), oracle._bf16_to_f64(x), oracle._bf16_to_f64(g), None, 1e-6)
     ops.check_bf16(ops.host(dz[pick]), w, err, "dz")
     ops.check_f32(ops.host(dg), wg, ref.NORM_DG_REL * mags, "dg")
+
+
+# powers of two that rows lie at: their squares, and the cube of 1 / rms, leave fp32 on both sides
+FAR = [-120, -100, -70, -45, -13, 0, 20, 47, 50, 70, 100, 118]
+
+
+def _far(rng, K, g_powers=(0,)):
+    """Rows near 2^FAR and a weight near the given powers of two, column by column."""
+    x = rng.standard_normal((len(FAR), K)) * np.exp2(FAR)[:, None]
+    g = (1 + 0.2 * rng.standard_normal(K)) * np.exp2(rng.choice(g_powers, K))
+    return wl.f32_to_bf16_bits(x.astype(np.float32)), wl.f32_to_bf16_bits(g.astype(np.float32))
+
+
+@pytest.mark.parametrize("g_powers", [(0,), (-40, 0), (50, 20)])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+@pytest.mark.parametrize("K", [272, 6144, 8208])
+def test_gradient_of_rows_far_from_one(gg, K, eps, g_powers):
+    # dY about as far out as the rows' root mean square: the gradient is near the weight whatever the row,
+    # while dY * weight, its products with Z, Z's squares and r^3 are not
+    rng = np.random.default_rng(K + len(g_powers))
+    z, g = _far(rng, K, g_powers)
+    rms = np.log2(np.sqrt(np.exp2(2.0 * np.array(FAR)) + eps))
+    out = np.clip(rms, -100, 90)
+    dy, res = (wl.f32_to_bf16_bits((rng.standard_normal((len(FAR), K)) * np.exp2(p)[:, None]).astype(np.float32))
+               for p in (out, out - rms))
+    Z, W, D, R = (oracle._bf16_to_f64(a) for a in (z, g, dy, res))
+    for r in (None, R):
+        want, dg, err, mags = ref.norm_grad(D, Z, W, r, eps)
+        dz, dw = gg.rms_norm_grad(ops.to_dev(dy), ops.to_dev(z), ops.to_dev(g), eps=eps,
+                                  d_residual=None if r is None else ops.to_dev(res))
+        for t in range(len(FAR)):
+            ops.check_bf16(ops.host(dz[t]), want[t], err[t], "dz of a row at 2^%d" % FAR[t])
+        ops.check_f32(ops.host(dw), dg, ref.NORM_DG_REL * mags, "dg")
+    # a row at a time, so that none hides behind the largest one's share of dg
+    for t in range(len(FAR)):
+        _, dg, _, mags = ref.norm_grad(D[t:t + 1], Z[t:t + 1], W, None, eps)
+        if mags[mags > 0].min() < 2.0 ** -120:
+            continue  # (eps outweighs the row: no normal fp32 numbers)
+        dw = gg.rms_norm_grad(ops.to_dev(dy[t:t + 1]), ops.to_dev(z[t:t + 1]), ops.to_dev(g), eps=eps)[1]
+        ops.check_f32(ops.host(dw), dg, ref.NORM_DG_REL * mags, "dg of a row at 2^%d" % FAR[t])
+
+
+@pytest.mark.parametrize("K", [144, 2064, 8208])
+def test_gradient_where_rows_begin_to_be_far(gg, K):
+    # rows and gradients on both sides of the powers of two up to which a row's sums are taken in
+    # fp32, half of dY zeros, and a row without any gradient
+    rng = np.random.default_rng(K)
+    rows = [(z, d) for z in (-22, -21, -20, -19, -10, 0, 19, 20, 21) for d in (-118, -100, -90, -82, -60, 0, 55, 62)
+            if d - z >= -100] + [(0, None)]
+    z = wl.f32_to_bf16_bits((rng.standard_normal((len(rows), K)) * np.exp2([[p] for p, _ in rows])).astype(np.float32))
+    g = wl.f32_to_bf16_bits((1 + 0.2 * rng.standard_normal(K)).astype(np.float32))
+    dy = rng.standard_normal((len(rows), K)) * [[0 if p is None else 2.0 ** p] for _, p in rows] * rng.integers(0, 2, (len(rows), K))
+    dy = wl.f32_to_bf16_bits(dy.astype(np.float32))
+    Z, W, D = (oracle._bf16_to_f64(a) for a in (z, g, dy))
+    want, dg, err, mags = ref.norm_grad(D, Z, W, None, 0.0)
+    dz, dw = gg.rms_norm_grad(ops.to_dev(dy), ops.to_dev(z), ops.to_dev(g), eps=0.0)
+    for t, row in enumerate(rows):
+        ops.check_bf16(ops.host(dz[t]), want[t], err[t], "dz of %s" % (row,))
+    ops.check_f32(ops.host(dw), dg, ref.NORM_DG_REL * mags, "dg")
+
+
+def test_gradient_of_zeros_without_eps_is_nan(gg):
+    z = torch.zeros((2, 272), dtype=torch.bfloat16, device=DEV)
+    z[1] = 2.0 ** -100
+    dy, w = torch.ones_like(z), torch.ones(272, dtype=torch.bfloat16, device=DEV)
+    dz, dg = gg.rms_norm_grad(dy, z, w, eps=0.0)
+    assert dz[0].isnan().all() and dg.isnan().all()
+    assert (dz[1].abs() <= 2.0 ** 100 * 2.0 ** -14).all()  # 2^100 (1 - 1): what fp32 leaves of it
