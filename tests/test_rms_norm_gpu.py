@@ -217,3 +217,60 @@ def test_gradient_of_zeros_without_eps_is_nan(gg):
     dz, dg = gg.rms_norm_grad(dy, z, w, eps=0.0)
     assert dz[0].isnan().all() and dg.isnan().all()
     assert (dz[1].abs() <= 2.0 ** 100 * 2.0 ** -14).all()  # 2^100 (1 - 1): what fp32 leaves of it
+
+
+@pytest.mark.parametrize("g_powers", [(0,), (-60, 0), (70, 20)])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+@pytest.mark.parametrize("K", [272, 6144, 8208, 16384])
+def test_norm_of_rows_far_from_one(gg, K, eps, g_powers):
+    # squares that leave fp32 on both sides, 1 / rms near its ends, and z * weight beyond them
+    rng = np.random.default_rng(K + 3 * len(g_powers))
+    x, g = _far(rng, K, g_powers)
+    res = wl.f32_to_bf16_bits((rng.standard_normal(x.shape) * np.exp2(FAR)[:, None]).astype(np.float32))
+    X, R, W = (oracle._bf16_to_f64(a) for a in (x, res, g))
+    for residual in (None, R):
+        z, y = ref.norm(X, residual, W, eps)
+        got = gg.rms_norm_fp8(ops.to_dev(x), ops.to_dev(g), residual=None if residual is None else ops.to_dev(res),
+                              eps=eps, with_norm=True)
+        if residual is not None:
+            assert np.array_equal(ops.host(got[2]), z)
+        q, s, norm = got[0].view(torch.uint8).cpu().numpy(), ops.host(got[1]), ops.host(got[-1])
+        assert np.isfinite(s).all()
+        for t in range(len(FAR)):
+            check_fp8(q[t:t + 1], s[:, t:t + 1], y[t:t + 1], ref.NORM_REL)
+            # (half a step of a subnormal bf16 number besides, where eps outweighs a row by far)
+            ops.check_bf16(norm[t], y[t], ref.NORM_REL * np.abs(y[t]) + 2.0 ** -134, "norm of a row at 2^%d" % FAR[t])
+
+
+@pytest.mark.parametrize("K", [144, 2064, 16384])
+def test_norm_where_a_product_with_the_weight_leaves_fp32(gg, K):
+    # ordinary rows but for a few values and weights so far out that their product is subnormal or
+    # beyond fp32 while the normalised value is neither
+    rng = np.random.default_rng(K + 1)
+    x, _, g = _inputs(rng, 9, K)
+    X, W = oracle._bf16_to_f64(x), oracle._bf16_to_f64(g)
+    for row, (scale, value, weight) in enumerate([(2.0 ** 40, 2.0 ** 41, 2.0 ** 90), (2.0 ** -40, 2.0 ** -41, 2.0 ** -90),
+                                                  (2.0 ** -30, 2.0 ** -60, 2.0 ** -75), (1.0, 2.0 ** -100, 2.0 ** -20)]):
+        at = int(rng.integers(0, K))
+        X[row] *= scale
+        X[row, at] = value
+        W[at] = weight
+    X[5, ::2] = 0.0
+    X[6] = 0.0
+    X[7, : K // 2] = 0.0
+    x, g = wl.f32_to_bf16_bits(X.astype(np.float32)), wl.f32_to_bf16_bits(W.astype(np.float32))
+    _, y = ref.norm(oracle._bf16_to_f64(x), None, oracle._bf16_to_f64(g), 1e-30)
+    q, s, norm = gg.rms_norm_fp8(ops.to_dev(x), ops.to_dev(g), eps=1e-30, with_norm=True)
+    check_fp8(q.view(torch.uint8).cpu().numpy(), ops.host(s), y, ref.NORM_REL)
+    ops.check_bf16(ops.host(norm), y, ref.NORM_REL * np.abs(y) + 2.0 ** -134, "norm")
+
+
+def test_norm_of_zeros_without_eps_is_nan(gg):
+    x = torch.zeros((3, 272), dtype=torch.bfloat16, device=DEV)
+    x[1], x[2] = 2.0 ** -120, -2.0 ** 120
+    q, s, y = gg.rms_norm_fp8(x, torch.ones(272, dtype=torch.bfloat16, device=DEV), eps=0.0, with_norm=True)
+    assert s[:, 0].isnan().all() and (q[0].view(torch.uint8) == 0).all() and y[0].isnan().all()
+    assert (y[1] == 1).all() and (y[2] == -1).all() and (s[:, 1:] == np.float32(1 / 448)).all()
+    # eps alone decides: r = 0, and everything finite is 0
+    q, s, y = gg.rms_norm_fp8(x, torch.full((272,), 2.0 ** 100, dtype=torch.bfloat16, device=DEV), eps=float("inf"), with_norm=True)
+    assert (y == 0).all() and (s == np.float32(2.0 ** -100 / 448)).all()
