@@ -834,7 +834,8 @@ def grouped_gemm_fp8_block(Aq, a_scale, Bq, b_scale, offsets, out=None, bm: int 
     Aq, a_scale: E4M3 codes [M_cap, K] (float8_e4m3fn or uint8) and fp32 scales
     [ceil(K/128), M_cap], one for 128 values of a row (fp8_quantize); Bq, b_scale:
     codes [E, N, K] and scales [E, ceil(N/128), ceil(K/128)], one for 128 x 128
-    values (fp8_quantize_weights; any fp32 numbers). offsets int32 [E+1]; out:
+    values (fp8_quantize_weights). The scales are any fp32 numbers; where the product
+    of two is below fp32's normal numbers, the block's part is off by up to 2^-125. offsets int32 [E+1]; out:
     optional fp32 or bf16 [M_cap, N] (out_dtype when out is not given, default
     fp32; bf16 is the fp32 result rounded to nearest even). K is a multiple of 16,
     N of 8. Rows at or past offsets[E] are left as they were. bm and stream as in

@@ -668,6 +668,54 @@ __device__ __forceinline__ void ring_mma_fp8(f32x4 (&acc)[C::NI][C::MI], const l
   static_for<L>([&](auto jc) { add(std::integral_constant<int, P - L + decltype(jc)::value>{}); });
 }
 
+// An fp32 scale as its power of two (of a subnormal number -127) and the rest.
+struct ScaleParts {
+  int power;
+  float rest;
+  __device__ __forceinline__ explicit ScaleParts(float s) {
+    power = min((int)(__builtin_bit_cast(uint32_t, s) >> 23 & 255), 254) - 127;  // (infinity, NaN: the rest)
+    rest = __builtin_ldexpf(s, -power);
+  }
+};
+
+// 8 bits: row block mi anew, from memory, with the scales' powers of two applied apart
+// from their product: a block's sum is a multiple of 2^-18 and at most 2^25, so times
+// 2^-100 .. 2^100 it is exact. What is left of the power beyond that goes to the product
+// of the rests, up to 2^+-120, where the result is infinite or 0 anyway.
+template <class C>
+__device__ __forceinline__ void ring_block_apart(f32x4 (&acc)[C::NI][C::MI], int mi, const RingTile &t,
+                                                 cst_f32 *columns, int wm0, int wn0, int lane) {
+  const int g = lane / 16, s = lane % 16, KT = ring_slices(t);
+  auto read = [&](const char *base, int rows, int r, int k) {
+    const buf_rsrc b = ring_rows(base, rows, t, k);
+    auto piece = [&](uint32_t at) {
+      return ld_buf16(b, at < t.pitch - (uint32_t)k * kRowBytes ? (uint32_t)r * t.pitch + at : kOob, 0);
+    };
+    return __builtin_bit_cast(ring_i32x8, __builtin_shufflevector(piece(16u * g), piece(64u + 16u * g),
+                                                                  0, 1, 2, 3, 4, 5, 6, 7));
+  };
+#pragma unroll
+  for (int ni = 0; ni < C::NI; ++ni) acc[ni][mi] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k = 0; k < KT; ++k) {
+    const int r = wm0 + mi * 16 + s;
+    const buf_rsrc rs = make_buf(t.As + (uint64_t)k * t.as_step, 4u * (uint32_t)t.rows);
+    const ScaleParts row(__builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * r, 0, 0))),
+        column(columns[k]);
+    const int power = row.power + column.power, at_once = min(max(power, -100), 100);
+    const float first = __builtin_ldexpf(1.0f, at_once),
+                rest = __builtin_ldexpf(row.rest * column.rest, min(max(power - at_once, -120), 120));
+    const ring_i32x8 y = read(t.A, t.rows, r, k);
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ++ni) {
+      const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          read(t.B, t.ncols, wn0 + ni * 16 + s, k), y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[ni][mi][j] = __builtin_fmaf(d[j] * first, rest, acc[ni][mi][j]);
+    }
+  }
+}
+
 // One step: multiply slice k out of its stage (a_cur and b_cur, both its
 // start) and meanwhile refill the stage that slice k - 1 left: a_nxt is that
 // stage, b_nxt too, or with EARLY_B the present one, whose weights are read
@@ -755,12 +803,20 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
   wait_loads<0>();
   wg_barrier();
   epi.begin();
+  // 8 bits: where the product of a row's and the columns' scale passed fp32, all that this
+  // wave has of the row is infinite or (for sums of 0) NaN, one value as good as another.
+  auto store = [&](int mi) {
+    if constexpr (C::FP8)
+      if (__ballot(!(fabsf(acc[0][mi].x) < INFINITY)) != 0)
+        ring_block_apart<C>(acc, mi, t, columns, wm0, wn0, lane);
+    epi.block(acc, mi);
+  };
   // Row block mi is final. The empty asm keeps its products ahead of the
   // epilogue's branches (the compiler would move them into those).
   auto final_block = [&](int mi) {
 #pragma unroll
     for (int ni = 0; ni < C::NI; ++ni) asm volatile("" : "+v"(acc[ni][mi]));
-    if constexpr (C::MI <= 4) epi.block(acc, mi);
+    if constexpr (C::MI <= 4) store(mi);
   };
   const lds_u8 *const last = lds + cur * C::STAGE;
   auto none = [](auto) {};
@@ -773,7 +829,7 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
   if constexpr (C::MI > 4) {
 #pragma unroll
     for (int mi = 0; mi < C::MI; ++mi) {
-      epi.block(acc, mi);
+      store(mi);
       __builtin_amdgcn_sched_barrier(0);
     }
   }

@@ -249,6 +249,72 @@ def test_scales_are_any_numbers(gg):
     assert (np.abs(got - C)[~nan] <= 2.0 ** -23 * np.abs(C)[~nan]).all()
 
 
+# pairs of a row's and of the columns' scales: finite each, their product beyond fp32 or below its
+# normal numbers, and the results of the codes' sums not
+LARGE = [(2.0 ** 70, 2.0 ** 70), (1.37 * 2.0 ** 100, -1.2 * 2.0 ** 39), (1.9 * 2.0 ** 127, 1.1 * 2.0 ** 12), (-2.0 ** 13, 2.0 ** 127)]
+SMALL = [(1.37 * 2.0 ** -75, 1.6 * 2.0 ** -74), (-1.1 * 2.0 ** -126, 1.3 * 2.0 ** -22), (1.2 * 2.0 ** -20, 1.7 * 2.0 ** -126),
+         (2.0 ** -140, 1.4 * 2.0 ** -5), (1.5 * 2.0 ** -10, 2.0 ** -135), (2.0 ** -108, 2.0 ** -100)]
+
+
+@pytest.mark.parametrize("bm", BMS)
+@pytest.mark.parametrize("N", [264, 1288])
+def test_scales_whose_product_is_beyond_fp32(gg, N, bm):
+    # a first block of the least codes, zeros in a third of the rows and columns, at such scales, then
+    # ordinary ones: the sums of 0 have to add 0, the others what the scales make of them
+    rng = np.random.default_rng(N + bm)
+    E, m, K = len(LARGE), 150, 400
+    a, b = (rng.integers(-3, 4, shape).astype(np.float64) for shape in ((E * m, K), (E, N, K)))
+    a[:, :128], b[:, :, :128] = 0, 0
+    a[:, 5:9], b[:, :, 3:12] = (2.0 ** -9 * rng.integers(-1, 2, shape) for shape in ((E * m, 4), (E, N, 9)))
+    a[::3, :128] = 0
+    b[:, ::3, :128] = 0
+    As, Bs = np.ones((4, E * m), np.float32), np.ones((E, -(-N // 128), 4), np.float32)
+    for e, (row, column) in enumerate(LARGE):
+        As[0, e * m:(e + 1) * m], Bs[e, :, 0] = row, column
+    As[0, 7], As[3, 7] = 1.0, 2.0 ** 100  # and rows without one, or with one only
+    Bs[1, 1, 0], Bs[2, 0, 3] = 0.0, 2.0 ** 40
+    args = (ref.to_e4m3(a), As, ref.to_e4m3(b), Bs, ops.offsets_of([m] * E))
+    C, S, G = ref.fp8_product(*args)
+    assert np.abs(C).max() < 2.0 ** 127.9
+    err = ref.fp8_product_error(S, G, K)
+    got = gg.grouped_gemm_fp8_block(*_dev(args), bm=bm)
+    ops.check_f32(ops.host(got), C, err, "fp32")
+    ops.check_bf16(ops.host(gg.grouped_gemm_fp8_block(*_dev(args), bm=bm, out_dtype=torch.bfloat16)), C, err, "bf16")
+    # where no block sum but the ordinary ones' counts, the results are theirs to the last bit (whole
+    # numbers below 2^24, which fp32 adds exactly; the far scales of the last block give others)
+    args[1][0], args[3][:, :, 0] = 1.0, 1.0
+    plain = ref.fp8_product(*args, bounds=False)[0]
+    zero = (np.arange(E * m) % 3 == 0)[:, None] | (np.arange(N) % 3 == 0)
+    zero &= np.abs(plain) < 2 ** 24
+    assert zero.sum() > E * m * N / 3 and (ops.host(got)[zero] == plain[zero]).all()
+
+
+@pytest.mark.parametrize("K", [128, 384])
+def test_scales_whose_product_is_below_fp32(gg, K):
+    # a product of scales below 2^-126 is off by 2^-150 at most, a block's sum is less than
+    # 448 * 448 * 128 < 2^25: that much a block, and the usual besides
+    rng = np.random.default_rng(K)
+    E, N, m = len(SMALL), 264, 21
+    a, b = (rng.integers(14, 29, shape) * 16.0 for shape in ((E * m, K), (E, N, K)))
+    slices = -(-K // 128)
+    As = np.repeat(np.array([p for p, _ in SMALL], dtype=np.float32), m)[None].repeat(slices, 0)
+    Bs = np.array([p for _, p in SMALL], dtype=np.float32)[:, None, None] * np.ones((E, -(-N // 128), slices), np.float32)
+    args = (ref.to_e4m3(a), As, ref.to_e4m3(b), Bs, ops.offsets_of([m] * E))
+    C, S, G = ref.fp8_product(*args)
+    got = gg.grouped_gemm_fp8_block(*_dev(args))
+    ops.check_f32(ops.host(got), C, ref.fp8_product_error(S, G, K) + slices * 2.0 ** -125, "fp32")
+
+
+def test_infinite_scales_are_the_formulas(gg):
+    rng = np.random.default_rng(18)
+    args = list(_exact_operands(rng, [20, 30], 256, 264))
+    args[1][0, 3], args[1][1, 30], args[3][0, 1, 0] = np.inf, -np.inf, np.inf
+    with np.errstate(invalid="ignore"):
+        C = ref.fp8_product(*args, bounds=False)[0]
+    got = ops.host(gg.grouped_gemm_fp8_block(*_dev(args)))
+    assert np.isinf(C).any() and np.isnan(C).any() and same(got, C.astype(np.float32))
+
+
 def test_rows_past_the_last_group_are_never_used(gg):
     rng = np.random.default_rng(13)
     args = list(_exact_operands(rng, [5, 6], 144, 72, extra=20))
