@@ -520,10 +520,10 @@ gg_status_t gg_fp8_quantize_weights(const void *B, void *q, float *scales, int32
  *                Rows at or beyond off[E] are never used.
  *   Bq, b_scale  codes uint8 [E][N][K] and scales fp32 [E][ceil(N/128)][ceil(K/128)].
  *                The scales are any fp32 numbers, not only what the quantiser makes, and
- *                the product of a row's and the columns' may lie beyond fp32. (Rows that
- *                come out infinite or NaN are computed twice for that, the second time
- *                slowly.) Where it lies below fp32's normal numbers, what the block adds
- *                is off by up to 2^-125 besides.
+ *                the product of a row's and the columns' may lie beyond fp32 (those
+ *                rows are computed again, 50 to 150 times as slowly). Where it lies
+ *                below fp32's normal numbers, what the block adds is off by up to 2^-125
+ *                besides.
  *   C            fp32 [M_cap][N]. Rows at or beyond off[E] are not touched.
  * K is a multiple of 16 and at most GG_MAX_K, N a multiple of 8 and at most
  * GG_MAX_N; all pointers but group_offsets (4) are 16-byte aligned. Offsets, E,

@@ -678,41 +678,72 @@ struct ScaleParts {
   }
 };
 
-// 8 bits: row block mi anew, from memory, with the scales' powers of two applied apart
-// from their product: a block's sum is a multiple of 2^-18 and at most 2^25, so times
-// 2^-100 .. 2^100 it is exact. What is left of the power beyond that goes to the product
-// of the rests, up to 2^+-120, where the result is infinite or 0 anyway.
+// 8 bits: the scale of a wave's columns (they lie in one block of 128) in each slice, to
+// be read through the scalar cache. (A wave past the last column takes the last block's.)
+template <class C>
+__device__ __forceinline__ cst_f32 *ring_columns(const RingTile &t, int wn0) {
+  const int band = C::BN > 128 ? min(wn0, t.ncols - 1) / 128 : 0;
+  return (cst_f32 *)(t.Bs + (uint64_t)band * t.bs_step);
+}
+
+// Sum of 16 products of E4M3 codes.
+__device__ __forceinline__ float dot16_fp8(u32x4 a, u32x4 b, float sum) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    static_for<2>([&](auto high) {
+      const f32x2 x = __builtin_amdgcn_cvt_pk_f32_fp8((int)a[i], decltype(high)::value),
+                  y = __builtin_amdgcn_cvt_pk_f32_fp8((int)b[i], decltype(high)::value);
+      sum = __builtin_fmaf(x.y, y.y, __builtin_fmaf(x.x, y.x, sum));
+    });
+  return sum;
+}
+
+// 8 bits: row block mi, where a row of it came out infinite or NaN. If that may be since
+// the product of its scale and the columns' passed fp32, the block is computed anew from
+// memory, an output at a time, with the scales' powers of two applied apart from their
+// product: a block's sum is a multiple of 2^-18 and at most 2^25, so times 2^-100 ..
+// 2^100 it is exact. What is left of the power beyond that goes to the product of the
+// rests, up to 2^+-120, where the result is infinite or 0 anyway. (Rare, so it is kept
+// small; a matrix instruction would make it ten times as fast, and its code too large.)
 template <class C>
 __device__ __forceinline__ void ring_block_apart(f32x4 (&acc)[C::NI][C::MI], int mi, const RingTile &t,
-                                                 cst_f32 *columns, int wm0, int wn0, int lane) {
-  const int g = lane / 16, s = lane % 16, KT = ring_slices(t);
-  auto read = [&](const char *base, int rows, int r, int k) {
-    const buf_rsrc b = ring_rows(base, rows, t, k);
-    auto piece = [&](uint32_t at) {
-      return ld_buf16(b, at < t.pitch - (uint32_t)k * kRowBytes ? (uint32_t)r * t.pitch + at : kOob, 0);
-    };
-    return __builtin_bit_cast(ring_i32x8, __builtin_shufflevector(piece(16u * g), piece(64u + 16u * g),
-                                                                  0, 1, 2, 3, 4, 5, 6, 7));
+                                                 int wm0, int wn0, int lane) {
+  cst_f32 *const columns = ring_columns<C>(t, wn0);
+  const int g = lane / 16, row = wm0 + mi * 16 + lane % 16, KT = ring_slices(t);
+  auto row_scale = [&](int k) {
+    const buf_rsrc rs = make_buf(t.As + (uint64_t)k * t.as_step, 4u * (uint32_t)t.rows);
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * row, 0, 0));
   };
-#pragma unroll
-  for (int ni = 0; ni < C::NI; ++ni) acc[ni][mi] = f32x4{0.f, 0.f, 0.f, 0.f};
+  bool passed = false;
 #pragma unroll 1
   for (int k = 0; k < KT; ++k) {
-    const int r = wm0 + mi * 16 + s;
-    const buf_rsrc rs = make_buf(t.As + (uint64_t)k * t.as_step, 4u * (uint32_t)t.rows);
-    const ScaleParts row(__builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * r, 0, 0))),
-        column(columns[k]);
-    const int power = row.power + column.power, at_once = min(max(power, -100), 100);
-    const float first = __builtin_ldexpf(1.0f, at_once),
-                rest = __builtin_ldexpf(row.rest * column.rest, min(max(power - at_once, -120), 120));
-    const ring_i32x8 y = read(t.A, t.rows, r, k);
-#pragma unroll
-    for (int ni = 0; ni < C::NI; ++ni) {
-      const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-          read(t.B, t.ncols, wn0 + ni * 16 + s, k), y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[ni][mi][j] = __builtin_fmaf(d[j] * first, rest, acc[ni][mi][j]);
+    const float s = row_scale(k), c = columns[k];
+    passed |= fabsf(s * c) == INFINITY && fabsf(s) < INFINITY && fabsf(c) < INFINITY;
+  }
+  if (__ballot(passed) == 0) return;
+#pragma unroll 1
+  for (int q = 0; q < 4 * C::NI; ++q) {
+    const int col = wn0 + q / 4 * 16 + 4 * g + q % 4;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < KT; ++k) {
+      const ScaleParts r(row_scale(k)), c(columns[k]);
+      const int power = r.power + c.power, at_once = min(max(power, -100), 100);
+      const buf_rsrc ra = ring_rows(t.A, t.rows, t, k), rb = ring_rows(t.B, t.ncols, t, k);
+      float d = 0.0f;
+#pragma unroll 1
+      for (uint32_t at = 0; at < kRowBytes; at += 16) {
+        const bool in = at < t.pitch - (uint32_t)k * kRowBytes;
+        d = dot16_fp8(ld_buf16(ra, in ? (uint32_t)row * t.pitch + at : kOob, 0),
+                      ld_buf16(rb, in ? (uint32_t)col * t.pitch + at : kOob, 0), d);
+      }
+      sum = __builtin_fmaf(__builtin_ldexpf(d, at_once),
+                           __builtin_ldexpf(r.rest * c.rest, min(max(power - at_once, -120), 120)), sum);
     }
+#pragma unroll
+    for (int ni = 0; ni < C::NI; ++ni)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[ni][mi][j] = q == 4 * ni + j ? sum : acc[ni][mi][j];
   }
 }
 
@@ -761,10 +792,16 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[C::NI][C::MI], const Ring
 // was one that stores behind the prologue, STORES times at least a wave, that many
 // may stay in flight at the first slice (64 x 256 rows, K = 1024, N = 2688 with
 // SwiGLU 70.1 -> 68.7 us).
-template <class C, int STORES = 0, class Epi, class Next>
+//
+// again() gives t anew (8 bits): kept over the loop for what is rare after it, its parts
+// would take scalars that the loop does not have.
+struct NoTile {
+  __device__ __forceinline__ RingTile operator()() const { return RingTile{}; }
+};
+template <class C, int STORES = 0, class Epi, class Next, class Again = NoTile>
 __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, int tid,
                                               int n_blocks, Epi &&epi, Next &&next,
-                                              bool after = false) {
+                                              bool after = false, Again &&again = NoTile{}) {
   const int wave = scalar(tid / kWave);
   const int lane = tid % kWave;
   const int wm0 = (wave / C::WN) * C::WTM, wn0 = (wave % C::WN) * C::WTN;
@@ -775,14 +812,10 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
     for (int mi = 0; mi < C::MI; ++mi) acc[ni][mi] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int KT = ring_slices(t);
   int cur = 0, nxt = C::S - 1;  // stages of slice k and of slice k + S - 1
-  // 8 bits: the scale of this wave's columns (they lie in one block of 128) in each
-  // slice, through the scalar cache
   cst_f32 *columns = nullptr;
   float column = 0.0f;
   if constexpr (C::FP8) {
-    // (a wave past the last column takes the last block's)
-    const int band = C::BN > 128 ? min(wn0, t.ncols - 1) / 128 : 0;
-    columns = (cst_f32 *)(t.Bs + (uint64_t)band * t.bs_step);
+    columns = ring_columns<C>(t, wn0);
     column = columns[0];
   }
   for (int k = 0; k < KT - 1; ++k) {
@@ -804,11 +837,11 @@ __device__ __forceinline__ void run_ring_tile(const RingTile &t, lds_u8 *lds, in
   wg_barrier();
   epi.begin();
   // 8 bits: where the product of a row's and the columns' scale passed fp32, all that this
-  // wave has of the row is infinite or (for sums of 0) NaN, one value as good as another.
+  // wave has of the row is infinite or (for sums of 0) NaN, so one value a row is looked at.
   auto store = [&](int mi) {
     if constexpr (C::FP8)
-      if (__ballot(!(fabsf(acc[0][mi].x) < INFINITY)) != 0)
-        ring_block_apart<C>(acc, mi, t, columns, wm0, wn0, lane);
+      if (__builtin_expect(__ballot(!(fabsf(acc[0][mi].x) < INFINITY)) != 0, 0))
+        ring_block_apart<C>(acc, mi, again(), wm0, wn0, lane);
     epi.block(acc, mi);
   };
   // Row block mi is final. The empty asm keeps its products ahead of the

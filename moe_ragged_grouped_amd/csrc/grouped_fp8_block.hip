@@ -194,8 +194,16 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_product_kernel(Fp8BlockParams
     const int wave = scalar(tid / kWave);
     ProductEpi<C, O> epi{p.C, p.N, tl.row0, tl.col0, t.rows, t.ncols, (wave / C::WN) * C::WTM,
                          (wave % C::WN) * C::WTN, tid % kWave};
+    int expert = tl.expert;
+    asm volatile("" : "+v"(expert));  // (scalars are short)
+    auto again = [&] {
+      Tile same = tl;
+      same.expert = scalar(expert);
+      return make(same);
+    };
     // its stores: 8 row blocks of one, two or four
-    run_ring_tile<C, 8 * (O == MOut::F32 ? 4 : O == MOut::BF16 ? 2 : 1)>(t, lds, tid, 0, epi, next, after);
+    run_ring_tile<C, 8 * (O == MOut::F32 ? 4 : O == MOut::BF16 ? 2 : 1)>(t, lds, tid, 0, epi, next, after,
+                                                                         again);
     after = C::BM == 256 && C::BN == 256;
   };
   run_ring_tiles<kRowsFp8>(sched, grid, p.off, p.E, p.M_cap, p.N, p.bm_fixed, lds, make, run);
