@@ -584,8 +584,8 @@ gg_status_t gg_expert_sort(const void *experts, int32_t wide, const float *weigh
 /*
  * gg_expert_spread -- each token's row to the rows of its choices:
  * out[pos[t][j]] = X[t] for every pos[t][j] in [0, M_cap); other choices are
- * skipped, and rows that no choice names are not touched. Two choices that name the
- * same row race.
+ * skipped, and rows that no choice names are not touched. A row that two choices name
+ * is undefined, and so are its scales: parts of both tokens', not one of the two.
  *   X, out   [T] and [M_cap] rows of row_bytes bytes, a multiple of 16; 16-byte
  *            aligned. Any type: bytes are moved.
  *   scales, out_scales  block scales that go with the rows, [slices][T] and
@@ -618,7 +618,7 @@ gg_status_t gg_expert_combine(const void *Y, int32_t y_fp32, const int32_t *pos,
  *   dY[pos[t][j]][n] = weights[t][j] * dO[t][n]
  *   dweights[t][j]   = sum_n dO[t][n] * Y[pos[t][j]][n]     (0 where pos is not in [0, M_cap))
  * dO, Y and dY are all fp32 (fp32 != 0) or all bf16. Rows of dY that no choice names
- * are not touched; two choices that name the same row race. Products and sums are
+ * are not touched; a row that two choices name is undefined (parts of both). Products and sums are
  * in fp32, dY is rounded once, dweights is fp32 [T][k] summed in a fixed order.
  * N is a multiple of 8, N <= GG_MAX_N, T < 2^24.
  */

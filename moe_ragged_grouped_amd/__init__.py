@@ -931,9 +931,9 @@ def expert_spread(X, pos, scale=None, M_cap=None, out=None, out_scale=None, stre
     X: [T, K] of any type whose rows are a multiple of 16 bytes (bf16, fp32, fp8
     or 4-bit codes); pos: int32 [T, k] (expert_sort), entries outside [0, M_cap) are
     skipped; out: optional [M_cap, K] like X (default: M_cap = T*k rows, or M_cap
-    where it is given). Rows that no choice names are left as they were; of two
-    choices that name one row either may land. scale: the
-    block scales of X, which go with their rows: fp32 [ceil(K/128), T]
+    where it is given). Rows that no choice names are left as they were; a row that
+    two choices name (expert_sort makes none) is undefined, parts of both tokens'
+    codes and scales. scale: the block scales of X, which go with their rows: fp32 [ceil(K/128), T]
     (fp8_quantize, rms_norm_fp8) or uint8 [ceil(K/256), T, 8] (mx4_quantize); then
     (out, out_scale) is returned, out_scale [.., M_cap(, 8)]. The gradient with
     respect to X is expert_combine(d_out, pos).
@@ -1006,7 +1006,8 @@ def expert_combine_grad(dO, Y, pos, weights, out=None, out_weights=None, stream=
 
     dO: [T, N] and Y: [M_cap, N], both bf16 or both fp32; pos: int32 [T, k];
     weights: fp32 [T, k]. dY[pos[t, j]] = weights[t, j] * dO[t], like Y (``out``;
-    rows that no choice names are left as they were); dweights[t, j] = <dO[t],
+    rows that no choice names are left as they were, a row that two choices name is
+    undefined, parts of both); dweights[t, j] = <dO[t],
     Y[pos[t, j]]>, fp32 [T, k] (``out_weights``), 0 where a choice has no row.
     Everything in fp32, dY rounded once, sums in a fixed order.
     """
