@@ -637,8 +637,9 @@ gg_status_t gg_expert_combine_grad(const void *dO, const void *Y, int32_t fp32, 
  *                X or residual itself, from its start.
  *   norm         bf16 [T][K]: y rounded once; or NULL.
  * K is a multiple of 16, at most 16384; T in [0, 2^24 - 2]; eps >= 0; everything
- * 16-byte aligned. A row that holds an infinity or a NaN, or zeros alone with eps =
- * 0, has NaN in the blocks where y is not finite.
+ * 16-byte aligned. Rows and weights may lie anywhere in bf16's range: what leaves fp32
+ * on the way does no harm where y does not. A row that holds an infinity or a NaN, or
+ * zeros alone with eps = 0, has NaN in the blocks where y is not finite.
  */
 gg_status_t gg_rms_norm_fp8(const void *X, const void *residual, const void *weight, void *q,
                             float *scales, void *sum, void *norm, int64_t T, int32_t K, float eps,
