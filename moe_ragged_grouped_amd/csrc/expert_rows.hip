@@ -367,7 +367,7 @@ struct CombineParams {
   float *dw;
   long long units;
   int T, k, N, M, segments;
-  bool stream;
+  bool stream;  // the combined rows
 };
 
 template <class Y, class O>
@@ -444,7 +444,10 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(CombineParams
           dot[j] = __builtin_fmaf(d.get(i), y[j].get(i), dot[j]);
           o[i] = w[j] * d.get(i);
         }
-        store8((Y *)p.out + (size_t)at[j] * p.N + n, o, p.stream);
+        // (not as streaming data: the gradients of the products read it at once. 64 MB 34.6 us
+        // so, 27.1 streamed, and with a reader behind 49.1 and 52.6; 192 MB 95.3 and 93.9, 143
+        // and 151; into one buffer again and again 128 MB 53.8 and 64.0, 87 and 100)
+        store8((Y *)p.out + (size_t)at[j] * p.N + n, o, false);
       }
     }
 #pragma unroll
@@ -611,8 +614,7 @@ extern "C" gg_status_t gg_expert_combine_grad(const void *dO, const void *Y, int
              w = span(weights, T, k, 4), dy = span(dY, M_cap, N, b), dw = span(dweights, T, k, 4);
   if (!apart(dy, o, y, at, w, dw) || !apart(dw, o, y, at, w)) return GG_ERR_INVALID_VALUE;
   if (T == 0) return GG_OK;
-  const CombineParams p{Y, dO, pos, weights, dY, dweights, T, (int)T, k, N, (int)M_cap, 1,
-                        streams(M_cap * N * b)};
+  const CombineParams p{Y, dO, pos, weights, dY, dweights, T, (int)T, k, N, (int)M_cap, 1, false};
   return launch(fp32 ? combine_grad_kernel<float> : combine_grad_kernel<uint16_t>, dim3((unsigned)T),
                 kRowThreads, 0, stream, p);
 }
