@@ -39,12 +39,19 @@ inline gg_status_t launch(void (*kernel)(P...), dim3 grid, int threads, int lds,
   return GG_ERR_LAUNCH;
 }
 
-// Outputs of this many bytes are stored as streaming data: half of what the L2s
-// hold (32 MB), each of which keeps what its own XCD wrote and the next call may
-// read on another. Measured (us, without / with): 2048 x 8 rows of 6144 combined
-// (25 MB) 46.9 / 41.7, the gradient 90.2 / 87.8; the norm of 16384 x 6144 128.1 /
-// 123.2, its gradient (8191) 89.2 / 86.8; weights [64][1024][2688] to 8 bits 92.1 /
-// 84.6.
+// Outputs of this many bytes written are stored as streaming data: half of what the L2s
+// hold (32 MB), each of which keeps what its own XCD wrote and the next call may read
+// on another. Measured (us, plain / streamed, three outputs in turn; then with a reader
+// behind, bf16 rows to 8 bits):
+//   combine             16 MB 14.6 / 14.4, 21.6 / 21.9   32 MB 35.7 / 31.6, 44.6 / 43.6
+//                      128 MB  132 / 122,   168 / 163
+//   norm with its sum   24 MB 14.8 / 14.4, 22.0 / 21.7   96 MB 50.3 / 46.7, 66.8 / 66.0
+//   its gradient        16 MB 21.6 / 21.4, 28.5 / 28.7  128 MB 85.0 / 83.4,  122 / 122
+//   weights to 8 bits  176 MB 92.1 / 84.6
+// From 2 to 6 MB the two differ by 4% either way; at 8 MB the norm without its sum gains
+// (10.2 / 9.5, 17.4 / 17.2), the others do not. An output that is written again and again
+// to one place loses with the reader (combine 64 MB 81.7 / 84.6, norm gradient 65.1 /
+// 68.4), as does the combine's gradient always, which does not ask.
 inline bool streams(long long bytes) { return bytes >= (16LL << 20); }
 
 inline bool valid_bm(int bm) {

@@ -438,7 +438,7 @@ extern "C" gg_status_t gg_rms_norm_fp8(const void *X, const void *residual, cons
   const NormParams p{static_cast<const u32x4 *>(X), static_cast<const u32x4 *>(residual),
                      static_cast<const u32x4 *>(weight), static_cast<u32x2 *>(q), scales,
                      static_cast<u32x4 *>(sum), static_cast<u32x4 *>(norm), (int)T, K, eps,
-                     streams(T * K * 2)};
+                     streams(T * K * (1 + 2 * (sum != nullptr) + 2 * (norm != nullptr)))};
   const int v = (K + kNormPiece - 1) / kNormPiece;
   void (*const kernel)(NormParams) = v == 1   ? norm_kernel<1>
                                      : v == 2 ? norm_kernel<2>
