@@ -405,12 +405,6 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineParams p) {
 
 // A workgroup a token: the gradient of its rows, and the scalar products with
 // them that are the gradient of its weights.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d, kWave);
-  return v;
-}
-
 template <class Y>
 __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(CombineParams p) {
   __shared__ float sums[kRowWaves][kJ];
@@ -452,7 +446,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(CombineParams
     }
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
-      const float s = wave_sum(dot[j]);
+      const float s = sum_of_wave(dot[j]);
       if (tid % kWave == 0) sums[tid / kWave][j] = s;
     }
     __syncthreads();

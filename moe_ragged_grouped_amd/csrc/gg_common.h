@@ -98,6 +98,14 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
 }
 
+// The sum over a wave, in every lane.
+template <class T>
+__device__ __forceinline__ T sum_of_wave(T v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d, kWave);
+  return v;
+}
+
 // A store of a lane's piece of a row, as streaming data (nt) or not. (The empty
 // asm keeps the compiler from making one plain store of the two.)
 template <class T>

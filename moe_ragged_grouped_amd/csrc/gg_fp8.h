@@ -32,7 +32,8 @@ __device__ __forceinline__ float fp8_scale(float m) {
 }
 
 // Two values over their scale -> two codes in half HIGH of a dword
-// (v_cvt_pk_fp8_f32: nearest, ties to even; nothing here is above 448).
+// (v_cvt_pk_fp8_f32: nearest, ties to even. Nothing here is above 448, but for the
+// norm's values, whose two roundings may pass it by a last bit and which go to 448.)
 template <bool HIGH>
 __device__ __forceinline__ uint32_t fp8_pair(uint32_t old, float a, float b) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HIGH);

@@ -47,8 +47,7 @@ typedef __attribute__((address_space(1))) u32x2 gbl_u32x2;
 
 __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// What a slice holds beside its 128-byte rows (the values of the products are
-// template arguments below; false and true name the first two).
+// What a slice holds beside its 128-byte rows.
 constexpr int kRowsBf16 = 0;  // nothing
 constexpr int kRowsMx4 = 1;   // 8 scale bytes a row, one for 32 values
 constexpr int kRowsFp8 = 2;   // one fp32 scale a row of A (that of 128 columns is a scalar)

@@ -168,7 +168,7 @@ __global__ __launch_bounds__(kThreads, 1) void dgrad_kernel(DgradParams p) {
                        (wave % C::WN) * C::WTN, tid % kWave, {}};
     run_ring_tile<C>(t, lds, tid, 0, epi, next);
   };
-  run_ring_tiles<false>(sched, grid, p.off, p.E, p.M_cap, p.K, p.bm_fixed, lds, make, run);
+  run_ring_tiles<kRowsBf16>(sched, grid, p.off, p.E, p.M_cap, p.K, p.bm_fixed, lds, make, run);
 }
 
 template <DOut O>

@@ -295,7 +295,7 @@ __global__ __launch_bounds__(kThreads, 1) void mx4_product_kernel(Mx4Params p) {
                          (wave % C::WN) * C::WTN, tid % kWave};
     run_ring_tile<C>(t, lds, tid, p.K / kBlockK, epi, next);
   };
-  run_ring_tiles<true>(sched, grid, p.off, p.E, p.M_cap, p.N, p.bm_fixed, lds, make, run);
+  run_ring_tiles<kRowsMx4>(sched, grid, p.off, p.E, p.M_cap, p.N, p.bm_fixed, lds, make, run);
 }
 
 template <MOut O>

@@ -26,13 +26,6 @@ constexpr int kNormWaves = 4, kNormRows = 2;
 constexpr int kNormThreads = kNormWaves * kNormRows * kWave;
 constexpr int kNormPiece = kNormWaves * kWave * 8;  // values of a row at one time
 
-template <class T>
-__device__ __forceinline__ T sum_of_wave(T v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d, kWave);
-  return v;
-}
-
 // e with 2^-2 <= ms 2^-2e < 1, so that 1 / sqrt(ms) is 2^-e times a number in (1, 2]
 // (0 where ms is 0, infinite or NaN).
 __device__ __forceinline__ int root_exponent(double ms) { return (__builtin_amdgcn_frexp_exp(ms) + 1) >> 1; }
