@@ -3,7 +3,7 @@
 // token's rows, and its gradient.
 //
 // All of them move bytes. 2048 tokens of 8 choices, rows of 6144 bf16: spread 34 us
-// for 226 MB (6.6 TB/s), combine 42 for 227 (5.4), gradient 87 for 428 (4.9, half
+// for 226 MB (6.6 TB/s), combine 41 for 227 (5.5), gradient 90 for 428 (4.8, half
 // of it writes). The sort moves little and waits: 64 x 8 choices 4 us, 16384 x 8 in
 // two launches 8, each launch's start and its round trips to memory.
 

@@ -6,9 +6,9 @@
 // z is rounded before it is normalised, as the layers behind the residual see
 // it. Everything else is held in fp32 or more and rounded once.
 //
-// Both move bytes, in one pass over the rows: 16384 x 6144 with a residual 123 us
-// for 708 MB (5.8 TB/s); the gradient of 8191 x 6144 77 us for 403 MB and 5 for the
-// shares of dg. 16 x 6144: 5 us, a launch and two round trips.
+// Both move bytes, in one pass over the rows: 16384 x 6144 with a residual 124.5 us
+// for 708 MB (5.7 TB/s); the gradient of 8191 x 6144 77 us for 403 MB and 5 for the
+// shares of dg. 16 x 6144: 5.7 us, a launch and two round trips.
 
 #include <float.h>
 
