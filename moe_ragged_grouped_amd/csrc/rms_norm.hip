@@ -289,7 +289,8 @@ void norm_grad_kernel(NormGradParams p) {
         part = __builtin_fmaf(u[i][j], zf[i][j], part);
       }
       if (!(fabsf(part) >= kGradLeast && fabsf(part) <= kGradTop && least >= FLT_MIN)) {
-        bool far = !(fabsf(part) <= kGradTop) || (fabsf(part) < kGradLeast && !empty(z[i]) && !empty(d[i]));
+        bool far = !(fabsf(part) <= kGradTop) ||
+                   (fabsf(part) < kGradLeast && !empty(z[i]) && !empty(d[i]) && !empty(g[i]));
 #pragma unroll
         for (int j = 0; j < 8; ++j) far |= __builtin_amdgcn_classf(u[i][j], kSubnormal);
         if (far) part = NAN;  // (zeros are no reason)

@@ -274,3 +274,42 @@ def test_norm_of_zeros_without_eps_is_nan(gg):
     # eps alone decides: r = 0, and everything finite is 0
     q, s, y = gg.rms_norm_fp8(x, torch.full((272,), 2.0 ** 100, dtype=torch.bfloat16, device=DEV), eps=float("inf"), with_norm=True)
     assert (y == 0).all() and (s == np.float32(2.0 ** -100 / 448)).all()
+
+
+@pytest.mark.parametrize("K", [272, 6144, 16384])
+def test_gradient_with_weights_and_gradients_of_zero(gg, K):
+    # weights of 0 (as a layer begins with) in all columns and in runs of them, gradients of 0 in rows and runs
+    rng = np.random.default_rng(K + 2)
+    z, _, g = _inputs(rng, 6, K)
+    dy = ops.bits(rng, 6, K, scale=0.02)
+    dy[1], dy[2, 8:40], z[3, 64:96] = 0, 0, 0
+    for weight in (np.zeros_like(g), np.where(np.arange(K) // 16 % 3 == 0, 0, g).astype(g.dtype)):
+        Z, W, D = (oracle._bf16_to_f64(a) for a in (z, weight, dy))
+        want, dg, err, mags = ref.norm_grad(D, Z, W, None, 1e-6)
+        dz, dw = gg.rms_norm_grad(ops.to_dev(dy), ops.to_dev(z), ops.to_dev(weight))
+        ops.check_bf16(ops.host(dz), want, err, "dz")
+        ops.check_f32(ops.host(dw), dg, ref.NORM_DG_REL * mags, "dg")
+
+
+def test_far_rows_among_others_in_a_workgroup(gg):
+    # rows of one workgroup in turn far and not, more rows than workgroups: each row's result is its own
+    rng = np.random.default_rng(4)
+    T, K = 5000, 272
+    z, _, g = _inputs(rng, T, K)
+    dy = ops.bits(rng, T, K, scale=0.02)
+    Z, D = oracle._bf16_to_f64(z), oracle._bf16_to_f64(dy)
+    far = rng.integers(0, 3, T)
+    Z *= np.array([1.0, 2.0 ** 60, 2.0 ** -60])[far][:, None]
+    D *= np.array([1.0, 2.0 ** 60, 2.0 ** -60])[far][:, None]
+    z, dy = (wl.f32_to_bf16_bits(a.astype(np.float32)) for a in (Z, D))
+    dz, _ = gg.rms_norm_grad(ops.to_dev(dy), ops.to_dev(z), ops.to_dev(g), eps=0.0)
+    q, s, y = gg.rms_norm_fp8(ops.to_dev(z), ops.to_dev(g), eps=0.0, with_norm=True)
+    W = oracle._bf16_to_f64(g)
+    want, _, err, _ = ref.norm_grad(D, Z, W, None, 0.0)
+    ops.check_bf16(ops.host(dz), want, err, "dz")
+    _, want = ref.norm(Z, None, W, 0.0)
+    check_fp8(q.view(torch.uint8).cpu().numpy(), ops.host(s), want, ref.NORM_REL)
+    ops.check_bf16(ops.host(y), want, ref.NORM_REL * np.abs(want), "norm")
+    for _ in range(3):
+        again = gg.rms_norm_grad(ops.to_dev(dy), ops.to_dev(z), ops.to_dev(g), eps=0.0)[0]
+        assert torch.equal(again, dz)
