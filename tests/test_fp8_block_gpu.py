@@ -289,6 +289,29 @@ def test_scales_whose_product_is_beyond_fp32(gg, N, bm):
     assert zero.sum() > E * m * N / 3 and (ops.host(got)[zero] == plain[zero]).all()
 
 
+@pytest.mark.parametrize("sizes", [[256] * 100 + [1], [700] * 24 + [100] * 60 + [30] * 50, [64] * 300])
+def test_repeated_blocks_in_rounds_of_tiles(gg, sizes):
+    # blocks that are computed again in some tiles of several rounds, between a tile's last products and the
+    # next one's first slices: a first block of zeros at scales whose product passes fp32, then whole numbers
+    rng = np.random.default_rng(len(sizes))
+    N, M, E = 2056, sum(sizes), len(sizes)
+    for K in (144, 400, 1024):
+        Aq, As, Bq, Bs, off = _exact_operands(rng, sizes, K, N)
+        Aq[:, :128] = 0
+        for far in (False, True):
+            As[0], Bs[:, :, 0] = 1.0, 1.0
+            if far:
+                As[0, rng.integers(0, 40, M) == 0] = 2.0 ** 100
+                Bs[rng.integers(0, 3, E) == 0, :, 0] = -2.0 ** 100
+            args = _dev((Aq, As, Bq, Bs, off))
+            got = [gg.grouped_gemm_fp8_block(*args), gg.grouped_gemm_fp8_block(*args, out_dtype=torch.bfloat16),
+                   gg.grouped_gemm_fp8_block_swiglu(*args)]
+            if not far:
+                want = got
+            for a, b in zip(got, want):
+                assert torch.equal(a, b), (K, far)
+
+
 @pytest.mark.parametrize("K", [128, 384])
 def test_scales_whose_product_is_below_fp32(gg, K):
     # a product of scales below 2^-126 is off by 2^-150 at most, a block's sum is less than
