@@ -707,7 +707,8 @@ __device__ __forceinline__ float dot16_fp8(u32x4 a, u32x4 b, float sum) {
 // product: a block's sum is a multiple of 2^-18 and at most 2^25, so times 2^-100 ..
 // 2^100 it is exact. What is left of the power beyond that goes to the product of the
 // rests, up to 2^+-120, where the result is infinite or 0 anyway. (Rare, so it is kept
-// small; a matrix instruction would make it ten times as fast, and its code too large.)
+// plain: with every row so, 64 x 256 rows, K = 1024, N = 2688 take 7.5 ms. Matrix
+// instructions stay in the slices' loops, which let no load be waited for.)
 template <class C>
 __device__ __forceinline__ void ring_block_apart(f32x4 (&acc)[C::NI][C::MI], int mi, const RingTile &t,
                                                  int wm0, int wn0, int lane) {
